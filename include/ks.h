@@ -295,6 +295,89 @@ ks_status ks_chain_noalloc(const void *X, const void *const *factors,
 ks_status ks_butterfly_factorize(const void *A, int log2n, void *const *factors,
                                  int dtype, void *stream);
 
+/* Low-rank adapters of many requests beside one shared KS projection: for
+ * every row n, with s = ids[n],
+ *     Y[n] = act(X[n] K^T + bias + scales[s] * (X[n] A[s]^T) B[s]^T).
+ * A is n_adapters x rank x (a*c*d), B is n_adapters x (a*b*d) x rank, both
+ * DEVICE arrays of the storage dtype, contiguous; scales is a DEVICE array of
+ * n_adapters floats, or NULL for ones; ids a DEVICE array of `batch` int32, or
+ * NULL when every row takes adapter 0.  A row with a negative id takes no
+ * adapter (its Y is that of ks_matmul_ep).  A row whose id is n_adapters or
+ * more takes none either, and the next ks_sync_status reports
+ * KS_ERR_INVALID_ARG: no such id is ever used as an index.  Any order of the ids is
+ * allowed; rows of one adapter next to each other run fastest, since a tile of
+ * rows passes once over the weights of each adapter that it holds.
+ * X, values, bias, activation and dtype are as for ks_matmul_ep (KS_TF32: the
+ * KS product uses TF32 as there, the adapters' products are fp32).  Y must not
+ * overlap any input.  1 <= n_adapters <= 65535, 1 <= rank <= 1024, batch <=
+ * 2^30.  H = scales[s] * X A[s]^T lives in a stream-ordered workspace from the
+ * library's pool (KS_ERR_ALLOC if it cannot be had). */
+ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_t b, int64_t c, int64_t d,
+                            int64_t batch, void *Y, int dtype, const void *bias, int activation, const void *A,
+                            const void *B, const float *scales, const int32_t *ids, int64_t n_adapters,
+                            int64_t rank, void *stream);
+
+/* Gradients of ks_adapter_matmul without an activation, from dY:
+ *     G[n] = scales[s] dY[n] B[s],    H[n] = scales[s] X[n] A[s]^T,
+ *     dX[n] = dY[n] K + G[n] A[s],
+ *     dA[s] = sum over the rows n with ids[n] == s of G[n]^T X[n],
+ *     dB[s] = sum over the same rows of dY[n]^T H[n],
+ * written, not accumulated, in the layouts of X, A and B; an adapter without
+ * rows gets zeros.  Each of dX, dA, dB may be NULL: it is not computed (values
+ * may be NULL without dX, X without dA and dB).  The gradients of the values
+ * and of the bias are ks_matmul_dv's and ks_bias_grad's.  Sums are fp32 in an
+ * order that depends on the sizes and ids alone, so the results are
+ * deterministic; bf16 gradients are rounded once.  No output may overlap an
+ * input or another output.  batch == 0 writes zeros to dA and dB.  Limits, ids
+ * and workspace are as for ks_adapter_matmul. */
+ks_status ks_adapter_backward(const void *dY, const void *X, const void *values, int64_t a, int64_t b, int64_t c,
+                              int64_t d, int64_t batch, int dtype, const void *A, const void *B,
+                              const float *scales, const int32_t *ids, int64_t n_adapters, int64_t rank, void *dX,
+                              void *dA, void *dB, void *stream);
+
+/* One tensor of an AdamW step (all pointers DEVICE memory of n elements unless
+ * said otherwise). */
+typedef struct ks_adamw_tensor {
+    void *param;             /* fp32 or bf16, updated                                        */
+    const void *grad;        /* the parameters' dtype                                        */
+    void *exp_avg;           /* m: fp32, or e4m3 numbers with state_bits 8                   */
+    void *exp_avg_sq;        /* v: fp32, or sqrt(v) as e4m3 numbers with state_bits 8        */
+    float *master;           /* fp32 master of a bf16 parameter, or NULL                     */
+    float *exp_avg_scale;    /* state_bits 8: ceil(n / 256) scales of exp_avg, else ignored  */
+    float *exp_avg_sq_scale; /* the same of exp_avg_sq                                       */
+    int64_t n;
+} ks_adamw_tensor;
+
+/* Numbers of a step.  The three pointers are DEVICE scalars, each NULL when not
+ * used; they are read when the step runs, so that a captured step can be
+ * replayed with other values. */
+typedef struct ks_adamw_options {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;             /* number of this step, from 1                                */
+    const int64_t *step_ptr;  /* holds the number of this step (from 1) in place of `step`  */
+    const float *lr_ptr;      /* holds the learning rate in place of `lr`                   */
+    const float *grad_scale;  /* factor of the gradients (loss scaling, clipping)           */
+} ks_adamw_options;
+
+/* One AdamW step over n_tensors tensors (a HOST array) in one launch for up to
+ * 400 of them.  For each element, t the step's number and g = grad_scale * grad:
+ *     m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2,
+ *     p = p (1 - lr weight_decay) - lr m / (1 - beta1^t) / (sqrt(v) / sqrt(1 - beta2^t) + eps),
+ * in fp32; bf16 parameters are rounded to nearest once.  With a master, p is
+ * the master, and the parameter receives its rounding (the parameter itself is
+ * not read).  dtype is KS_F32 or KS_BF16 (of param and grad).  state_bits 32
+ * keeps m and v in fp32; 8 keeps m and sqrt(v) as e4m3 numbers times one scale
+ * for each 256 consecutive elements of a tensor (scale = largest magnitude /
+ * 448; a block with nothing above 2^-100 is held as zeros; a positive sqrt(v)
+ * is never held as zero).  An infinite gradient makes its block's 8-bit states
+ * NaN, a NaN one its own element's.  Tensors of zero elements are skipped.  A parameter or
+ * state that shares bytes with any other buffer of the step is
+ * KS_ERR_INVALID_ARG, as are masters for some tensors only, betas outside
+ * [0, 1), or a negative or non-finite lr, eps or weight_decay.  Allocates no
+ * device memory. */
+ks_status ks_adamw_step(const ks_adamw_tensor *tensors, int64_t n_tensors, int dtype, int state_bits,
+                        const ks_adamw_options *options, void *stream);
+
 /* The library's workspace memory (not part of the paper's operation; for
  * callers that budget device memory).  *allocations (if non-NULL) receives
  * the number of workspace allocations the library has made from its pools
@@ -336,7 +419,8 @@ const char *ks_status_string(int status);
 
 /* Synchronises `stream`, then reports (and clears) the device-side status
  * word of the current device: KS_ERR_TIMEOUT if a bounded wait inside a
- * kernel gave up since the last call, KS_ERR_CUDA if the stream itself
+ * kernel gave up since the last call, KS_ERR_INVALID_ARG if a row of an
+ * adapter call had an id of n_adapters or more, KS_ERR_CUDA if the stream itself
  * failed, KS_OK otherwise. */
 ks_status ks_sync_status(void *stream);
 

@@ -22,6 +22,7 @@ from ._lib import (KS_BF16, KS_F32, KS_TF32, KS_VARIANT_AUTO, KS_VARIANT_FMA,  #
 Pattern = Tuple[int, int, int, int]
 
 __all__ = ["matmul", "matmul_host", "matmul_dx", "matmul_dv", "bias_grad", "chain", "butterfly_factorize", "KSLinear",
+           "adapter_matmul", "adapter_backward", "KSAdapterLinear", "adamw_step", "AdamW",
            "plan", "sync_status", "workspace_info", "ks_dtype_of", "KsError", "VARIANTS"]
 
 
@@ -282,3 +283,7 @@ def sync_status(stream: Optional[torch.cuda.Stream] = None) -> None:
     """Synchronise and raise KsError if a kernel reported a device-side failure."""
     dev = torch.device("cuda", torch.cuda.current_device())
     _lib.check(_lib.load().ks_sync_status(_stream_ptr(stream, dev)))
+
+
+from .adapters import KSAdapterLinear, adapter_backward, adapter_matmul  # noqa: E402,F401
+from .optim import AdamW, adamw_step  # noqa: E402,F401

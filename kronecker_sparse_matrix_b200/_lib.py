@@ -34,6 +34,16 @@ class KsPattern(ctypes.Structure):
     _fields_ = [("a", _i64), ("b", _i64), ("c", _i64), ("d", _i64)]
 
 
+class KsAdamwTensor(ctypes.Structure):
+    _fields_ = [(name, _vp) for name in ("param", "grad", "exp_avg", "exp_avg_sq", "master", "exp_avg_scale",
+                                         "exp_avg_sq_scale")] + [("n", _i64)]
+
+
+class KsAdamwOptions(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay")]
+                + [("step", _i64), ("step_ptr", _vp), ("lr_ptr", _vp), ("grad_scale", _vp)])
+
+
 SIGNATURES = {
     "ks_matmul": (_int, [_vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _int, _vp]),
     "ks_matmul_variant": (_int, [_vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _int, _int, _vp]),
@@ -49,6 +59,11 @@ SIGNATURES = {
     "ks_chain_ex": (_int, [_vp, ctypes.POINTER(_vp), ctypes.POINTER(KsPattern), _int, _i64, _vp, _int, _int, _vp]),
     "ks_chain_noalloc": (_int, [_vp, ctypes.POINTER(_vp), ctypes.POINTER(KsPattern), _int, _i64, _vp, _int, _vp]),
     "ks_bias_grad": (_int, [_vp, _i64, _i64, _vp, _int, _vp]),
+    "ks_adapter_matmul": (_int, [_vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _int, _vp, _int, _vp, _vp, _vp, _vp,
+                                 _i64, _i64, _vp]),
+    "ks_adapter_backward": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _i64, _i64,
+                                   _vp, _vp, _vp, _vp]),
+    "ks_adamw_step": (_int, [_vp, _i64, _int, _int, ctypes.POINTER(KsAdamwOptions), _vp]),
     "ks_workspace_info": (_int, [ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
     "ks_fma_rate_probe": (_int, [_vp, _int, _i64, _vp]),
     "ks_last_error": (ctypes.c_char_p, []),

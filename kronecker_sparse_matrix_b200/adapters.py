@@ -1,0 +1,180 @@
+"""Low-rank adapters of many requests beside one shared KS projection:
+``adapter_matmul``, its gradients ``adapter_backward`` and the layer built on
+them, ``KSAdapterLinear``.  As in the rest of the package, this module only
+marshals torch tensors into the C ABI (ks_adapter_matmul, ks_adapter_backward).
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import KSLinear, Pattern, _act, _bias_ptr, _lib, _stream_ptr, bias_grad, ks_dtype_of, matmul_dv
+
+
+def _empty(shape, like: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """An uninitialised tensor whose memory belongs to the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+def _check_adapters(x: torch.Tensor, values: Optional[torch.Tensor], pattern: Pattern, A: torch.Tensor,
+                    B: torch.Tensor, ids: Optional[torch.Tensor], scales: Optional[torch.Tensor], width: int,
+                    name: str) -> Tuple[int, int, int, int, int, int]:
+    a, b, c, d = (int(v) for v in pattern)
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous() or x.shape[1] != width:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of shape (batch, {width})")
+    if A.dim() != 3 or A.shape[2] != a * c * d or A.shape[0] == 0 or A.shape[1] == 0:
+        raise ValueError(f"A must have shape (adapters, rank, {a * c * d})")
+    s, r = A.shape[0], A.shape[1]
+    if B.shape != (s, a * b * d, r):
+        raise ValueError(f"B must have shape ({s}, {a * b * d}, {r})")
+    for t in (A, B, values):
+        if t is not None and (t.dtype != x.dtype or t.device != x.device or not t.is_contiguous()):
+            raise ValueError(f"values, A and B must be contiguous, with {name}'s dtype and device")
+    if values is not None and values.numel() != a * b * c * d:
+        raise ValueError(f"values must have {a * b * c * d} elements")
+    if ids is not None and (ids.dtype != torch.int32 or ids.device != x.device or ids.shape != (x.shape[0],)
+                            or not ids.is_contiguous()):
+        raise ValueError("ids must be a contiguous int32 tensor with one entry per row, on the same device")
+    if scales is not None and (scales.dtype != torch.float32 or scales.device != x.device or scales.shape != (s,)
+                               or not scales.is_contiguous()):
+        raise ValueError("scales must be a contiguous float32 tensor with one entry per adapter, on the same device")
+    return a, b, c, d, s, r
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: torch.Tensor, B: torch.Tensor,
+                   ids: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, *,
+                   bias: Optional[torch.Tensor] = None, act: str = "none", out: Optional[torch.Tensor] = None,
+                   tf32: bool = False, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Y[n] = act(X[n] K^T + bias + scales[s] (X[n] A[s]^T) B[s]^T) with s = ids[n].
+
+    x: (batch, a*c*d); values, bias and act as for ``matmul``; A: (adapters,
+    rank, a*c*d); B: (adapters, a*b*d, rank), both of x's dtype; ids: int32, one
+    per row (a negative id: no adapter; None: every row takes adapter 0);
+    scales: float32, one per adapter (None: ones).  An id that is too large
+    takes no adapter, and the next ``sync_status`` raises.  Rows of one adapter
+    next to each other run fastest.  Asynchronous on ``stream``."""
+    fin = int(pattern[0]) * int(pattern[2]) * int(pattern[3])
+    a, b, c, d, s, r = _check_adapters(x, values, pattern, A, B, ids, scales, fin, "x")
+    dt = ks_dtype_of(x, tf32)
+    batch, fout = x.shape[0], a * b * d
+    if out is None:
+        out = _empty((batch, fout), x, stream)
+    elif not out.is_contiguous() or out.dtype != x.dtype or out.device != x.device or out.shape != (batch, fout):
+        raise ValueError(f"out must be a contiguous ({batch}, {fout}) tensor with x's dtype and device")
+    with torch.cuda.device(x.device):
+        st = _lib.load().ks_adapter_matmul(x.data_ptr(), values.data_ptr(), a, b, c, d, batch, out.data_ptr(), dt,
+                                           _bias_ptr(bias, x, fout), _act(act), A.data_ptr(), B.data_ptr(),
+                                           _ptr(scales), _ptr(ids), s, r, _stream_ptr(stream, x.device))
+    _lib.check(st)
+    return out
+
+
+def adapter_backward(dy: torch.Tensor, x: Optional[torch.Tensor], values: Optional[torch.Tensor], pattern: Pattern,
+                     A: torch.Tensor, B: torch.Tensor, ids: Optional[torch.Tensor] = None,
+                     scales: Optional[torch.Tensor] = None, *, need_dx: bool = True, need_da: bool = True,
+                     need_db: bool = True, tf32: bool = False, stream: Optional[torch.cuda.Stream] = None):
+    """Gradients (dX, dA, dB) of ``adapter_matmul`` without an activation from
+    dY (batch, a*b*d); None in the place of one that is not needed (values may
+    be None without dX, x without dA and dB).  An adapter without rows gets
+    zeros.  Deterministic; fp32 sums, bf16 gradients rounded once."""
+    fout = int(pattern[0]) * int(pattern[1]) * int(pattern[3])
+    a, b, c, d, s, r = _check_adapters(dy, values, pattern, A, B, ids, scales, fout, "dy")
+    batch, fin = dy.shape[0], a * c * d
+    if need_dx and values is None:
+        raise ValueError("dX needs the values")
+    if need_da or need_db:
+        if x is None or x.shape != (batch, fin) or x.dtype != dy.dtype or x.device != dy.device or \
+                not x.is_contiguous():
+            raise ValueError(f"x must be a contiguous ({batch}, {fin}) tensor with dy's dtype and device")
+    dx = _empty((batch, fin), dy, stream) if need_dx else None
+    da = _empty(A.shape, A, stream) if need_da else None
+    db = _empty(B.shape, B, stream) if need_db else None
+    with torch.cuda.device(dy.device):
+        st = _lib.load().ks_adapter_backward(dy.data_ptr(), _ptr(x), _ptr(values), a, b, c, d, batch,
+                                             ks_dtype_of(dy, tf32), A.data_ptr(), B.data_ptr(), _ptr(scales),
+                                             _ptr(ids), s, r, _ptr(dx), _ptr(da), _ptr(db),
+                                             _stream_ptr(stream, dy.device))
+    _lib.check(st)
+    return dx, da, db
+
+
+class _KSAdapterFn(torch.autograd.Function):
+    """y = x K^T + bias + the adapters' products; every gradient on the GPU."""
+
+    @staticmethod
+    def forward(ctx, x, values, bias, A, B, scales, ids, pattern):
+        values, A, B = values.contiguous(), A.contiguous(), B.contiguous()
+        ctx.pattern = pattern
+        ctx.save_for_backward(x, values, A, B, scales, ids)
+        return adapter_matmul(x, values, pattern, A, B, ids, scales, bias=bias)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, values, A, B, scales, ids = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dy = dy.contiguous()
+        dx = da = db = None
+        if need[0] or need[3] or need[4]:
+            dx, da, db = adapter_backward(dy, x, values, ctx.pattern, A, B, ids, scales, need_dx=need[0],
+                                          need_da=need[3], need_db=need[4])
+        dv = matmul_dv(dy, x, ctx.pattern) if need[1] else None
+        dbias = bias_grad(dy) if need[2] else None
+        return dx, dv, dbias, da, db, None, None, None
+
+
+class KSAdapterLinear(KSLinear):
+    """A KSLinear with low-rank adapters beside it: y = x K^T (+ bias) +
+    alpha/rank (x A[s]^T) B[s]^T, s the row's adapter.
+
+    A (n_adapters, rank, in_features) is drawn N(0, 1/in_features), B
+    (n_adapters, out_features, rank) starts at zero, so a fresh layer is its
+    KSLinear.  ``scales`` is a buffer of alpha/rank per adapter (alpha defaults
+    to rank).  ``freeze_base()`` leaves the adapters alone to be trained."""
+
+    def __init__(self, pattern: Pattern, n_adapters: int, rank: int, alpha: Optional[float] = None, bias: bool = False,
+                 dtype=torch.float32, device=None):
+        super().__init__(pattern, bias=bias, dtype=dtype, device=device)
+        if n_adapters < 1 or rank < 1:
+            raise ValueError("n_adapters and rank must be positive")
+        A = torch.randn(n_adapters, rank, self.in_features, dtype=dtype, device=device) * self.in_features ** -0.5
+        self.A = torch.nn.Parameter(A)
+        self.B = torch.nn.Parameter(torch.zeros(n_adapters, self.out_features, rank, dtype=dtype, device=device))
+        self.register_buffer("scales", torch.full((n_adapters,), (rank if alpha is None else alpha) / rank,
+                                                  dtype=torch.float32, device=device))
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        if self.scales.dtype != torch.float32:  # the scales stay fp32 under .to(dtype)
+            self.scales = self.scales.float()
+        return self
+
+    def freeze_base(self) -> "KSAdapterLinear":
+        self.values.requires_grad_(False)
+        if self.bias is not None:
+            self.bias.requires_grad_(False)
+        return self
+
+    def forward(self, x: torch.Tensor, ids: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """ids: int32, of x's leading shape or of its first dimensions (one id
+        for each sequence of a padded batch, say); None where the layer has a
+        single adapter."""
+        lead = x.shape[:-1]
+        if ids is None:
+            if self.A.shape[0] != 1:
+                raise ValueError("a layer with several adapters needs ids")
+        else:
+            if ids.shape != lead[:ids.dim()]:
+                raise ValueError(f"ids must have x's leading shape {tuple(lead)} or its first dimensions")
+            ids = ids.reshape(ids.shape + (1,) * (len(lead) - ids.dim())).expand(lead).reshape(-1).contiguous()
+        y = _KSAdapterFn.apply(x.reshape(-1, self.in_features).contiguous(), self.values, self.bias, self.A, self.B,
+                               self.scales, ids, self.pattern)
+        return y.reshape(*lead, self.out_features)

@@ -33,6 +33,8 @@ ks_status fail(ks_status s, const char *fmt, ...) {
 
 ks_status ok() { return KS_OK; }
 
+}  // namespace
+
 // a*b with overflow check on non-negative operands.
 bool mul_ok(int64_t a, int64_t b, int64_t *out) {
     if (a != 0 && b > INT64_MAX / a) return false;
@@ -83,6 +85,8 @@ ks_status check_align(const void *p, int elem, const char *name) {
 ks_status cuda_fail(cudaError_t e, const char *what) {
     return fail(KS_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+namespace {
 
 // Validates a single product and builds the Problem; *noop set for batch == 0.
 ks_status make_problem(const void *X, const void *V, int64_t a, int64_t b, int64_t c, int64_t d,
@@ -756,6 +760,8 @@ ks_status ks_sync_status(void *stream) {
         e = cudaMemcpy(p, &zero, sizeof(zero), cudaMemcpyHostToDevice);
         if (e != cudaSuccess) return cuda_fail(e, "clearing device status");
         if (v & kDevTimeout) return fail(KS_ERR_TIMEOUT, "a bounded device-side wait gave up (status 0x%x)", v);
+        if (v & kDevBadIndex)
+            return fail(KS_ERR_INVALID_ARG, "an adapter id was n_adapters or more (its rows took no adapter)");
         return fail(KS_ERR_CUDA, "device status 0x%x", v);
     }
     return KS_OK;

@@ -130,6 +130,7 @@ cudaError_t launch_butterfly12(const void *X, const void *const *factors, long l
 // Device status word (ks_api.cu): kernels OR these bits in on failure.
 enum DeviceStatusBits : unsigned {
     kDevTimeout = 1u,
+    kDevBadIndex = 2u,  // an adapter id at or past the number of adapters
 };
 unsigned *device_status_ptr();  // address of the status word on the current device
 
@@ -139,5 +140,15 @@ int sm_count();
 // Records the message ks_last_error() returns on this host thread and passes
 // the status through (for entry points defined outside ks_api.cu).
 ks_status record_error(ks_status s, const char *fmt, ...);
+
+
+// Argument checks shared by the entry points (ks_api.cu).
+bool mul_ok(int64_t a, int64_t b, int64_t *out);  // a * b without overflow, operands not negative
+bool ranges_overlap(const void *p, int64_t pbytes, const void *q, int64_t qbytes);
+ks_status check_sizes(int64_t a, int64_t b, int64_t c, int64_t d, int64_t batch, int64_t *in_f, int64_t *out_f,
+                      int64_t *nvals);
+ks_status check_dtype(int dtype);
+ks_status check_align(const void *p, int elem, const char *name);
+ks_status cuda_fail(cudaError_t e, const char *what);
 
 }  // namespace ks
