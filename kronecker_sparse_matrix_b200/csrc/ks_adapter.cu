@@ -36,45 +36,276 @@ __device__ __forceinline__ int adapter_of(const int *ids, long long n, int adapt
     return s < 0 ? -1 : s;
 }
 
-// H[n][r] = scale[s] sum_f X[n][f] W[s][r * rs + f * fs]; one warp per row.
-template <typename T>
+// ---------------------------------------------------------------- H = scale X W^T
+//
+// W[s] is rank x F with F contiguous (A, or B transposed).  H[n][r], r < ldh, is
+// scale[s] sum_f X[n][f] W[s][r][f], zero for ranks past R and rows without an
+// adapter; fp32, or bf16 (rounded once) where it becomes a tensor-core operand:
+// its rounding, 2^-9 of each term of the low-rank sum on average, stays below
+// the rounding of a bf16 result.
+
+// Any size, type and alignment: one warp per row.
+template <typename T, typename O>
 __global__ void __launch_bounds__(256)
-    shrink_kernel(const T *__restrict__ X, const T *__restrict__ W, const float *__restrict__ scales,
-                  const int *__restrict__ ids, float *__restrict__ H, long long N, int F, int R, int ldh, int S,
-                  int rs, int fs, unsigned *status) {
+    shrink_any_kernel(const T *__restrict__ X, const T *__restrict__ W, const float *__restrict__ scales,
+                      const int *__restrict__ ids, O *__restrict__ H, long long N, int F, int R, int ldh, int S,
+                      unsigned *status) {
     const int lane = threadIdx.x & 31;
     const long long n = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (n >= N) return;
     const int s = adapter_of(ids, n, S, status);
-    float *h = H + n * ldh;
+    O *h = H + n * ldh;
     if (s < 0) {
-        for (int r = lane; r < ldh; r += 32) h[r] = 0.f;
+        for (int r = lane; r < ldh; r += 32) put(h + r, 0.f);
         return;
     }
     const T *x = X + n * F, *w = W + (long long)s * R * F;
     const float sc = scales ? scales[s] : 1.f;
-    for (int r0 = 0; r0 < R; r0 += 8) {
+    for (int r0 = 0; r0 < ldh; r0 += 8) {
         float acc[8] = {};
         for (int f = lane; f < F; f += 32) {
             const float xv = to_f(x[f]);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (r0 + e < R) acc[e] = fmaf(xv, to_f(w[(long long)(r0 + e) * rs + (long long)f * fs]), acc[e]);
+                if (r0 + e < R) acc[e] = fmaf(xv, to_f(w[(long long)(r0 + e) * F + f]), acc[e]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], o);
-            if (lane == e && r0 + e < ldh) h[r0 + e] = r0 + e < R ? sc * acc[e] : 0.f;
+            if (lane == e && r0 + e < ldh) put(h + r0 + e, r0 + e < R ? sc * acc[e] : 0.f);
         }
     }
 }
 
-// Y[n][f] = act(Y[n][f] + bias[f] + sum_r H[n][r] W[s][r * rs + f * fs]).
+// The smallest id above `last` among the warp's (INT_MAX: none left).
+__device__ __forceinline__ int next_id(int id, int last) {
+    return (int)__reduce_min_sync(0xFFFFFFFFu, (unsigned)(id > last ? id : INT_MAX));
+}
+
+// fp32, F a multiple of 4 and 16-byte aligned: a warp takes eight rows and eight
+// ranks at a time, its lanes the features (four each), and adds the lanes up at
+// the end: 62 shuffles for the 64 sums, each exchange halving what a lane holds.
+// An adapter's pass runs over all eight rows and keeps those that take it.
+// Bound by X for few ranks (16 FMAs for each 16 bytes a lane loads).
+__global__ void __launch_bounds__(128)
+    shrink_fp32_kernel(const float *__restrict__ X, const float *__restrict__ W, const float *__restrict__ scales,
+                       const int *__restrict__ ids, float *__restrict__ H, long long N, int F, int R, int ldh, int S,
+                       unsigned *status) {
+    const int lane = threadIdx.x & 31;
+    const long long n0 = ((long long)blockIdx.x * 4 + (threadIdx.x >> 5)) * 8;
+    if (n0 >= N) return;
+    const int id = lane < 8 && n0 + lane < N ? adapter_of(ids, n0 + lane, S, status) : -1;
+    const int row = lane >> 2;  // the row and ranks (2 q, 2 q + 1) whose sums end in this lane
+    const long long n = n0 + row;
+    if (__shfl_sync(0xFFFFFFFFu, id, row) < 0 && n < N)
+        for (int r = 2 * (lane & 3); r < ldh; r += 8) {
+            H[n * ldh + r] = 0.f;
+            if (r + 1 < ldh) H[n * ldh + r + 1] = 0.f;
+        }
+    for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
+        const bool mine = __shfl_sync(0xFFFFFFFFu, id, row) == s;
+        const float sc = scales ? scales[s] : 1.f;
+        for (int r0 = 0; r0 < R; r0 += 8) {
+            const float *w = W + ((long long)s * R + r0) * F;
+            float acc[64];
+#pragma unroll
+            for (int q = 0; q < 64; ++q) acc[q] = 0.f;
+            for (int f = lane * 4; f < F; f += 128) {
+                float4 x[8];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {  // rows past the last are read as the last one
+                    const long long nn = n0 + m < N ? n0 + m : N - 1;
+                    x[m] = *reinterpret_cast<const float4 *>(X + nn * F + f);
+                }
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int rr = r0 + r < R ? r : 0;
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(w + (long long)rr * F + f));
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        float a = acc[m * 8 + r];
+                        a = fmaf(x[m].x, v.x, a);
+                        a = fmaf(x[m].y, v.y, a);
+                        a = fmaf(x[m].z, v.z, a);
+                        acc[m * 8 + r] = fmaf(x[m].w, v.w, a);
+                    }
+                }
+            }
+            // sums over the lanes: lane keeps the half of its values that its bit picks
+#pragma unroll
+            for (int half = 32; half >= 2; half >>= 1) {
+                const int bit = half >> 1;  // lane bits 16, 8, 4, 2, 1
+                const bool up = lane & bit;
+#pragma unroll
+                for (int q = 0; q < half; ++q) {
+                    const float send = up ? acc[q] : acc[q + half], keep = up ? acc[q + half] : acc[q];
+                    acc[q] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, bit);
+                }
+            }
+            if (mine) {  // values 2 lane, 2 lane + 1: row lane / 4, ranks 2 (lane % 4) ..
+                const int r = r0 + 2 * (lane & 3);
+                if (r < ldh) H[n * ldh + r] = r < R ? sc * acc[0] : 0.f;
+                if (r + 1 < ldh) H[n * ldh + r + 1] = r + 1 < R ? sc * acc[1] : 0.f;
+            }
+        }
+    }
+}
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8) of bf16 fragments in registers.
+__device__ __forceinline__ void mma16816(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
+                                         unsigned b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The adapters among each 128 rows and their rows, for the tensor-core product
+// (TcAdapters::lists): one warp per 128 rows.
+__device__ void tile_list(const int *__restrict__ ids, int *__restrict__ lists, int list_stride, long long N, int S,
+                          long long tile, int lane) {
+    int id[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const long long n = tile * 128 + 32 * q + lane;
+        id[q] = n < N ? (ids ? ids[n] : 0) : -1;
+        if (id[q] >= S) id[q] = -1;
+    }
+    int *list = lists + tile * list_stride;
+    int count = 0, last = -1;
+    while (true) {
+        int best = INT_MAX;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) best = id[q] > last ? min(best, id[q]) : best;
+        last = (int)__reduce_min_sync(0xFFFFFFFFu, (unsigned)best);
+        if (last == INT_MAX) break;
+        unsigned off[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) off[q] = ~__ballot_sync(0xFFFFFFFFu, id[q] == last);
+        if (lane == 0) {
+            int *e = list + 8 + 8 * count;
+            e[0] = last;
+            *reinterpret_cast<uint4 *>(e + 4) = make_uint4(off[0], off[1], off[2], off[3]);
+        }
+        ++count;
+    }
+    if (lane == 0) list[0] = count;
+}
+
+// bf16, F a multiple of 8 and 16-byte aligned, on the tensor cores (mma.sync: the
+// operands of so narrow a product are read once each, straight into registers,
+// and a tcgen05 tile would first have to pass through shared memory).  A block
+// takes 32 rows and NT * 8 ranks, its eight warps every eighth 32 features.  Both
+// operands have the features contiguous, and a sum does not care which of them an
+// MMA calls its k: lane (g, t) loads the eight features 8 t .. 8 t + 7 of rows g
+// (X, and W) as one 16-byte vector, which is its share of two MMA steps.  The
+// warps' sums meet in shared memory in a fixed order.  Blocks past the rows'
+// build the lists of the tensor-core product that follows.
+template <int NT, typename O>
+__global__ void __launch_bounds__(256)
+    shrink_mma_kernel(const __nv_bfloat16 *__restrict__ X, const __nv_bfloat16 *__restrict__ W,
+                      const float *__restrict__ scales, const int *__restrict__ ids, O *__restrict__ H, long long N,
+                      int F, int R, int ldh, int S, unsigned *status, int row_blocks, int *__restrict__ lists,
+                      int list_stride) {
+    constexpr int MT = 2, ROWS = 16 * MT, RC = 8 * NT, LD = RC + 1;
+    __shared__ float red[4][ROWS][LD];
+    __shared__ int row_id[ROWS], found[ROWS], n_found;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((int)blockIdx.x >= row_blocks) {
+        const long long tile = (long long)(blockIdx.x - row_blocks) * 8 + warp;
+        if (blockIdx.y == 0 && tile * 128 < N) tile_list(ids, lists, list_stride, N, S, tile, lane);
+        return;
+    }
+    const long long n0 = (long long)blockIdx.x * ROWS;
+    const int r0 = blockIdx.y * RC;
+    if (warp == 0) {
+        const int id = n0 + lane < N ? adapter_of(ids, n0 + lane, S, status) : -1;
+        row_id[lane] = id;
+        int count = 0;
+        for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
+            if (lane == 0) found[count] = s;
+            ++count;
+        }
+        if (lane == 0) n_found = count;
+    }
+    __syncthreads();
+    const int g = lane >> 2, t = lane & 3;
+    for (int q = threadIdx.x; q < ROWS * RC; q += 256) {
+        const int m = q / RC, r = r0 + q % RC;
+        if (row_id[m] < 0 && n0 + m < N && r < ldh) put(H + (n0 + m) * ldh + r, 0.f);
+    }
+    const uint4 *x[2 * MT];
+#pragma unroll
+    for (int m = 0; m < 2 * MT; ++m) {  // rows past the last are read as the last one
+        const long long n = n0 + 8 * m + g < N ? n0 + 8 * m + g : N - 1;
+        x[m] = reinterpret_cast<const uint4 *>(X + n * F);
+    }
+    const int n_s = n_found;
+    for (int k = 0; k < n_s; ++k) {
+        const int s = found[k];
+        const uint4 *w[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {  // ranks past R are read as the last one
+            const int r = min(r0 + 8 * j + g, R - 1);
+            w[j] = reinterpret_cast<const uint4 *>(W + ((long long)s * R + r) * F);
+        }
+        float acc[MT][NT][4] = {};
+#pragma unroll NT <= 2 ? 4 : 2
+        for (int f = warp * 32 + 8 * t; f - 8 * t < F; f += 256) {
+            const bool in = f < F;
+            uint4 xv[2 * MT], wv[NT];
+#pragma unroll
+            for (int m = 0; m < 2 * MT; ++m) xv[m] = in ? x[m][f >> 3] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) wv[j] = in ? __ldg(w[j] + (f >> 3)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    mma16816(acc[m][j], xv[2 * m].x, xv[2 * m + 1].x, xv[2 * m].y, xv[2 * m + 1].y, wv[j].x, wv[j].y);
+                    mma16816(acc[m][j], xv[2 * m].z, xv[2 * m + 1].z, xv[2 * m].w, xv[2 * m + 1].w, wv[j].z, wv[j].w);
+                }
+        }
+        // warps 4..7 hand their sums to warps 0..3, which add theirs
+        if (warp >= 4) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        red[warp - 4][16 * m + g + 8 * (e >> 1)][8 * j + 2 * t + (e & 1)] = acc[m][j][e];
+        }
+        __syncthreads();
+        if (warp < 4) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        red[warp][16 * m + g + 8 * (e >> 1)][8 * j + 2 * t + (e & 1)] += acc[m][j][e];
+        }
+        __syncthreads();
+        const float sc = scales ? scales[s] : 1.f;
+        for (int q = threadIdx.x; q < ROWS * RC; q += 256) {
+            const int m = q / RC, c = q % RC, r = r0 + c;
+            if (row_id[m] == s && r < ldh)
+                put(H + (n0 + m) * ldh + r,
+                    r < R ? sc * ((red[0][m][c] + red[1][m][c]) + (red[2][m][c] + red[3][m][c])) : 0.f);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- Y = act(Y + bias + H W)
+
+// Any size and alignment: one thread per output.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    expand_kernel(T *__restrict__ Y, const T *__restrict__ W, const int *__restrict__ ids, const float *__restrict__ H,
-                  long long N, int F, int R, int ldh, int S, int rs, int fs, const T *__restrict__ bias, int act) {
+    expand_any_kernel(T *__restrict__ Y, const T *__restrict__ W, const int *__restrict__ ids,
+                      const float *__restrict__ H, long long N, int F, int R, int ldh, int S, int rs, int fs,
+                      const T *__restrict__ bias, int act) {
     const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
     const long long n = at / F;
     if (n >= N) return;
@@ -90,6 +321,103 @@ __global__ void __launch_bounds__(256)
     }
     put(Y + at, ep_apply(y, bias, f, act));
 }
+
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(*reinterpret_cast<const unsigned *>(&a), *reinterpret_cast<const unsigned *>(&b));
+}
+
+// F a multiple of 4 and vectors of four aligned: a thread owns four outputs of 16
+// rows and passes once over the weights of each adapter among them, four ranks at
+// a time; H is read from shared memory (the same address in a warp).
+// RC: the ranks are contiguous in W (B) and come in whole fours; otherwise the
+// features are (A).
+template <typename T, bool RC>
+__global__ void __launch_bounds__(128)
+    expand_kernel(T *__restrict__ Y, const T *__restrict__ W, const int *__restrict__ ids,
+                  const float *__restrict__ H, long long N, int F, int R, int ldh, int S, const T *__restrict__ bias,
+                  int act) {
+    constexpr int ROWS = 16;
+    extern __shared__ float4 hs[];  // [rank / 4][row]
+    __shared__ int row_id[ROWS];
+    const long long n0 = (long long)blockIdx.x * ROWS;
+    const int rows = (int)min((long long)ROWS, N - n0);
+    if (threadIdx.x < ROWS) {
+        const int s = (int)threadIdx.x < rows ? (ids ? ids[n0 + threadIdx.x] : 0) : -1;
+        row_id[threadIdx.x] = s < S ? s : -1;
+    }
+    const int rq = ldh / 4;
+    for (int q = threadIdx.x; q < rows * rq; q += 128)
+        hs[(q % rq) * ROWS + q / rq] = *reinterpret_cast<const float4 *>(H + n0 * ldh + (long long)q * 4);
+    __syncthreads();
+    const int f = (blockIdx.y * 128 + threadIdx.x) * 4;
+    const bool in = f < F;
+    float4 acc[ROWS];
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m) acc[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int lane = threadIdx.x & 31;
+    const int id = lane < ROWS ? row_id[lane] : -1;
+    for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
+        const unsigned take = __ballot_sync(0xFFFFFFFFu, id == s);
+        if (!in) continue;
+        const T *w = W + (long long)s * R * F;
+        for (int r = 0; r < R; r += 4) {
+            // v[c]: ranks r .. r + 3 of output f + c
+            float4 v[4];
+            if constexpr (RC) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = load4(w + (long long)(f + c) * R + r);
+            } else {
+                float4 u[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    u[e] = r + e < R ? load4(w + (long long)(r + e) * F + f) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[0] = make_float4(u[0].x, u[1].x, u[2].x, u[3].x);
+                v[1] = make_float4(u[0].y, u[1].y, u[2].y, u[3].y);
+                v[2] = make_float4(u[0].z, u[1].z, u[2].z, u[3].z);
+                v[3] = make_float4(u[0].w, u[1].w, u[2].w, u[3].w);
+            }
+            const float4 *h = hs + (r >> 2) * ROWS;
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m) {
+                if (take >> m & 1) {
+                    const float4 x = h[m];
+                    float4 a = acc[m];
+                    a.x = fmaf(x.w, v[0].w, fmaf(x.z, v[0].z, fmaf(x.y, v[0].y, fmaf(x.x, v[0].x, a.x))));
+                    a.y = fmaf(x.w, v[1].w, fmaf(x.z, v[1].z, fmaf(x.y, v[1].y, fmaf(x.x, v[1].x, a.y))));
+                    a.z = fmaf(x.w, v[2].w, fmaf(x.z, v[2].z, fmaf(x.y, v[2].y, fmaf(x.x, v[2].x, a.z))));
+                    a.w = fmaf(x.w, v[3].w, fmaf(x.z, v[3].z, fmaf(x.y, v[3].y, fmaf(x.x, v[3].x, a.w))));
+                    acc[m] = a;
+                }
+            }
+        }
+    }
+    if (!in) return;
+    float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (bias) b = load4(bias + f);
+    T *y = Y + n0 * F + f;
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m) {
+        if (m < rows) {
+            float4 v = load4(y + (long long)m * F);
+            v.x = ep_act_fn(v.x + acc[m].x + b.x, act);
+            v.y = ep_act_fn(v.y + acc[m].y + b.y, act);
+            v.z = ep_act_fn(v.z + acc[m].z + b.z, act);
+            v.w = ep_act_fn(v.w + acc[m].w + b.w, act);
+            store4(y + (long long)m * F, v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dA and dB
 
 // The rows of each adapter in order: perm[offsets[s] .. offsets[s + 1]) holds the
 // rows with id s.  Block s counts the rows of smaller ids and of its own, then
@@ -141,77 +469,414 @@ __global__ void __launch_bounds__(1024)
     if (s == S - 1 && t == 0) offsets[S] = base;
 }
 
-// out[s][r * rs + f * fs] = sum over the rows n of adapter s of P[n][f] Q[n][r].
-template <typename T>
-__global__ void __launch_bounds__(128)
-    grad_kernel(const T *__restrict__ P, const float *__restrict__ Q, const int *__restrict__ perm,
-                const int *__restrict__ offsets, T *__restrict__ out, int N, int F, int R, int ldh, int rs, int fs) {
-    const int f = blockIdx.x * 128 + threadIdx.x, s = blockIdx.y, r0 = blockIdx.z * 8;
-    if (f >= F) return;
-    const int begin = offsets ? offsets[s] : 0, end = offsets ? offsets[s + 1] : N;
-    float acc[8] = {};
-    for (int k = begin; k < end; ++k) {
-        const long long n = perm ? perm[k] : k;
-        const float x = to_f(P[n * F + f]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (r0 + e < R) acc[e] = fmaf(x, Q[n * ldh + r0 + e], acc[e]);
+
+// A gradient is out[s][f][r] = sum over the rows n of adapter s of P[n][f] Q[n][r]
+// (dA: P = X, Q = G; dB: P = dY, Q = H).  The rows in the adapters' order are cut
+// into chunks of `chunk` positions; a block takes some features of one chunk and
+// writes, for each adapter s with rows in chunk z, a partial sum to slot z + s.
+// (A step from one piece (z, s) to the next raises z or s, so z + s is a piece's
+// own, and chunks + S slots are enough, however the rows spread.)  reduce_kernel
+// adds an adapter's slots in order.
+
+// Piece of chunk z: the positions of adapter s in it, [lo, hi).
+struct Piece {
+    int s, lo, hi;
+};
+// The first adapter whose rows end after position p.
+__device__ __forceinline__ int adapter_at(const int *offsets, int S, int p) {
+    int a = 0, b = S;  // offsets[a] <= p < offsets[b] where such exist
+    while (b - a > 1) {
+        const int mid = (a + b) >> 1;
+        if (offsets[mid] <= p)
+            a = mid;
+        else
+            b = mid;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (r0 + e < R) put(out + (long long)s * R * F + (long long)(r0 + e) * rs + (long long)f * fs, acc[e]);
+    return a;
 }
 
+// fp32: a warp takes 128 features (four a lane) and every fourth row of the chunk,
+// RC ranks of each; Q's row is the same address in a warp.  64 FMAs (RC = 16) for
+// each 16 bytes of P a lane loads.  Types and alignment: any (VEC: vectors of four).
+template <typename T, typename Q, int RC, bool VEC>
+__global__ void __launch_bounds__(128)
+    grad_kernel(const T *__restrict__ P, const Q *__restrict__ V, const int *__restrict__ perm,
+                const int *__restrict__ offsets, float *__restrict__ W, int N, int F, int R, int ldh, int S,
+                int chunk) {
+    __shared__ float4 red[3][RC][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int f = (blockIdx.x * 32 + lane) * 4, r0 = blockIdx.z * RC;
+    const int total = offsets ? offsets[S] : N;
+    const int begin = blockIdx.y * chunk, end = min(begin + chunk, total);
+    if (begin >= end) return;
+    int s = offsets ? adapter_at(offsets, S, begin) : 0;
+    for (int lo = begin; lo < end; ++s) {
+        const int hi = offsets ? min(end, offsets[s + 1]) : end;
+        if (hi <= lo) continue;
+        float4 acc[RC];
+#pragma unroll
+        for (int r = 0; r < RC; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int k = lo + warp; k < hi; k += 4) {
+            const long long n = perm ? perm[k] : k;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            const T *p = P + n * F + f;
+            if constexpr (VEC) {
+                if (f < F) x = load4(p);
+            } else {
+                if (f < F) x.x = to_f(p[0]);
+                if (f + 1 < F) x.y = to_f(p[1]);
+                if (f + 2 < F) x.z = to_f(p[2]);
+                if (f + 3 < F) x.w = to_f(p[3]);
+            }
+            const Q *v = V + n * ldh + r0;
+#pragma unroll
+            for (int r = 0; r < RC; r += 4) {
+                if (r0 + r >= ldh) break;
+                const float4 q = load4(v + r);
+                const float qq[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[r + e].x = fmaf(x.x, qq[e], acc[r + e].x);
+                    acc[r + e].y = fmaf(x.y, qq[e], acc[r + e].y);
+                    acc[r + e].z = fmaf(x.z, qq[e], acc[r + e].z);
+                    acc[r + e].w = fmaf(x.w, qq[e], acc[r + e].w);
+                }
+            }
+        }
+        if (warp) {
+#pragma unroll
+            for (int r = 0; r < RC; ++r) red[warp - 1][r][lane] = acc[r];
+        }
+        __syncthreads();
+        if (!warp) {
+            float *w = W + (long long)(blockIdx.y + s) * R * F;
+#pragma unroll
+            for (int r = 0; r < RC; ++r) {
+                if (r0 + r >= R) break;
+                float4 a = acc[r];
+#pragma unroll
+                for (int q = 0; q < 3; ++q) {
+                    const float4 b = red[q][r][lane];
+                    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+                }
+                float *d = w + (long long)(r0 + r) * F + f;
+                if (f + 3 < F && F % 4 == 0) {
+                    store4(d, a);
+                } else {
+                    if (f < F) d[0] = a.x;
+                    if (f + 1 < F) d[1] = a.y;
+                    if (f + 2 < F) d[2] = a.z;
+                    if (f + 3 < F) d[3] = a.w;
+                }
+            }
+        }
+        __syncthreads();
+        lo = hi;
+    }
+}
+
+__device__ __forceinline__ uint4 load8_bf16(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint4 *>(p); }
+__device__ __forceinline__ uint4 load8_bf16(const float *p) {
+    const float4 a = load4(p), b = load4(p + 4);
+    uint4 v;
+    const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w),
+                                 __floats2bfloat162_rn(b.x, b.y), __floats2bfloat162_rn(b.z, b.w)};
+    v.x = *reinterpret_cast<const unsigned *>(&h[0]), v.y = *reinterpret_cast<const unsigned *>(&h[1]);
+    v.z = *reinterpret_cast<const unsigned *>(&h[2]), v.w = *reinterpret_cast<const unsigned *>(&h[3]);
+    return v;
+}
+
+// bf16, F a multiple of 8 and 16-byte aligned: out^T = Q^T P on the tensor cores, m
+// the ranks (MT * 16 of them), n the features, k the rows.  A warp takes 64
+// features: lane (g, t) loads features 8 g .. 8 g + 7 of rows 4 t .. 4 t + 3 as four
+// 16-byte vectors, and pairs rows with byte permutes, which gives its share of
+// eight MMAs whose columns are features 8 g + j, j = 0 .. 7 (the order of the rows
+// within a sum and of the features across columns is free).  P goes straight
+// to registers, four whole 128-byte lines for each warp load; Q, R/512 of P's bytes
+// or so, is staged transposed in shared memory, 128 positions at a time.  Bound by
+// P's bytes.  Q is rounded to bf16 where it is fp32.
+template <int MT, typename Q>
+__global__ void __launch_bounds__(256)
+    grad_mma_kernel(const __nv_bfloat16 *__restrict__ P, const Q *__restrict__ V, const int *__restrict__ perm,
+                    const int *__restrict__ offsets, float *__restrict__ W, int N, int F, int R, int ldh, int S,
+                    int chunk) {
+    constexpr int RC = 16 * MT, POS = 128, LD = POS + 16;  // 72 words a row: 8-byte reads of four rows hit all banks
+    __shared__ __align__(16) unsigned short qs[RC][LD];
+    __shared__ int rows[POS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int f0 = (blockIdx.x * (blockDim.x >> 5) + warp) * 64, r0 = blockIdx.z * RC;
+    const int total = offsets ? offsets[S] : N;
+    const int begin = blockIdx.y * chunk, end = min(begin + chunk, total);
+    if (begin >= end) return;
+    const bool in = f0 + 8 * g < F;
+    const __nv_bfloat16 *p = P + f0 + 8 * g;
+    int s = offsets ? adapter_at(offsets, S, begin) : 0;
+    for (int lo = begin; lo < end; ++s) {
+        const int hi = offsets ? min(end, offsets[s + 1]) : end;
+        if (hi <= lo) continue;
+        float acc[MT][8][4] = {};
+        for (int k0 = lo; k0 < hi; k0 += POS) {
+            const int here = min(POS, hi - k0);
+            __syncthreads();
+            for (int q = threadIdx.x; q < POS * 2 * MT; q += blockDim.x) {
+                const int k = q / (2 * MT), r = (q % (2 * MT)) * 8;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (k < here && r0 + r < ldh) {
+                    const long long n = perm ? perm[k0 + k] : k0 + k;
+                    v = load8_bf16(V + n * ldh + r0 + r);
+                    if (r == 0) rows[k] = (int)n;
+                }
+                const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) qs[r + e][k] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
+            }
+            __syncthreads();
+#pragma unroll 2
+            for (int k = 0; k < here; k += 16) {
+                uint4 x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = make_uint4(0u, 0u, 0u, 0u);
+                    const int kk = k + 4 * t + e;
+                    if (in && kk < here) x[e] = *reinterpret_cast<const uint4 *>(p + (long long)rows[kk] * F);
+                }
+                const unsigned xw[4][4] = {{x[0].x, x[0].y, x[0].z, x[0].w},
+                                           {x[1].x, x[1].y, x[1].z, x[1].w},
+                                           {x[2].x, x[2].y, x[2].z, x[2].w},
+                                           {x[3].x, x[3].y, x[3].z, x[3].w}};
+                uint2 a[MT][2];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    a[m][0] = *reinterpret_cast<const uint2 *>(&qs[16 * m + g][k + 4 * t]);
+                    a[m][1] = *reinterpret_cast<const uint2 *>(&qs[16 * m + g + 8][k + 4 * t]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const unsigned sel = j & 1 ? 0x7632u : 0x5410u;
+                    const unsigned b0 = __byte_perm(xw[0][j >> 1], xw[1][j >> 1], sel);
+                    const unsigned b1 = __byte_perm(xw[2][j >> 1], xw[3][j >> 1], sel);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        mma16816(acc[m][j], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, b0, b1);
+                }
+            }
+        }
+        // acc[m][j]: ranks 16 m + g (+ 8), features f0 + 16 t + j (+ 8)
+        float *w = W + (long long)(blockIdx.y + s) * R * F;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = r0 + 16 * m + g + 8 * h;
+                if (r >= R) continue;
+                float *d = w + (long long)r * F + f0 + 16 * t;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (f0 + 16 * t + 8 * c >= F) continue;
+                    store4(d + 8 * c, make_float4(acc[m][0][2 * h + c], acc[m][1][2 * h + c], acc[m][2][2 * h + c],
+                                                  acc[m][3][2 * h + c]));
+                    store4(d + 8 * c + 4, make_float4(acc[m][4][2 * h + c], acc[m][5][2 * h + c],
+                                                      acc[m][6][2 * h + c], acc[m][7][2 * h + c]));
+                }
+            }
+        lo = hi;
+    }
+}
+
+// out = the sums of the slots of each adapter, in order of the chunks; r * rs + f * fs
+// is an entry's place in out[s].
+template <typename T>
+__global__ void __launch_bounds__(256)
+    reduce_kernel(const float *__restrict__ W, const int *__restrict__ offsets, T *__restrict__ out, int N, int F,
+                  int R, int rs, int fs, int chunk) {
+    const int s = blockIdx.y;
+    const int lo = offsets ? offsets[s] : 0, hi = offsets ? offsets[s + 1] : s == 0 ? N : 0;
+    const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (at >= (long long)R * F) return;
+    float sum = 0.f;
+    if (lo < hi) {
+        const float *w = W + (long long)s * R * F + at;
+        for (int z = lo / chunk; z <= (hi - 1) / chunk; ++z) sum += w[(long long)z * R * F];
+    }
+    const int r = (int)(at / F), f = (int)(at - (long long)r * F);
+    put(out + (long long)s * R * F + (long long)r * rs + (long long)f * fs, sum);
+}
+
+// The adapters' weights as the tensor-core product reads them: out[s][f][r], r < Rp
+// (a multiple of 8), zero past R, from W[s][r * rs + f * fs].
+__global__ void __launch_bounds__(256)
+    pack_kernel(const unsigned short *__restrict__ W, unsigned short *__restrict__ out, int S, int F, int R, int Rp,
+                int rs, int fs) {
+    const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int octets = Rp / 8;
+    if (at >= (long long)S * octets * F) return;
+    const int f = (int)(at % F), o = (int)(at / F % octets);
+    const long long s = at / F / octets;
+    const unsigned short *w = W + s * R * F + (long long)f * fs;
+    unsigned v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int r = 8 * o + e;
+        if (r < R) v[e >> 1] |= (unsigned)w[(long long)r * rs] << (16 * (e & 1));
+    }
+    *reinterpret_cast<uint4 *>(out + (s * F + f) * Rp + 8 * o) = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// ---------------------------------------------------------------- host side
 struct Adapters {
-    const void *A, *B;
     const float *scales;
     const int *ids;
-    int S, R, ldh;
+    int S, R;
     bool bf16;
     cudaStream_t st;
 };
 
-// W[s][r][f] at r * rs + f * fs: A is rank x in, B is out x rank
-cudaError_t shrink(const Adapters &q, const void *X, bool with_a, long long N, int F, float *H) {
-    const int rs = with_a ? F : 1, fs = with_a ? 1 : q.R;
-    const unsigned grid = (unsigned)((N + 7) / 8);
-    if (q.bf16)
-        shrink_kernel<__nv_bfloat16><<<grid, 256, 0, q.st>>>(
-            static_cast<const __nv_bfloat16 *>(X), static_cast<const __nv_bfloat16 *>(with_a ? q.A : q.B), q.scales,
-            q.ids, H, N, F, q.R, q.ldh, q.S, rs, fs, device_status_ptr());
-    else
-        shrink_kernel<float><<<grid, 256, 0, q.st>>>(static_cast<const float *>(X),
-                                                     static_cast<const float *>(with_a ? q.A : q.B), q.scales, q.ids,
-                                                     H, N, F, q.R, q.ldh, q.S, rs, fs, device_status_ptr());
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int round_up(int x, int m) { return (x + m - 1) / m * m; }
+
+// Words of a tile's list (TcAdapters::lists), and tiles.
+int list_stride(int S) { return 8 + 8 * std::min(S, 128); }
+long long list_tiles(long long N) { return (N + 127) / 128; }
+
+// Whether X and W (S x R x F) can take the vector kernels.
+bool shrink_vec(const Adapters &q, const void *X, const void *W, int F) {
+    return aligned(X, 16) && aligned(W, 16) && F % (q.bf16 ? 8 : 4) == 0;
+}
+
+template <typename O>
+cudaError_t shrink_bf16(const Adapters &q, const void *X, const void *W, long long N, int F, O *H, int ldh,
+                        int *lists) {
+    const auto *x = static_cast<const __nv_bfloat16 *>(X), *w = static_cast<const __nv_bfloat16 *>(W);
+    if (!shrink_vec(q, X, W, F)) {  // (with lists the caller has made sure of vectors)
+        shrink_any_kernel<<<(unsigned)((N + 7) / 8), 256, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S,
+                                                                     device_status_ptr());
+        return cudaGetLastError();
+    }
+    const int row_blocks = (int)((N + 31) / 32), list_blocks = lists ? (int)((list_tiles(N) + 7) / 8) : 0;
+    const int nt = ldh <= 8 ? 1 : ldh <= 16 ? 2 : ldh <= 32 ? 4 : 8;
+    const dim3 grid((unsigned)(row_blocks + list_blocks), (unsigned)((ldh + 8 * nt - 1) / (8 * nt)));
+    const auto go = [&](auto kernel) {
+        kernel<<<grid, 256, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S, device_status_ptr(), row_blocks,
+                                       lists, list_stride(q.S));
+    };
+    switch (nt) {
+        case 1: go(shrink_mma_kernel<1, O>); break;
+        case 2: go(shrink_mma_kernel<2, O>); break;
+        case 4: go(shrink_mma_kernel<4, O>); break;
+        default: go(shrink_mma_kernel<8, O>); break;
+    }
     return cudaGetLastError();
 }
 
-cudaError_t expand(const Adapters &q, void *Y, bool with_a, long long N, int F, const float *H, const void *bias,
-                   int act) {
-    const int rs = with_a ? F : 1, fs = with_a ? 1 : q.R;
-    const unsigned grid = (unsigned)((N * F + 255) / 256);
-    if (q.bf16)
-        expand_kernel<__nv_bfloat16><<<grid, 256, 0, q.st>>>(
-            static_cast<__nv_bfloat16 *>(Y), static_cast<const __nv_bfloat16 *>(with_a ? q.A : q.B), q.ids, H, N, F,
-            q.R, q.ldh, q.S, rs, fs, static_cast<const __nv_bfloat16 *>(bias), act);
+// H = scale X W^T, fp32.
+cudaError_t shrink_fp32_out(const Adapters &q, const void *X, const void *W, long long N, int F, float *H, int ldh) {
+    if (q.bf16) return shrink_bf16<float>(q, X, W, N, F, H, ldh, nullptr);
+    const auto *x = static_cast<const float *>(X), *w = static_cast<const float *>(W);
+    if (shrink_vec(q, X, W, F))
+        shrink_fp32_kernel<<<(unsigned)((N + 31) / 32), 128, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S,
+                                                                        device_status_ptr());
     else
-        expand_kernel<float><<<grid, 256, 0, q.st>>>(static_cast<float *>(Y),
-                                                     static_cast<const float *>(with_a ? q.A : q.B), q.ids, H, N, F,
-                                                     q.R, q.ldh, q.S, rs, fs, static_cast<const float *>(bias), act);
+        shrink_any_kernel<<<(unsigned)((N + 7) / 8), 256, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S,
+                                                                     device_status_ptr());
     return cudaGetLastError();
 }
 
-cudaError_t grad(const Adapters &q, const void *P, const float *Q, const int *perm, const int *offsets, void *out,
-                 bool with_a, long long N, int F) {
+// Y = act(Y + bias + H W); with_a: W is A (rank x F), else B (F x rank).
+template <typename T>
+cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long long N, int F, const float *H, int ldh,
+                   const void *bias, int act) {
+    T *y = static_cast<T *>(Y);
+    const T *w = static_cast<const T *>(W), *b = static_cast<const T *>(bias);
+    const size_t smem = (size_t)ldh * 16 * 4;
+    if (F % 4 == 0 && aligned(Y, 4 * sizeof(T)) && aligned(W, 4 * sizeof(T)) && aligned(bias, 4 * sizeof(T)) &&
+        (with_a || q.R % 4 == 0) && smem <= 40 * 1024 && (F + 511) / 512 <= 65535) {
+        const dim3 grid((unsigned)((N + 15) / 16), (unsigned)((F + 511) / 512));
+        if (with_a)
+            expand_kernel<T, false><<<grid, 128, smem, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, b, act);
+        else
+            expand_kernel<T, true><<<grid, 128, smem, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, b, act);
+        return cudaGetLastError();
+    }
     const int rs = with_a ? F : 1, fs = with_a ? 1 : q.R;
-    const dim3 grid((unsigned)((F + 127) / 128), (unsigned)q.S, (unsigned)((q.R + 7) / 8));
+    const long long blocks = (N * F + 255) / 256;
+    if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+    expand_any_kernel<T><<<(unsigned)blocks, 256, 0, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, rs, fs, b, act);
+    return cudaGetLastError();
+}
+
+// How a gradient of width F is cut: `bx` blocks of features, `bz` of ranks, chunks of
+// `chunk` of the N rows, about four blocks for each SM.
+struct GradPlan {
+    bool mma;
+    int warps, bx, bz, rc, chunk, chunks;
+    size_t bytes;  // of the partial sums
+};
+GradPlan grad_plan(const Adapters &q, const void *P, long long N, int F) {
+    GradPlan g{};
+    g.mma = q.bf16 && F % 8 == 0 && aligned(P, 16);
+    if (g.mma) {
+        g.warps = std::min(8, (F + 63) / 64);
+        g.bx = (F + 64 * g.warps - 1) / (64 * g.warps);
+        g.rc = std::min(64, round_up(q.R, 16));
+        if (g.rc == 48) g.rc = 64;
+    } else {
+        g.warps = 4;
+        g.bx = (F + 127) / 128;
+        g.rc = q.R <= 8 ? 8 : 16;
+    }
+    g.bz = (q.R + g.rc - 1) / g.rc;
+    const long long wanted = std::max<long long>(1, 4LL * sm_count() * 4 / g.warps / ((long long)g.bx * g.bz));
+    const int least = 64;
+    long long chunk = std::max<long long>(least, (N + wanted - 1) / wanted);
+    chunk = std::min<long long>((chunk + 15) / 16 * 16, std::max<long long>(16, (N + 15) / 16 * 16));
+    chunk = std::max<long long>(chunk, (N + 65534) / 65535);  // grid limit
+    g.chunk = (int)chunk;
+    g.chunks = (int)((N + chunk - 1) / chunk);
+    g.bytes = (size_t)(g.chunks + q.S) * (size_t)q.R * (size_t)F * 4;
+    return g;
+}
+
+template <typename Q>
+cudaError_t grad(const Adapters &q, const GradPlan &g, const void *P, const Q *V, int ldh, const int *perm,
+                 const int *offsets, void *out, bool with_a, long long N, int F, float *W) {
+    const dim3 grid((unsigned)g.bx, (unsigned)g.chunks, (unsigned)g.bz);
+    const int n = (int)N;
+    if (g.mma) {
+        const auto *p = static_cast<const __nv_bfloat16 *>(P);
+        const auto go = [&](auto kernel) {
+            kernel<<<grid, 32 * g.warps, 0, q.st>>>(p, V, perm, offsets, W, n, F, q.R, ldh, q.S, g.chunk);
+        };
+        if (g.rc == 16)
+            go(grad_mma_kernel<1, Q>);
+        else if (g.rc == 32)
+            go(grad_mma_kernel<2, Q>);
+        else
+            go(grad_mma_kernel<4, Q>);
+    } else {
+        const auto go = [&](auto kernel, const auto *p) {
+            kernel<<<grid, 128, 0, q.st>>>(p, V, perm, offsets, W, n, F, q.R, ldh, q.S, g.chunk);
+        };
+        if (q.bf16) {
+            const auto *p = static_cast<const __nv_bfloat16 *>(P);
+            g.rc == 8 ? go(grad_kernel<__nv_bfloat16, Q, 8, false>, p) : go(grad_kernel<__nv_bfloat16, Q, 16, false>, p);
+        } else {
+            const auto *p = static_cast<const float *>(P);
+            const bool vec = F % 4 == 0 && aligned(P, 16);
+            if (g.rc == 8)
+                vec ? go(grad_kernel<float, Q, 8, true>, p) : go(grad_kernel<float, Q, 8, false>, p);
+            else
+                vec ? go(grad_kernel<float, Q, 16, true>, p) : go(grad_kernel<float, Q, 16, false>, p);
+        }
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int rs = with_a ? F : 1, fs = with_a ? 1 : q.R;
+    const dim3 rgrid((unsigned)(((long long)q.R * F + 255) / 256), (unsigned)q.S);
     if (q.bf16)
-        grad_kernel<__nv_bfloat16><<<grid, 128, 0, q.st>>>(static_cast<const __nv_bfloat16 *>(P), Q, perm, offsets,
-                                                           static_cast<__nv_bfloat16 *>(out), (int)N, F, q.R, q.ldh,
-                                                           rs, fs);
+        reduce_kernel<<<rgrid, 256, 0, q.st>>>(W, offsets, static_cast<__nv_bfloat16 *>(out), n, F, q.R, rs, fs, g.chunk);
     else
-        grad_kernel<float><<<grid, 128, 0, q.st>>>(static_cast<const float *>(P), Q, perm, offsets,
-                                                   static_cast<float *>(out), (int)N, F, q.R, q.ldh, rs, fs);
+        reduce_kernel<<<rgrid, 256, 0, q.st>>>(W, offsets, static_cast<float *>(out), n, F, q.R, rs, fs, g.chunk);
     return cudaGetLastError();
 }
 
@@ -255,7 +920,40 @@ ks_status check_apart(const void *out, int64_t bytes, const char *name, const vo
     return KS_OK;
 }
 
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+// Offsets of the parts of one workspace, 256-byte aligned.
+struct Layout {
+    size_t bytes = 0;
+    size_t add(size_t n) {
+        const size_t at = bytes;
+        bytes += (n + 255) / 256 * 256;
+        return at;
+    }
+};
+
+// Whether the tensor-core kernel can take the product with adapters beside it:
+// bf16, a pattern that AUTO gives to it, and A's vectors aligned (null: a
+// workspace's).  The product's V may be null: a workspace's.
+bool fuses(const Adapters &q, Problem p, const void *A, int F, const void *bias) {
+    if (!q.bf16) return false;
+    static const char dummy[16] __attribute__((aligned(256))) = {};
+    if (!p.V) p.V = dummy;
+    p.bias = bias;
+    Plan plan;
+    const char *why = "";
+    const int ldh = round_up(q.R, 8);
+    const TcAdapters tc{dummy, dummy, nullptr, q.S, ldh, ldh, 0};
+    return make_plan(p, KS_VARIANT_AUTO, &plan, &why) && plan.variant == KS_VARIANT_TC &&
+           tc_adapters_supported(p, tc) && shrink_vec(q, p.X, A, F);
+}
+
+cudaError_t pack(const Adapters &q, const void *W, void *out, int F, int Rp, bool with_a) {
+    const long long n = (long long)q.S * F * (Rp / 8);
+    if ((n + 255) / 256 > INT_MAX) return cudaErrorInvalidConfiguration;
+    pack_kernel<<<(unsigned)((n + 255) / 256), 256, 0, q.st>>>(static_cast<const unsigned short *>(W),
+                                                               static_cast<unsigned short *>(out), q.S, F, q.R, Rp,
+                                                               with_a ? F : 1, with_a ? 1 : q.R);
+    return cudaGetLastError();
+}
 
 ks_status alloc(char **p, size_t bytes, cudaStream_t st) {
     const cudaError_t e = pool_alloc(reinterpret_cast<void **>(p), bytes, st);
@@ -282,20 +980,48 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         return record_error(KS_ERR_INVALID_ARG, "unknown activation %d", activation);
     if (batch == 0) return KS_OK;
     if ((s = check_apart(Y, batch * o.out_f * o.elem, "Y", A, B, scales, ids, n_adapters, batch, o)) != KS_OK) return s;
+    Problem p;
+    bool noop = false;
+    if ((s = make_problem(X, values, a, b, c, d, batch, Y, dtype, stream, &p, &noop)) != KS_OK) return s;
     if ((s = check_align(bias, o.elem, "bias")) != KS_OK) return s;
     if (bias && ranges_overlap(Y, batch * o.out_f * o.elem, bias, o.out_f * o.elem))
         return record_error(KS_ERR_INVALID_ARG, "Y overlaps bias");
-    // The product checks X, values and Y; the adapters, the bias and the
-    // activation are added to it.  In bf16 the product is rounded before they are.
-    if ((s = ks_matmul(X, values, a, b, c, d, batch, Y, dtype, stream)) != KS_OK) return s;
-    const Adapters q{A, B, scales, ids, (int)n_adapters, (int)rank, (int)(rank + 3) / 4 * 4, dtype == KS_BF16,
-                     static_cast<cudaStream_t>(stream)};
+    const Adapters q{scales, ids, (int)n_adapters, (int)rank, dtype == KS_BF16, p.stream};
+    const int in_f = (int)o.in_f, out_f = (int)o.out_f;
+    cudaError_t e;
     char *w = nullptr;
-    if ((s = alloc(&w, (size_t)batch * q.ldh * 4, q.st)) != KS_OK) return s;
-    float *H = reinterpret_cast<float *>(w);
-    cudaError_t e = shrink(q, X, true, batch, (int)o.in_f, H);
-    if (e == cudaSuccess) e = expand(q, Y, false, batch, (int)o.out_f, H, bias, activation);
-    if (e != cudaSuccess) s = cuda_fail(e, "adapter launch");
+    if (fuses(q, p, A, in_f, bias)) {
+        // the adapters as K steps of the tensor-core product, with its bias and activation
+        Layout m;
+        const int ldh = round_up(q.R, 8);
+        const size_t h = m.add((size_t)batch * ldh * 2), l = m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4);
+        const bool packed = q.R != ldh || !aligned(B, 16);
+        const size_t b_at = packed ? m.add((size_t)q.S * out_f * ldh * 2) : 0;
+        if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
+        const TcAdapters tc{packed ? w + b_at : B, w + h, reinterpret_cast<int *>(w + l), q.S, ldh, ldh, list_stride(q.S)};
+        e = packed ? pack(q, B, w + b_at, out_f, ldh, false) : cudaSuccess;
+        if (e == cudaSuccess)
+            e = shrink_bf16(q, X, A, batch, in_f, reinterpret_cast<__nv_bfloat16 *>(w + h), ldh,
+                            reinterpret_cast<int *>(w + l));
+        if (e == cudaSuccess) {
+            p.bias = bias;
+            p.act = activation;
+            p.ad = &tc;
+            s = run(p, KS_VARIANT_TC);
+        }
+    } else {
+        // The product, then one pass that adds the adapters, the bias and the
+        // activation.  In bf16 the product is rounded before they are added.
+        const int ldh = round_up(q.R, 4);
+        if ((s = alloc(&w, (size_t)batch * ldh * 4, q.st)) != KS_OK) return s;
+        float *H = reinterpret_cast<float *>(w);
+        s = run(p, KS_VARIANT_AUTO);
+        e = s == KS_OK ? shrink_fp32_out(q, X, A, batch, in_f, H, ldh) : cudaSuccess;
+        if (s == KS_OK && e == cudaSuccess)
+            e = q.bf16 ? expand<__nv_bfloat16>(q, Y, B, false, batch, out_f, H, ldh, bias, activation)
+                       : expand<float>(q, Y, B, false, batch, out_f, H, ldh, bias, activation);
+    }
+    if (e != cudaSuccess && s == KS_OK) s = cuda_fail(e, "adapter launch");
     e = cudaFreeAsync(w, q.st);
     if (e != cudaSuccess && s == KS_OK) s = cuda_fail(e, "workspace free");
     return s;
@@ -322,8 +1048,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
             if (ranges_overlap(outs[k].p, outs[k].bytes, outs[j].p, outs[j].bytes))
                 return record_error(KS_ERR_INVALID_ARG, "%s overlaps %s", outs[k].name, outs[j].name);
     }
-    const Adapters q{A, B, scales, ids, (int)n_adapters, (int)rank, (int)(rank + 3) / 4 * 4, dtype == KS_BF16,
-                     static_cast<cudaStream_t>(stream)};
+    const Adapters q{scales, ids, (int)n_adapters, (int)rank, dtype == KS_BF16, static_cast<cudaStream_t>(stream)};
     if (batch == 0) {  // empty sums
         cudaError_t e = cudaSuccess;
         if (dA) e = cudaMemsetAsync(dA, 0, (size_t)o.abytes, q.st);
@@ -332,30 +1057,85 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     }
     if (!dY || ((dA || dB) && !X) || (dX && !values))
         return record_error(KS_ERR_INVALID_ARG, "dY, X (for dA and dB) and values (for dX) must be non-null");
-    if ((s = check_align(dY, o.elem, "dY")) != KS_OK || (s = check_align(X, o.elem, "X")) != KS_OK) return s;
-    if (dX && (s = ks_matmul_dx(dY, values, a, b, c, d, batch, dX, dtype, stream)) != KS_OK) return s;
+    if ((s = check_align(dY, o.elem, "dY")) != KS_OK || (s = check_align(X, o.elem, "X")) != KS_OK ||
+        (s = check_align(values, o.elem, "values")) != KS_OK)
+        return s;
     if (!dX && !dA && !dB) return KS_OK;
-    const size_t hb = up256((size_t)batch * q.ldh * 4);
-    const size_t pb = up256((size_t)batch * 4), ob = up256((size_t)(q.S + 1) * 4);
+    const int in_f = (int)o.in_f, out_f = (int)o.out_f;
+    // Workspace: G and H, B transposed to rank x out (what G contracts over), the
+    // rows' order, the partial sums (dA's, then dB's), and for a fused dX the
+    // transposed values, A packed to in x rank and the lists.
+    Layout m;
+    const int ldh = round_up(q.R, 8);
+    const size_t bt = m.add((size_t)o.bbytes), vt = dX ? m.add((size_t)(o.nvals * o.elem)) : 0;
+    Problem p;  // dX = dY K: the product of pattern (a, c, b, d) with the transposed blocks
+    bool fused = false;
+    if (dX) {
+        p = Problem{dY, nullptr, dX, a, c, b, d, batch, dtype, q.st};
+        fused = fuses(q, p, nullptr, out_f, nullptr);
+    }
+    const size_t h_bytes = (size_t)batch * ldh * (fused ? 2 : 4);
+    const size_t g_at = dX || dA ? m.add(h_bytes) : 0, h_at = dB ? m.add(h_bytes) : 0;
+    const size_t l_at = fused ? m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4) : 0;
+    const size_t ap = fused ? m.add((size_t)q.S * in_f * ldh * 2) : 0;
+    const bool sorted = ids && (dA || dB);
+    const size_t perm_at = sorted ? m.add((size_t)batch * 4) : 0, off_at = sorted ? m.add((size_t)(q.S + 1) * 4) : 0;
+    const GradPlan ga = grad_plan(q, X, batch, in_f), gb = grad_plan(q, dY, batch, out_f);
+    const size_t w_at = dA || dB ? m.add(std::max(dA ? ga.bytes : 0, dB ? gb.bytes : 0)) : 0;
     char *w = nullptr;
-    if ((s = alloc(&w, 2 * hb + pb + ob, q.st)) != KS_OK) return s;
-    float *G = reinterpret_cast<float *>(w), *H = reinterpret_cast<float *>(w + hb);
-    int *perm = reinterpret_cast<int *>(w + 2 * hb), *offsets = reinterpret_cast<int *>(w + 2 * hb + pb);
+    if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
+    int *perm = sorted ? reinterpret_cast<int *>(w + perm_at) : nullptr;
+    int *offsets = sorted ? reinterpret_cast<int *>(w + off_at) : nullptr;
+    float *W = reinterpret_cast<float *>(w + w_at);
+    const auto f32 = [&](size_t at) { return reinterpret_cast<float *>(w + at); };
+    const auto b16 = [&](size_t at) { return reinterpret_cast<__nv_bfloat16 *>(w + at); };
     cudaError_t e = cudaSuccess;
-    const auto then = [&](cudaError_t r) { if (e == cudaSuccess) e = r; };
-    if (dX || dA) then(shrink(q, dY, false, batch, (int)o.out_f, G));
-    if (dX && e == cudaSuccess) then(expand(q, dX, true, batch, (int)o.in_f, G, nullptr, KS_ACT_NONE));
-    if ((dA || dB) && ids && e == cudaSuccess) {
-        order_kernel<<<(unsigned)q.S, 1024, 0, q.st>>>(ids, perm, offsets, (int)batch, q.S);
-        then(cudaGetLastError());
+    const auto then = [&](auto &&step) { if (e == cudaSuccess && s == KS_OK) e = step(); };
+    if (dX || dA) {
+        then([&] { return launch_transpose_blocks(B, w + bt, q.S, o.out_f, q.R, dtype, q.st); });
+        then([&] {
+            int *lists = fused ? reinterpret_cast<int *>(w + l_at) : nullptr;
+            return fused ? shrink_bf16(q, dY, w + bt, batch, out_f, b16(g_at), ldh, lists)
+                         : shrink_fp32_out(q, dY, w + bt, batch, out_f, f32(g_at), ldh);
+        });
     }
-    if (!ids) perm = offsets = nullptr;
-    if (dA && e == cudaSuccess) then(grad(q, X, G, perm, offsets, dA, true, batch, (int)o.in_f));
-    if (dB && e == cudaSuccess) {
-        then(shrink(q, X, true, batch, (int)o.in_f, H));
-        if (e == cudaSuccess) then(grad(q, dY, H, perm, offsets, dB, false, batch, (int)o.out_f));
+    if (dX) {
+        then([&] { return launch_transpose_blocks(values, w + vt, a * d, b, c, dtype, q.st); });
+        p.V = w + vt;
+        const TcAdapters tc{w + ap, w + g_at, reinterpret_cast<int *>(w + l_at), q.S, ldh, ldh, list_stride(q.S)};
+        if (fused) {
+            then([&] { return pack(q, A, w + ap, in_f, ldh, true); });
+            p.ad = &tc;
+        }
+        if (e == cudaSuccess) s = run(p, fused ? KS_VARIANT_TC : KS_VARIANT_AUTO);
+        if (!fused)
+            then([&] {
+                return q.bf16
+                           ? expand<__nv_bfloat16>(q, dX, A, true, batch, in_f, f32(g_at), ldh, nullptr, KS_ACT_NONE)
+                           : expand<float>(q, dX, A, true, batch, in_f, f32(g_at), ldh, nullptr, KS_ACT_NONE);
+            });
     }
-    if (e != cudaSuccess) s = cuda_fail(e, "adapter gradient launch");
+    if (sorted)
+        then([&] {
+            order_kernel<<<(unsigned)q.S, 1024, 0, q.st>>>(ids, perm, offsets, (int)batch, q.S);
+            return cudaGetLastError();
+        });
+    if (dA)
+        then([&] {
+            return fused ? grad(q, ga, X, b16(g_at), ldh, perm, offsets, dA, true, batch, in_f, W)
+                         : grad(q, ga, X, f32(g_at), ldh, perm, offsets, dA, true, batch, in_f, W);
+        });
+    if (dB) {
+        then([&] {
+            return fused ? shrink_bf16(q, X, A, batch, in_f, b16(h_at), ldh, nullptr)
+                         : shrink_fp32_out(q, X, A, batch, in_f, f32(h_at), ldh);
+        });
+        then([&] {
+            return fused ? grad(q, gb, dY, b16(h_at), ldh, perm, offsets, dB, false, batch, out_f, W)
+                         : grad(q, gb, dY, f32(h_at), ldh, perm, offsets, dB, false, batch, out_f, W);
+        });
+    }
+    if (e != cudaSuccess && s == KS_OK) s = cuda_fail(e, "adapter gradient launch");
     e = cudaFreeAsync(w, q.st);
     if (e != cudaSuccess && s == KS_OK) s = cuda_fail(e, "workspace free");
     return s;

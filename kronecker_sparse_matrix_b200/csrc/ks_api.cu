@@ -86,8 +86,6 @@ ks_status cuda_fail(cudaError_t e, const char *what) {
     return fail(KS_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-namespace {
-
 // Validates a single product and builds the Problem; *noop set for batch == 0.
 ks_status make_problem(const void *X, const void *V, int64_t a, int64_t b, int64_t c, int64_t d,
                        int64_t batch, void *Y, int dtype, void *stream, Problem *p, bool *noop) {
@@ -127,6 +125,8 @@ ks_status run(const Problem &p, int variant) {
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
     return ok();
 }
+
+namespace {
 
 // Device status word, one per device (a __device__ variable is instantiated
 // per device by the runtime).

@@ -9,6 +9,17 @@
 
 namespace ks {
 
+// Low-rank adapters that the tensor-core kernel adds to a bf16 product:
+// Y[n] += H[n] W[s]^T for the rows n of adapter s.  lists, per 128 rows: [0] the
+// number of adapters among them, then from [8] on eight words for each: s, three
+// unused, and a bit for each of the 128 rows that does NOT take it.
+struct TcAdapters {
+    const void *W;      // S x out_features x R bf16, R a multiple of 8, 16-byte aligned
+    const void *H;      // batch x ldh bf16, ldh a multiple of 8, 16-byte aligned
+    const int *lists;   // list_stride words for each 128 rows, 16-byte aligned
+    int S, R, ldh, list_stride;
+};
+
 // One KS product, after validation: Y = X K^T with K of pattern (a,b,c,d).
 struct Problem {
     const void *X;
@@ -25,6 +36,7 @@ struct Problem {
     // caller's buffers only (the fp32 kernel reads the values in place instead
     // of staging a transposed copy in a pooled workspace).
     bool no_workspace = false;
+    const TcAdapters *ad = nullptr;  // adapters of the tensor-core kernel (plan with tc_adapters_supported)
 
     int64_t in_features() const { return a * c * d; }
     int64_t out_features() const { return a * b * d; }
@@ -60,6 +72,7 @@ bool make_plan(const Problem &p, int variant, Plan *out, const char **why);
 bool stream_supported(const Problem &p);
 bool fma_supported(const Problem &p, const char **why);
 bool tc_supported(const Problem &p, const char **why);
+bool tc_adapters_supported(const Problem &p, const TcAdapters &q);
 FmaConfig fma_choose(const Problem &p);
 TcConfig tc_choose(const Problem &p);
 
@@ -150,5 +163,10 @@ ks_status check_sizes(int64_t a, int64_t b, int64_t c, int64_t d, int64_t batch,
 ks_status check_dtype(int dtype);
 ks_status check_align(const void *p, int elem, const char *name);
 ks_status cuda_fail(cudaError_t e, const char *what);
+// Validates one product's arguments into a Problem (*noop: batch == 0), and runs a Problem with a
+// ks_variant (ks_api.cu).
+ks_status make_problem(const void *X, const void *V, int64_t a, int64_t b, int64_t c, int64_t d, int64_t batch,
+                       void *Y, int dtype, void *stream, Problem *p, bool *noop);
+ks_status run(const Problem &p, int variant);
 
 }  // namespace ks

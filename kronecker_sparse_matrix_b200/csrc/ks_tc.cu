@@ -155,6 +155,24 @@ struct TcParams {
     int x3d;                         // X chunks come from the (c*d, a, N) map (DLS < 8, or d == 8)
 };
 
+// Low-rank adapters beside the product (bf16): Y[n] += H[n] W[s]^T for the rows n
+// of each adapter s, as further K steps of the same accumulation.  After a tile's
+// X chunks come, for each adapter that its 128 rows hold (lists), chunks of
+// CTJ ranks: the transposer warps copy the rows' H into the ring slot as one
+// operand plane (the same for every l), the producer fetches W[s] of the tile's
+// outputs into the values ring in the values' own layout, and the MMAs leave
+// out the lanes of the rows of other adapters, so that nothing an adapter holds
+// (infinities, NaN) reaches a row that does not take it.  Y is still written once.
+template <bool AD>
+struct TcAd {};
+template <>
+struct TcAd<true> {
+    CUtensorMap wmap;        // W viewed as (rank, k, l, i + a * s)
+    const uint16_t *H;       // N x ldh bf16
+    const int *lists;        // per 128 rows: see TcAdapters
+    int R, ldh, list_stride;
+};
+
 // Element type T: __nv_bfloat16 (kind::f16) or float (kind::tf32).
 template <typename T>
 __device__ __forceinline__ void mma_kind(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -186,10 +204,11 @@ __device__ __forceinline__ void transpose4x4_b32(const uint4 (&in)[4], uint4 (&o
 // a 4-D TMA store of [k][row][l] boxes (32-byte l runs, d > DLS), chosen at compile
 // time so that the other instantiations carry none of it (a run-time choice
 // cost the d == DLS TF32 epilogue 5-7%).
-template <int DLS, typename T, bool EP, bool Y4 = false>
+// AD: adapters beside the product (TcAd).
+template <int DLS, typename T, bool EP, bool Y4 = false, bool AD = false>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap vmap,
-              const __grid_constant__ CUtensorMap ymap, const TcParams p) {
+              const __grid_constant__ CUtensorMap ymap, const TcParams p, const __grid_constant__ TcAd<AD> ad) {
     constexpr int ES = (int)sizeof(T);
     constexpr int KJ = step_j(ES);          // j per MMA
     constexpr int CTJ = chunk_j(DLS, ES);
@@ -278,6 +297,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(sV + vs * p.v_stage_bytes, &vmap, &v_full[vs], ch * CTJ, ps * p.bp, i * p.d + l0);
                     ++vq;
                 }
+                if constexpr (AD) {
+                    const int *list = ad.lists + rb * ad.list_stride;
+                    const int count = list[0];
+                    for (int q = 0; q < count && ok; ++q) {
+                        const int is = i + p.a * list[8 + 8 * q];
+                        for (int r0 = 0; r0 < ad.R && ok; r0 += CTJ) {
+                            // the slot is free: the transposer warps may write the rows' H there
+                            const int xs = xq % S;
+                            ok = mbar_wait(&x_empty[xs], ((xq / S) & 1) ^ 1, abort_flag, p.status, wait_ns);
+                            if (!ok) break;
+                            mbar_arrive(&x_full[xs]);
+                            ++xq;
+                            const int vs = vq % VS;
+                            ok = mbar_wait(&v_empty[vs], ((vq / VS) & 1) ^ 1, abort_flag, p.status, wait_ns);
+                            if (!ok) break;
+                            mbar_expect_tx(&v_full[vs], (uint32_t)p.v_stage_bytes);
+                            tma_load_4d(sV + vs * p.v_stage_bytes, &ad.wmap, &v_full[vs], r0, ps * p.bp, l0, is);
+                            ++vq;
+                        }
+                    }
+                }
             }
             // On abort, copies already issued may still be landing in shared
             // memory: wait (bounded) for them before leaving.
@@ -300,8 +340,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (a_major << 15) |
                                    ((uint32_t)(p.bp >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
             uint32_t xq = 0, vq = 0, accq = 0;
+            uint32_t ad_phase = 0;  // DLS == 1: a_ready's parity of each slot (only adapter chunks use it)
             bool ok = true;
             for (long long tile = blockIdx.x; tile < p.n_tiles && ok; tile += gridDim.x, ++accq) {
+                const int *list = nullptr;
+                int count = 0;
+                if constexpr (AD) {
+                    list = ad.lists + tile / p.passes / p.n_g * ad.list_stride;
+                    count = list[0];
+                }
                 const int buf = (int)(accq % p.nbuf);
                 ok = mbar_wait(&acc_empty[buf], ((accq / p.nbuf) & 1) ^ 1, abort_flag, p.status, wait_ns);
                 if (!ok) break;
@@ -342,6 +389,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(&v_empty[vs]);
                     mma_commit(&x_empty[xs]);
                 }
+                if constexpr (AD) {
+                    for (int q = 0; q < count && ok; ++q) {
+                        const int4 m = *reinterpret_cast<const int4 *>(list + 8 + 8 * q + 4);
+                        const uint32_t off[4] = {(uint32_t)m.x, (uint32_t)m.y, (uint32_t)m.z, (uint32_t)m.w};
+                        for (int r0 = 0; r0 < ad.R && ok; r0 += CTJ, ++xq) {
+                            const int xs = xq % S;
+                            const uint32_t par = DLS == 1 ? (ad_phase >> xs) & 1 : (xq / S) & 1;
+                            ok = mbar_wait(&a_ready[xs], par, abort_flag, p.status, wait_ns);
+                            if (!ok) break;
+                            ad_phase ^= 1u << xs;
+                            const int vs = vq % VS;
+                            ok = mbar_wait(&v_full[vs], (vq / VS) & 1, abort_flag, p.status, wait_ns);
+                            ++vq;
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t stage = su32(sR) + xs * SB;
+                            const uint32_t vstage = su32(sV) + vs * p.v_stage_bytes;
+                            const int steps = (min(CTJ, ad.R - r0) + KJ - 1) / KJ;
+                            for (int sl = 0; sl < steps; ++sl) {
+                                const uint64_t adsc = DLS == 1    ? smem_desc_sw128(stage + sl * 32, 1024)
+                                                      : DLS == 16 ? smem_desc(stage, 128, kG16)
+                                                                  : smem_desc(stage + sl * 2 * OS, OS, GS);
+#pragma unroll
+                                for (int l = 0; l < DLS; ++l) {
+                                    const uint32_t b_addr = vstage + l * (p.bp * CTJ * ES) + sl * 32;
+                                    const uint64_t bd = smem_desc_sw(b_addr, 8 * CTJ * ES, v_layout(DLS, ES));
+                                    mma_bf16_lanes(d_base + l * p.bp, adsc, bd, idesc, off);
+                                }
+                            }
+                            mma_commit(&v_empty[vs]);
+                            mma_commit(&x_empty[xs]);
+                        }
+                    }
+                }
                 if (ok) mma_commit(&acc_full[buf]);
             }
             // every MMA this thread issued has finished before TMEM is freed
@@ -350,6 +431,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kEpiWarp0) {
         // ------------------------------------------------ in-place transpose (DLS > 1)
+        // Adapter chunks of a tile: the 128 rows' H, CTJ ranks at a time, into the
+        // ring slot, as the K-major tile (DLS == 1) or as plane 0 of the transposed
+        // chunks (a task is 8 rows x 8 ranks).  Ranks past R and rows past N are
+        // zeros.  The loads are issued before the slot is waited for.
+        auto adapter_chunks = [&](long long tile, uint32_t &xq) -> bool {
+            if constexpr (AD) {
+                const int t = threadIdx.x - kLoadWarp0 * 32;  // 0..127
+                const long long rb = tile / p.passes / p.n_g;
+                const int count = ad.lists[rb * ad.list_stride];
+                const int octet = DLS == 1 ? 0 : t >> 4, g = DLS == 1 ? 0 : t & 15;
+                const bool task = DLS == 1 || octet < CTJ / 8;
+                for (int q = 0; q < count; ++q) {
+                    for (int r0 = 0; r0 < ad.R; r0 += CTJ, ++xq) {
+                        uint4 in[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            // DLS == 1: row t, ranks r0 + 8 e ..; else row 8 g + e, ranks r0 + 8 octet ..
+                            const long long n = rb * kRows + (DLS == 1 ? t : 8 * g + e);
+                            const int r = r0 + 8 * (DLS == 1 ? e : octet);
+                            in[e] = make_uint4(0u, 0u, 0u, 0u);
+                            if (task && n < p.N && r < ad.R)
+                                in[e] = *reinterpret_cast<const uint4 *>(ad.H + n * ad.ldh + r);
+                        }
+                        const int xs = xq % S;
+                        const bool w = mbar_wait(&x_full[xs], (xq / S) & 1, abort_flag, p.status, wait_ns);
+                        if (!bar_and(1, 128, w)) return false;
+                        uint8_t *st = sR + xs * SB;
+                        if constexpr (DLS == 1) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4 *>(st + t * 128 + ((e ^ (t & 7)) << 4)) = in[e];
+                        } else if (task) {
+                            uint4 out[8];
+                            transpose8x8_b16(in, out);
+                            uint8_t *base = DLS == 16 ? st + g * kG16 + octet * 128 : st + octet * OS + g * GS;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(base + e * 16) = out[e];
+                        }
+                        fence_proxy_async();
+                        mbar_arrive(&a_ready[xs]);
+                    }
+                }
+            }
+            return true;
+        };
+        if constexpr (DLS == 1 && AD) {
+            uint32_t xq = 0;
+            bool ok = true;
+            for (long long tile = blockIdx.x; tile < p.n_tiles && ok; tile += gridDim.x) {
+                xq += n_chunks;  // the TMA tiles are the operands
+                ok = adapter_chunks(tile, xq);
+            }
+        }
         if constexpr (DLS == 16) {
             // bf16, 16 l: raw row = 32 units of 16 bytes, unit q = (j = q / 2,
             // l half q % 2).  Warp tw takes row groups tw, tw + 4, tw + 8, tw + 12;
@@ -388,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async();
                     mbar_arrive(&a_ready[xs]);
                 }
+                if (ok) ok = adapter_chunks(tile, xq);
             }
         } else if (DLS > 1 && ES == 2) {
             const int t = threadIdx.x - kLoadWarp0 * 32;  // 0..127
@@ -442,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async();
                     mbar_arrive(&a_ready[xs]);
                 }
+                if (ok) ok = adapter_chunks(tile, xq);
             }
         } else if (DLS > 1) {
             // fp32: per l a K-major plane of 32-byte rows (8 j) with the 32-byte
@@ -905,6 +1041,12 @@ bool tc_supported(const Problem &p, const char **why) {
     return true;
 }
 
+// ranks in 16-byte units (W's strides and H's loads), W aligned, map coordinates in range
+bool tc_adapters_supported(const Problem &p, const TcAdapters &q) {
+    return p.dtype == KS_BF16 && q.R % 8 == 0 && reinterpret_cast<uintptr_t>(q.W) % 16 == 0 &&
+           p.a * q.S < (1LL << 31) && p.b * p.d * q.R * 2 < (1LL << 40);
+}
+
 template <int DLS, typename T>
 static cudaError_t launch_dls(const Problem &pr, const TcConfig &cfg) {
     constexpr int ES = (int)sizeof(T);
@@ -1023,13 +1165,45 @@ static cudaError_t launch_dls(const Problem &pr, const TcConfig &cfg) {
     p.off_bar = L.off_bar;
     p.v_stage_bytes = L.v_stage_bytes;
     const bool ep = pr.bias || pr.act;
+    const long long grid = std::min<long long>(p.n_tiles, (long long)sm_count());
+    if constexpr (ES == 2) {
+        if (pr.ad) {
+            // W[s] (out_f x R, ranks contiguous) viewed as (rank, k, l, i + a * s): a box
+            // (CTJ ranks, bp k, DLS l) lands like the values of CTJ j; ranks past R are
+            // filled with zeros.  Always with the epilogue: without a bias and an
+            // activation it measured the same as the kernel that leaves it out.
+            const TcAdapters &q = *pr.ad;
+            TcAd<true> ad;
+            cuuint64_t dims[4] = {(cuuint64_t)q.R, (cuuint64_t)pr.b, (cuuint64_t)pr.d, (cuuint64_t)(pr.a * q.S)};
+            cuuint64_t strides[3] = {(cuuint64_t)pr.d * q.R * ES, (cuuint64_t)q.R * ES,
+                                     (cuuint64_t)pr.b * pr.d * q.R * ES};
+            cuuint32_t box[4] = {(cuuint32_t)chunk_j(DLS, ES), (cuuint32_t)bp, (cuuint32_t)DLS, 1};
+            const int rb = v_row_bytes(DLS, ES);
+            r = encode(&ad.wmap, kType, 4, const_cast<void *>(q.W), dims, strides, box, estr,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       rb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                       : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : CU_TENSOR_MAP_SWIZZLE_32B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+            if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+            ad.H = static_cast<const uint16_t *>(q.H);
+            ad.lists = q.lists;
+            ad.R = q.R, ad.ldh = q.ldh, ad.list_stride = q.list_stride;
+            auto kern = tc_kernel<DLS, T, true, false, true>;
+            if constexpr (kY4)
+                if (y4d) kern = tc_kernel<DLS, T, true, true, true>;
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+            if (e != cudaSuccess) return e;
+            kern<<<(int)grid, kThreads, L.total, pr.stream>>>(xmap, vmap, ymap, p, ad);
+            return cudaGetLastError();
+        }
+    }
     auto kern = ep ? tc_kernel<DLS, T, true> : tc_kernel<DLS, T, false>;
     if constexpr (kY4)
         if (y4d) kern = ep ? tc_kernel<DLS, T, true, true> : tc_kernel<DLS, T, false, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
     if (e != cudaSuccess) return e;
-    const long long grid = std::min<long long>(p.n_tiles, (long long)sm_count());
-    kern<<<(int)grid, kThreads, L.total, pr.stream>>>(xmap, vmap, ymap, p);
+    kern<<<(int)grid, kThreads, L.total, pr.stream>>>(xmap, vmap, ymap, p, TcAd<false>{});
     return cudaGetLastError();
 }
 

@@ -223,6 +223,36 @@ def test_unused_weights_may_hold_anything(dtype):
         assert torch.equal(da[0], da2[0]) and torch.isfinite(db2).all() and (da2[1:] == 0).all()
 
 
+@pytest.mark.parametrize("p", [(1, 64, 48, 8), (1, 96, 80, 1), (2, 64, 32, 2), (1, 64, 64, 64), (3, 20, 12, 5)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_broken_adapter_harms_its_own_rows_only(p, dtype):
+    """Infinities and NaN in one adapter's weights or scale, in a tile that it shares."""
+    for n in (6, 200):
+        q = make(p, n, 3, 16, dtype, "rows", 13)
+        q["ids"][0] = 1
+        args = (q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"])
+        clean, (dx, da, db) = call(q, p), ks.adapter_backward(*args)
+        other = q["ids"] != 1
+        for name, value in (("A", float("inf")), ("B", float("nan")), ("scales", float("inf"))):
+            kept = q[name].clone()
+            q[name][1] = value
+            y, (dx2, da2, db2) = call(q, p), ks.adapter_backward(*args)
+            assert torch.equal(y[other], clean[other]) and torch.equal(dx2[other], dx[other])
+            assert torch.equal(da2[::2], da[::2]) and torch.equal(db2[::2], db[::2])
+            assert not torch.isfinite(y[0]).all()
+            q[name].copy_(kept)
+
+
+def test_without_ids_every_row_takes_the_first_adapter():
+    for dtype in (torch.float32, torch.bfloat16):
+        for p in ((1, 64, 48, 8), (1, 7, 9, 1)):
+            q = make(p, 140, 3, 8, dtype, "one", 4)
+            zero = dict(q, ids=torch.zeros(140, dtype=torch.int32, device=DEV))
+            assert_forward(call(q, p), zero, p)
+            assert_backward(zero, p, ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], None,
+                                                         q["scales"]))
+
+
 def test_scales_default_to_one_and_out_is_filled():
     p = (1, 64, 48, 8)
     q = make(p, 20, 2, 8, torch.float32, "rows", 2)
