@@ -1,4 +1,5 @@
-"""Builds the KS CUDA library in-tree: kronecker_sparse_matrix_b200/libks_b200.so.
+"""Builds the KS CUDA library in-tree: kronecker_sparse_matrix_b200/libks_b200.so,
+and the host-side module that reads tensor lists for it, _ks_marshal.so.
 
 Every kernel is compiled for sm_100a only
 (``-gencode arch=compute_100a,code=sm_100a``) with nvcc; objects go to
@@ -9,10 +10,12 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libks_b200.so")
+MARSHAL_SRC = os.path.join(CSRC, "ks_marshal.cpp")
+MARSHAL = os.path.join(PKG, "_ks_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -58,8 +63,24 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
     return (r.stdout + r.stderr).strip()
 
 
+def build_marshal(force: bool = False) -> str:
+    """The CPython module that reads tensor lists (host code only)."""
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SRC):
+        return MARSHAL
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-o", tmp, MARSHAL_SRC,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch, "include")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on ks_marshal.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    build_marshal(force)
     hdr_time = _newest(headers())
     jobs = []
     objs = []

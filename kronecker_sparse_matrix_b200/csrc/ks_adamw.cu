@@ -16,17 +16,16 @@
 // The step needs p, g, m and v read and p, m and v written once: 28 bytes per
 // fp32 element with fp32 states, 10.06 bytes per bf16 element with 8-bit ones.
 //
-// One block of 256 threads takes 2048 consecutive elements of one tensor, a warp
-// 256 of them (one scale's worth), a lane eight.  The tensors of a launch and
-// the prefix sums of their blocks travel in the kernel's parameters, so a step
+// One block of 256 threads takes 2048 consecutive elements of one tensor at a time,
+// a warp 256 of them (one scale's worth), a lane eight.  The tensors of a launch
+// and the prefix sums of their blocks travel in the kernel's parameters, so a step
 // over many tensors is one launch, with no table to copy to the device; a block
-// finds its tensor by bisection.
+// finds its tensor by bisection.  Arithmetic runs on pairs (fp32x2).
 //
 // Roundings: m and v are each two products and a sum, every one rounded to
-// nearest (not contracted into FMAs: the 8-bit codes then do not depend on how
-// a compiler contracts), and the square root is correctly rounded, so a state's
-// code is a function of its inputs alone.  The quotient of the update uses the
-// fast division (2 ulp), far inside the rounding of p.
+// nearest.  The square root of an 8-bit state and the reciprocal in the update are the
+// hardware's approximations (a few units in the last place of fp32), far inside
+// half a step of e4m3 and the rounding of p.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -43,7 +42,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;                  // elements of a scale: one warp's
-constexpr int kChunk = kThreads / 32 * kBlock;  // elements of a thread block
+constexpr int kChunk = kThreads / 32 * kBlock;  // elements that a thread block takes at a time
 constexpr float kTop = 448.f;                // largest e4m3 number
 constexpr float kLow = 0.001953125f;         // 2^-9, the smallest positive one
 constexpr float kNone = 7.888609052210118e-31f;  // 2^-100
@@ -69,7 +68,7 @@ struct Table {
     long long n[NT];
     int first[NT + 1];  // first thread block of each tensor
     unsigned char aligned[NT];
-    int count;
+    int count, iters;
 };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -168,14 +167,25 @@ __device__ __forceinline__ void store8(S *d, const float (&v)[8], bool vec, int 
 }
 
 // Largest magnitude of the warp's 256 elements (NaN elements do not count:
-// each keeps its own NaN code), zero below 2^-100.
+// each keeps its own NaN code), zero below 2^-100.  The bits of floats that are
+// not negative are ordered like the floats.
 __device__ __forceinline__ float warp_top(const float (&v)[8]) {
     float t = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) t = fmaxf(t, fabsf(v[e]));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+    t = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(t)));
     return t < kNone ? 0.f : t;
+}
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // T: type of p and g; S: type of the states (float, or unsigned char: e4m3).
@@ -192,30 +202,6 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
             hi = mid;
     }
     const int lane = threadIdx.x & 31;
-    const long long unit = (long long)(block - t.first[lo]) * (kThreads / 32) + (threadIdx.x >> 5);
-    const long long at = unit * kBlock;
-    const long long left = t.n[lo] - at;
-    if (left <= 0) return;
-    const bool vec = t.aligned[lo] && left >= kBlock;
-    T *p = static_cast<T *>(t.p[lo]) + at;
-    const T *g = static_cast<const T *>(t.g[lo]) + at;
-    S *m = static_cast<S *>(t.m[lo]) + at;
-    S *v = static_cast<S *>(t.v[lo]) + at;
-    float *w = MASTER ? t.master[lo] + at : nullptr;
-
-    float pe[8], ge[8], me[8], ve[8];
-    load8(g, ge, vec, lane, left);
-    load8(m, me, vec, lane, left);
-    load8(v, ve, vec, lane, left);
-    if constexpr (MASTER)
-        load8(w, pe, vec, lane, left);
-    else
-        load8(p, pe, vec, lane, left);
-    float m_scale = 1.f, v_scale = 1.f;
-    if constexpr (S8) {
-        m_scale = t.ms[lo][unit];
-        v_scale = t.vs[lo][unit];
-    }
     float lr = h.lr, bc1 = h.bc1, ib2 = h.inv_root_bc2;
     if (h.lr_dev) lr = *h.lr_dev;
     if (h.step) {
@@ -224,50 +210,89 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         ib2 = rsqrtf(-expm1f((float)(s * h.log_beta2)));
     }
     const float gs = h.grad_scale ? *h.grad_scale : 1.f;
-    const float keep = 1.f - lr * h.wd, rate = lr / bc1;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float gr = ge[e] * gs;
-        float m0 = me[e], v0 = ve[e];
+    const float2 keep = make_float2(1.f - lr * h.wd, 1.f - lr * h.wd), rate = make_float2(-lr / bc1, -lr / bc1);
+    const float2 b1 = make_float2(h.beta1, h.beta1), o1 = make_float2(h.omb1, h.omb1);
+    const float2 b2 = make_float2(h.beta2, h.beta2), o2 = make_float2(h.omb2, h.omb2);
+    const float2 gs2 = make_float2(gs, gs), ib = make_float2(ib2, ib2), eps = make_float2(h.eps, h.eps);
+    const long long n = t.n[lo];
+    const bool vectors = t.aligned[lo];
+    long long unit = (long long)(block - t.first[lo]) * (kThreads / 32 * t.iters) + (threadIdx.x >> 5);
+    for (int it = 0; it < t.iters; ++it, unit += kThreads / 32) {
+        const long long at = unit * kBlock;
+        const long long left = n - at;
+        if (left <= 0) return;
+        const bool vec = vectors && left >= kBlock;
+        T *p = static_cast<T *>(t.p[lo]) + at;
+        const T *g = static_cast<const T *>(t.g[lo]) + at;
+        S *m = static_cast<S *>(t.m[lo]) + at;
+        S *v = static_cast<S *>(t.v[lo]) + at;
+        float *w = MASTER ? t.master[lo] + at : nullptr;
+
+        float pe[8], ge[8], me[8], ve[8];
+        load8(g, ge, vec, lane, left);
+        load8(m, me, vec, lane, left);
+        load8(v, ve, vec, lane, left);
+        if constexpr (MASTER)
+            load8(w, pe, vec, lane, left);
+        else
+            load8(p, pe, vec, lane, left);
+        float2 m_scale, v_scale;
         if constexpr (S8) {
-            m0 = __fmul_rn(m0, m_scale);
-            v0 = __fmul_rn(v0, v_scale);
-            v0 = __fmul_rn(v0, v0);
+            m_scale.x = m_scale.y = t.ms[lo][unit];
+            v_scale.x = v_scale.y = t.vs[lo][unit];
         }
-        const float m1 = __fadd_rn(__fmul_rn(m0, h.beta1), __fmul_rn(gr, h.omb1));
-        const float v1 = __fadd_rn(__fmul_rn(v0, h.beta2), __fmul_rn(__fmul_rn(gr, gr), h.omb2));
-        const float root = __fsqrt_rn(v1);
-        pe[e] = fmaf(-rate, __fdividef(m1, fmaf(root, ib2, h.eps)), pe[e] * keep);
-        me[e] = m1;
-        ve[e] = S8 ? root : v1;
-    }
-    if constexpr (MASTER) store8(w, pe, vec, lane, left);
-    store8(p, pe, vec, lane, left);
-    if constexpr (S8) {
-        const float m_top = warp_top(me), v_top = warp_top(ve);
-        const float m_inv = m_top == 0.f ? 0.f : __fdiv_rn(kTop, m_top);
-        const float v_inv = v_top == 0.f ? 0.f : __fdiv_rn(kTop, v_top);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            me[e] = __fmul_rn(me[e], m_inv);
-            const float y = __fmul_rn(ve[e], v_inv);
-            ve[e] = ve[e] > 0.f && y < kLow ? kLow : y;
+        for (int e = 0; e < 8; e += 2) {
+            const float2 gr = __fmul2_rn(make_float2(ge[e], ge[e + 1]), gs2);
+            float2 m0 = make_float2(me[e], me[e + 1]), v0 = make_float2(ve[e], ve[e + 1]);
+            if constexpr (S8) {
+                m0 = __fmul2_rn(m0, m_scale);
+                v0 = __fmul2_rn(v0, v_scale);
+                v0 = __fmul2_rn(v0, v0);
+            }
+            const float2 m1 = __fadd2_rn(__fmul2_rn(m0, b1), __fmul2_rn(gr, o1));
+            const float2 v1 = __fadd2_rn(__fmul2_rn(v0, b2), __fmul2_rn(__fmul2_rn(gr, gr), o2));
+            float2 root;
+            if constexpr (S8)
+                root = make_float2(sqrt_approx(v1.x), sqrt_approx(v1.y));
+            else
+                root = make_float2(__fsqrt_rn(v1.x), __fsqrt_rn(v1.y));
+            const float2 den = __ffma2_rn(root, ib, eps);
+            const float2 change = __fmul2_rn(m1, make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+            const float2 p1 = __ffma2_rn(rate, change, __fmul2_rn(make_float2(pe[e], pe[e + 1]), keep));
+            pe[e] = p1.x, pe[e + 1] = p1.y;
+            me[e] = m1.x, me[e + 1] = m1.y;
+            ve[e] = S8 ? root.x : v1.x, ve[e + 1] = S8 ? root.y : v1.y;
         }
-        if (lane == 0) {
-            t.ms[lo][unit] = __fdiv_rn(m_top, kTop);
-            t.vs[lo][unit] = __fdiv_rn(v_top, kTop);
+        if constexpr (MASTER) store8(w, pe, vec, lane, left);
+        store8(p, pe, vec, lane, left);
+        if constexpr (S8) {
+            const float m_top = warp_top(me), v_top = warp_top(ve);
+            const float m_inv = m_top == 0.f ? 0.f : __fdividef(kTop, m_top);
+            const float v_inv = v_top == 0.f ? 0.f : __fdividef(kTop, v_top);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                me[e] *= m_inv;
+                const float y = ve[e] * v_inv;
+                ve[e] = ve[e] > 0.f ? fmaxf(y, kLow) : y;
+            }
+            if (lane == 0) {
+                t.ms[lo][unit] = m_top * (1.f / kTop);
+                t.vs[lo][unit] = v_top * (1.f / kTop);
+            }
         }
+        store8(m, me, vec, lane, left);
+        store8(v, ve, vec, lane, left);
     }
-    store8(m, me, vec, lane, left);
-    store8(v, ve, vec, lane, left);
 }
 
 bool is_aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 template <typename T, typename S, bool MASTER, int NT>
-cudaError_t launch_table(const ks_adamw_tensor *ts, int count, const Hyper &h, cudaStream_t st) {
+cudaError_t launch_table(const ks_adamw_tensor *ts, int count, int iters, const Hyper &h, cudaStream_t st) {
     Table<NT> t;
     t.count = count;
+    t.iters = iters;
     long long blocks = 0;
     for (int k = 0; k < count; ++k) {
         const ks_adamw_tensor &q = ts[k];
@@ -277,7 +302,7 @@ cudaError_t launch_table(const ks_adamw_tensor *ts, int count, const Hyper &h, c
         // eight elements of a lane as 16-byte (fp32: two) or 8-byte (e4m3) vectors
         t.aligned[k] = is_aligned(q.param, 16) && is_aligned(q.grad, 16) && is_aligned(q.exp_avg, 16) &&
                        is_aligned(q.exp_avg_sq, 16) && is_aligned(q.master, 16);
-        blocks += (q.n + kChunk - 1) / kChunk;
+        blocks += (q.n + (long long)kChunk * iters - 1) / ((long long)kChunk * iters);
     }
     t.first[count] = (int)blocks;
     adamw_kernel<T, S, MASTER, NT><<<(unsigned)blocks, kThreads, 0, st>>>(t, h);
@@ -302,8 +327,11 @@ cudaError_t launch_all(const std::vector<ks_adamw_tensor> &ts, const Hyper &h, c
             ++e;
         }
         const int count = (int)(e - k);
-        const cudaError_t err = count <= kFew ? launch_table<T, S, MASTER, kFew>(&ts[k], count, h, st)
-                                              : launch_table<T, S, MASTER, kMany>(&ts[k], count, h, st);
+        // four passes of a block where that leaves eight blocks and more for each SM:
+        // finding the tensor and the step's numbers are then paid once for four
+        const int iters = blocks >= 32LL * sm_count() ? 4 : 1;
+        const cudaError_t err = count <= kFew ? launch_table<T, S, MASTER, kFew>(&ts[k], count, iters, h, st)
+                                              : launch_table<T, S, MASTER, kMany>(&ts[k], count, iters, h, st);
         if (err != cudaSuccess) return err;
         k = e;
     }

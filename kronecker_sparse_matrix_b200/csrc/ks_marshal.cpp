@@ -1,0 +1,178 @@
+// Reads lists of torch tensors into the table of ks_adamw_step, for the Python
+// binding: type, device, contiguity, element count and address of each tensor
+// through the DLPack exchange functions that torch.Tensor publishes
+// (__dlpack_c_exchange_api__), so that no torch type is needed here.  The same
+// checks as attribute reads from Python take 18 us for a list of 60 tensors, an
+// order of magnitude more than here, and a step has up to seven lists.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/dlpack.h>
+
+#include <cstdint>
+#include <cstring>
+
+namespace {
+
+const DLPackExchangeAPI *g_api = nullptr;
+PyTypeObject *g_tensor = nullptr;
+
+// Type codes of the table: what ks_dtype and state_bits are chosen by.
+enum Kind { kNone = -1, kF32 = 0, kBF16 = 1, kE4M3 = 2 };
+
+int kind_of(const DLDataType &t) {
+    if (t.lanes != 1) return kNone;
+    if (t.code == kDLFloat && t.bits == 32) return kF32;
+    if (t.code == kDLBfloat && t.bits == 16) return kBF16;
+    if (t.code == kDLFloat8_e4m3fn && t.bits == 8) return kE4M3;
+    return kNone;
+}
+
+const char *kind_name(int k) {
+    return k == kF32 ? "torch.float32" : k == kBF16 ? "torch.bfloat16" : k == kE4M3 ? "torch.float8_e4m3fn" : "other";
+}
+
+struct Info {
+    uint64_t ptr;
+    int64_t numel;
+    int kind, device;  // device: CUDA index, or -1
+    bool contiguous;
+};
+
+bool read(PyObject *o, Info *out) {
+    if (!PyObject_TypeCheck(o, g_tensor)) {
+        PyErr_SetString(PyExc_TypeError, "expected torch tensors");
+        return false;
+    }
+    DLTensor t;
+    if (g_api->dltensor_from_py_object_no_sync(o, &t) != 0) return false;
+    out->ptr = (uint64_t)(uintptr_t)t.data + t.byte_offset;
+    out->kind = kind_of(t.dtype);
+    out->device = t.device.device_type == kDLCUDA ? t.device.device_id : -1;
+    int64_t n = 1;
+    bool c = true;
+    for (int d = t.ndim - 1; d >= 0; --d) {
+        if (t.strides && t.shape[d] > 1 && t.strides[d] != n) c = false;
+        n *= t.shape[d];
+    }
+    out->numel = n;
+    out->contiguous = c || n == 0;
+    return true;
+}
+
+const char *const kNames[7] = {"params", "grads", "exp_avgs", "exp_avg_sqs", "masters", "exp_avg_scales",
+                               "exp_avg_sq_scales"};
+constexpr int64_t kBlock = 256;  // elements that share a scale in an 8-bit state
+
+// adamw_table(params, grads, exp_avgs, exp_avg_sqs, masters, exp_avg_scales, exp_avg_sq_scales)
+//   -> (table, tensors, dtype kind, state kind, device index)
+// Lists of equal lengths; the last three may be None.
+PyObject *adamw_table(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    if (nargs != 7) return PyErr_Format(PyExc_TypeError, "adamw_table takes 7 lists");
+    PyObject *list[7] = {}, *table = nullptr, *result = nullptr;
+    Py_ssize_t count = 0;
+    int dtype = kNone, state = kNone, device = -1;
+    uint64_t *words = nullptr;
+    for (int c = 0; c < 7; ++c) {
+        if (args[c] == Py_None && c >= 4) continue;
+        list[c] = PySequence_Fast(args[c], "expected lists of tensors");
+        if (!list[c]) goto done;
+        if (c == 0) {
+            count = PySequence_Fast_GET_SIZE(list[0]);
+        } else if (PySequence_Fast_GET_SIZE(list[c]) != count) {
+            PyErr_Format(PyExc_ValueError, "%s must have one tensor for each parameter", kNames[c]);
+            goto done;
+        }
+    }
+    table = PyBytes_FromStringAndSize(nullptr, count * 64);  // ks_adamw_tensor: eight 64-bit words
+    if (!table) goto done;
+    words = reinterpret_cast<uint64_t *>(PyBytes_AS_STRING(table));
+    memset(words, 0, (size_t)count * 64);
+    for (int c = 0; c < 7; ++c) {
+        if (!list[c]) continue;
+        PyObject **items = PySequence_Fast_ITEMS(list[c]);
+        for (Py_ssize_t k = 0; k < count; ++k) {
+            Info t;
+            if (!read(items[k], &t)) goto done;
+            if (c == 0 && k == 0) {
+                dtype = t.kind;
+                device = t.device;
+                if (dtype != kF32 && dtype != kBF16) {
+                    PyErr_SetString(PyExc_TypeError, "unsupported dtype of params: use float32 or bfloat16");
+                    goto done;
+                }
+                if (device < 0) {
+                    PyErr_SetString(PyExc_ValueError, "params must be CUDA tensors");
+                    goto done;
+                }
+            }
+            if (c == 2 && k == 0) {
+                state = t.kind;
+                if (state != kF32 && state != kE4M3) {
+                    PyErr_SetString(PyExc_TypeError, "unsupported dtype of exp_avgs: use float32 or float8_e4m3fn");
+                    goto done;
+                }
+            }
+            const int want = c < 2 ? dtype : c < 4 ? state : kF32;
+            if (t.kind != want || t.device != device) {
+                PyErr_Format(PyExc_ValueError, "%s must be %s tensors on cuda:%d", kNames[c], kind_name(want), device);
+                goto done;
+            }
+            if (!t.contiguous) {
+                PyErr_Format(PyExc_ValueError, "%s must be contiguous", kNames[c]);
+                goto done;
+            }
+            if (c == 0) {
+                words[8 * k + 7] = (uint64_t)t.numel;
+            } else {
+                const int64_t n = (int64_t)words[8 * k + 7];
+                if (t.numel != (c < 5 ? n : (n + kBlock - 1) / kBlock)) {
+                    PyErr_Format(PyExc_ValueError,
+                                 "%s must have the parameters' element counts (scales: one for each 256)", kNames[c]);
+                    goto done;
+                }
+            }
+            words[8 * k + c] = t.ptr;
+        }
+    }
+    result = Py_BuildValue("Oniii", table, count, dtype, state, device);
+done:
+    Py_XDECREF(table);
+    for (PyObject *l : list) Py_XDECREF(l);
+    return result;
+}
+
+PyMethodDef kMethods[] = {
+    {"adamw_table", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adamw_table)), METH_FASTCALL,
+     "The table of ks_adamw_step from lists of tensors."},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ks_marshal", nullptr, -1, kMethods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__ks_marshal(void) {
+    PyObject *torch = PyImport_ImportModule("torch");
+    if (!torch) return nullptr;
+    PyObject *type = PyObject_GetAttrString(torch, "Tensor");
+    Py_DECREF(torch);
+    if (!type) return nullptr;
+    PyObject *capsule = PyObject_GetAttrString(type, "__dlpack_c_exchange_api__");
+    if (!capsule) {
+        Py_DECREF(type);
+        return nullptr;
+    }
+    const auto *api = static_cast<const DLPackExchangeAPI *>(PyCapsule_GetPointer(capsule, "dlpack_exchange_api"));
+    Py_DECREF(capsule);
+    if (api && (api->header.version.major != DLPACK_MAJOR_VERSION || !api->dltensor_from_py_object_no_sync)) {
+        PyErr_SetString(PyExc_ImportError, "torch's DLPack exchange functions have another version than this build");
+        api = nullptr;
+    }
+    if (!api) {
+        Py_DECREF(type);
+        return nullptr;
+    }
+    g_api = api;
+    g_tensor = reinterpret_cast<PyTypeObject *>(type);  // kept
+    return PyModule_Create(&kModule);
+}

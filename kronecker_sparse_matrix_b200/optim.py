@@ -2,10 +2,8 @@
 optimizer class ``AdamW`` built on it, with states in 32 bits or in 8 bits."""
 from __future__ import annotations
 
-import array
 import ctypes
-from itertools import chain, repeat
-from operator import attrgetter
+from itertools import chain
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
@@ -14,27 +12,15 @@ from . import KS_BF16, KS_F32, _lib, _stream_ptr
 
 ADAMW_BLOCK = 256  # elements that share a scale in an 8-bit state
 
-_dtype, _device = attrgetter("dtype"), attrgetter("device")
-_ptr, _numel, _contiguous = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
 
-
-def _pointers(name: str, tensors, count: int, dtype: torch.dtype, device: torch.device, numels=None):
-    """The tensors' addresses, after checking them."""
-    if len(tensors) != count:
-        raise ValueError(f"{name} must have one tensor for each parameter")
-    if set(map(_dtype, tensors)) != {dtype} or set(map(_device, tensors)) != {device}:
-        raise ValueError(f"{name} must be {dtype} tensors on {device}")
-    if not all(map(_contiguous, tensors)):
-        raise ValueError(f"{name} must be contiguous")
-    if numels is not None and list(map(_numel, tensors)) != numels:
-        raise ValueError(f"{name} must have the parameters' element counts (scales: one for each {ADAMW_BLOCK})")
-    return map(_ptr, tensors)
-
-
-def _scalar(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch.device) -> int:
-    if t.dtype != dtype or t.device != device or t.numel() != 1:
-        raise ValueError(f"{name} as a tensor must hold one {dtype} on {device}")
+def _scalar(name: str, t: torch.Tensor, dtype: torch.dtype, device: int) -> int:
+    if t.dtype != dtype or t.get_device() != device or t.numel() != 1:
+        raise ValueError(f"{name} as a tensor must hold one {dtype} on cuda:{device}")
     return t.data_ptr()
+
+
+def _run(device: int, opt, args, stream: Optional[torch.cuda.Stream]) -> int:
+    return _lib.load().ks_adamw_step(*args, ctypes.byref(opt), _stream_ptr(stream, torch.device("cuda", device)))
 
 
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor],
@@ -54,35 +40,16 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     ``masters``: fp32 masters of bf16 parameters.  step counts from 1.  step (int64), lr and
     grad_scale (float32) may be one-element CUDA tensors, read when the step
     runs: a captured step follows them.  Asynchronous on ``stream``."""
-    count = len(params)
-    if count == 0:
+    if len(params) == 0:
         return
-    dt, dev = params[0].dtype, params[0].device
-    if dt not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"unsupported dtype {dt}: use float32 or bfloat16")
-    if dev.type != "cuda":
-        raise ValueError("params must be CUDA tensors")
-    numels = list(map(_numel, params))
-    if len(exp_avgs) != count:
-        raise ValueError("exp_avgs must have one tensor for each parameter")
-    state = exp_avgs[0].dtype
-    if state not in (torch.float32, torch.float8_e4m3fn):
-        raise TypeError(f"unsupported state dtype {state}: use float32 or float8_e4m3fn")
-    bits = 8 if state is torch.float8_e4m3fn else 32
-    if (bits == 8) != (exp_avg_scales is not None) or (bits == 8) != (exp_avg_sq_scales is not None):
+    if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
+        raise ValueError("exp_avg_scales and exp_avg_sq_scales come together")
+    from ._ks_marshal import adamw_table  # built with the library
+    table, count, dtype, state, dev = adamw_table(params, grads, exp_avgs, exp_avg_sqs, masters, exp_avg_scales,
+                                                  exp_avg_sq_scales)
+    bits = 8 if state == 2 else 32  # kinds: 0 float32, 1 bfloat16, 2 float8_e4m3fn
+    if (bits == 8) != (exp_avg_scales is not None):
         raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales, 32-bit states take none")
-    none = repeat(0, count)
-    columns = [_pointers("params", params, count, dt, dev), _pointers("grads", grads, count, dt, dev, numels),
-               _pointers("exp_avgs", exp_avgs, count, state, dev, numels),
-               _pointers("exp_avg_sqs", exp_avg_sqs, count, state, dev, numels),
-               none if masters is None else _pointers("masters", masters, count, torch.float32, dev, numels)]
-    if bits == 8:
-        blocks = [(n + ADAMW_BLOCK - 1) // ADAMW_BLOCK for n in numels]
-        columns += [_pointers("exp_avg_scales", exp_avg_scales, count, torch.float32, dev, blocks),
-                    _pointers("exp_avg_sq_scales", exp_avg_sq_scales, count, torch.float32, dev, blocks)]
-    else:
-        columns += [repeat(0, count), repeat(0, count)]
-    table = array.array("Q", chain.from_iterable(zip(*columns, numels)))  # ks_adamw_tensor: eight 64-bit words
     opt = _lib.KsAdamwOptions(0.0, betas[0], betas[1], eps, weight_decay, 1)
     if isinstance(lr, torch.Tensor):
         opt.lr_ptr = _scalar("lr", lr, torch.float32, dev)
@@ -94,9 +61,12 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
         opt.step = step
     if grad_scale is not None:
         opt.grad_scale = _scalar("grad_scale", grad_scale, torch.float32, dev)
-    with torch.cuda.device(dev):
-        st = _lib.load().ks_adamw_step(table.buffer_info()[0], count, KS_F32 if dt is torch.float32 else KS_BF16, bits,
-                                       ctypes.byref(opt), _stream_ptr(stream, dev))
+    args = (table, count, KS_BF16 if dtype == 1 else KS_F32, bits)
+    if torch.cuda.current_device() == dev:
+        st = _run(dev, opt, args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = _run(dev, opt, args, stream)
     _lib.check(st)
 
 
