@@ -43,6 +43,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;                  // elements of a scale: one warp's
 constexpr int kChunk = kThreads / 32 * kBlock;  // elements that a thread block takes at a time
+// units of a warp in a large step (142M bf16 parameters with 8-bit states: 286 us
+// with 4, 276 us with 8; 49M with masters and fp32 states: 218 and 221 us)
+constexpr int kIters8 = 8, kIters32 = 4;
 constexpr float kTop = 448.f;                // largest e4m3 number
 constexpr float kLow = 0.001953125f;         // 2^-9, the smallest positive one
 constexpr float kNone = 7.888609052210118e-31f;  // 2^-100
@@ -216,11 +219,23 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const float2 gs2 = make_float2(gs, gs), ib = make_float2(ib2, ib2), eps = make_float2(h.eps, h.eps);
     const long long n = t.n[lo];
     const bool vectors = t.aligned[lo];
-    long long unit = (long long)(block - t.first[lo]) * (kThreads / 32 * t.iters) + (threadIdx.x >> 5);
-    for (int it = 0; it < t.iters; ++it, unit += kThreads / 32) {
-        const long long at = unit * kBlock;
+    // Units of the block: its warps side by side, iters times over.  Their scales
+    // are read and written as one piece: stores of single scales, 4 bytes of a
+    // sector that other warps are reading, made the step up to 1.5x slower.
+    constexpr int kWarps = kThreads / 32;
+    __shared__ float scales[S8 ? 2 : 1][S8 ? kWarps * kIters8 : 1];
+    const long long unit0 = (long long)(block - t.first[lo]) * (kWarps * t.iters);
+    const int units = (int)min((long long)kWarps * t.iters, (n + kBlock - 1) / kBlock - unit0);
+    if constexpr (S8) {
+        if ((int)threadIdx.x < units) {
+            scales[0][threadIdx.x] = t.ms[lo][unit0 + threadIdx.x];
+            scales[1][threadIdx.x] = t.vs[lo][unit0 + threadIdx.x];
+        }
+        __syncthreads();
+    }
+    for (int u = threadIdx.x >> 5; u < units; u += kWarps) {
+        const long long at = (unit0 + u) * kBlock;
         const long long left = n - at;
-        if (left <= 0) return;
         const bool vec = vectors && left >= kBlock;
         T *p = static_cast<T *>(t.p[lo]) + at;
         const T *g = static_cast<const T *>(t.g[lo]) + at;
@@ -238,8 +253,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
             load8(p, pe, vec, lane, left);
         float2 m_scale, v_scale;
         if constexpr (S8) {
-            m_scale.x = m_scale.y = t.ms[lo][unit];
-            v_scale.x = v_scale.y = t.vs[lo][unit];
+            m_scale.x = m_scale.y = scales[0][u];
+            v_scale.x = v_scale.y = scales[1][u];
         }
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -276,13 +291,20 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 const float y = ve[e] * v_inv;
                 ve[e] = ve[e] > 0.f ? fmaxf(y, kLow) : y;
             }
-            if (lane == 0) {
-                t.ms[lo][unit] = m_top * (1.f / kTop);
-                t.vs[lo][unit] = v_top * (1.f / kTop);
+            if (lane == 0) {  // (the warp's reductions above come after every lane's reads)
+                scales[0][u] = m_top * (1.f / kTop);
+                scales[1][u] = v_top * (1.f / kTop);
             }
         }
         store8(m, me, vec, lane, left);
         store8(v, ve, vec, lane, left);
+    }
+    if constexpr (S8) {
+        __syncthreads();
+        if ((int)threadIdx.x < units) {
+            t.ms[lo][unit0 + threadIdx.x] = scales[0][threadIdx.x];
+            t.vs[lo][unit0 + threadIdx.x] = scales[1][threadIdx.x];
+        }
     }
 }
 
@@ -327,9 +349,10 @@ cudaError_t launch_all(const std::vector<ks_adamw_tensor> &ts, const Hyper &h, c
             ++e;
         }
         const int count = (int)(e - k);
-        // four passes of a block where that leaves eight blocks and more for each SM:
-        // finding the tensor and the step's numbers are then paid once for four
-        const int iters = blocks >= 32LL * sm_count() ? 4 : 1;
+        // several units a warp where that leaves eight blocks and more for each SM:
+        // finding the tensor and the step's numbers are then paid once for them
+        constexpr int many = sizeof(S) == 1 ? kIters8 : kIters32;
+        const int iters = blocks >= 8LL * many * sm_count() ? many : 1;
         const cudaError_t err = count <= kFew ? launch_table<T, S, MASTER, kFew>(&ts[k], count, iters, h, st)
                                               : launch_table<T, S, MASTER, kMany>(&ts[k], count, iters, h, st);
         if (err != cudaSuccess) return err;
