@@ -185,6 +185,7 @@ __device__ void tile_list(const int *__restrict__ ids, int *__restrict__ lists, 
         if (lane == 0) {
             int *e = list + 8 + 8 * count;
             e[0] = last;
+            if (count == 0) list[1] = last;
             *reinterpret_cast<uint4 *>(e + 4) = make_uint4(off[0], off[1], off[2], off[3]);
         }
         ++count;
@@ -200,13 +201,18 @@ __device__ void tile_list(const int *__restrict__ ids, int *__restrict__ lists, 
 // MMA calls its k: lane (g, t) loads the eight features 8 t .. 8 t + 7 of rows g
 // (X, and W) as one 16-byte vector, which is its share of two MMA steps.  The
 // warps' sums meet in shared memory in a fixed order.  Blocks past the rows'
-// build the lists of the tensor-core product that follows.
+// build the lists of the tensor-core product that follows, whose operand planes
+// (TcAdapters::planes) take H instead of, or beside, the rows of H.
+__device__ __forceinline__ unsigned short *plane_at(unsigned short *planes, long long n, int r, int plane_r) {
+    return planes + n / 128 * (plane_r * 128) + (r >> 3) * 1024 + (int)(n % 128 >> 3) * 64 + (r & 7) * 8 + (int)(n & 7);
+}
+
 template <int NT, typename O>
 __global__ void __launch_bounds__(256)
     shrink_mma_kernel(const __nv_bfloat16 *__restrict__ X, const __nv_bfloat16 *__restrict__ W,
                       const float *__restrict__ scales, const int *__restrict__ ids, O *__restrict__ H, long long N,
                       int F, int R, int ldh, int S, unsigned *status, int row_blocks, int *__restrict__ lists,
-                      int list_stride) {
+                      int list_stride, unsigned short *__restrict__ planes, int plane_r) {
     constexpr int MT = 2, ROWS = 16 * MT, RC = 8 * NT, LD = RC + 1;
     __shared__ float red[4][ROWS][LD];
     __shared__ int row_id[ROWS], found[ROWS], n_found;
@@ -232,7 +238,7 @@ __global__ void __launch_bounds__(256)
     const int g = lane >> 2, t = lane & 3;
     for (int q = threadIdx.x; q < ROWS * RC; q += 256) {
         const int m = q / RC, r = r0 + q % RC;
-        if (row_id[m] < 0 && n0 + m < N && r < ldh) put(H + (n0 + m) * ldh + r, 0.f);
+        if (H && row_id[m] < 0 && n0 + m < N && r < ldh) put(H + (n0 + m) * ldh + r, 0.f);
     }
     const uint4 *x[2 * MT];
 #pragma unroll
@@ -290,9 +296,12 @@ __global__ void __launch_bounds__(256)
         const float sc = scales ? scales[s] : 1.f;
         for (int q = threadIdx.x; q < ROWS * RC; q += 256) {
             const int m = q / RC, c = q % RC, r = r0 + c;
-            if (row_id[m] == s && r < ldh)
-                put(H + (n0 + m) * ldh + r,
-                    r < R ? sc * ((red[0][m][c] + red[1][m][c]) + (red[2][m][c] + red[3][m][c])) : 0.f);
+            if (row_id[m] == s) {
+                const float h = r < R ? sc * ((red[0][m][c] + red[1][m][c]) + (red[2][m][c] + red[3][m][c])) : 0.f;
+                if (H && r < ldh) put(H + (n0 + m) * ldh + r, h);
+                if (planes && r < plane_r)
+                    *plane_at(planes, n0 + m, r, plane_r) = __bfloat16_as_ushort(__float2bfloat16_rn(h));
+            }
         }
         __syncthreads();
     }
@@ -739,14 +748,18 @@ int round_up(int x, int m) { return (x + m - 1) / m * m; }
 int list_stride(int S) { return 8 + 8 * std::min(S, 128); }
 long long list_tiles(long long N) { return (N + 127) / 128; }
 
+// Bytes of H as operand planes (TcAdapters::planes).
+size_t plane_bytes(long long N, int R) { return (size_t)list_tiles(N) * round_up(R, 16) * 256; }
+
 // Whether X and W (S x R x F) can take the vector kernels.
 bool shrink_vec(const Adapters &q, const void *X, const void *W, int F) {
     return aligned(X, 16) && aligned(W, 16) && F % (q.bf16 ? 8 : 4) == 0;
 }
 
+// lists, planes: null, or for the tensor-core product; H may then be null.
 template <typename O>
 cudaError_t shrink_bf16(const Adapters &q, const void *X, const void *W, long long N, int F, O *H, int ldh,
-                        int *lists) {
+                        int *lists, unsigned short *planes) {
     const auto *x = static_cast<const __nv_bfloat16 *>(X), *w = static_cast<const __nv_bfloat16 *>(W);
     if (!shrink_vec(q, X, W, F)) {  // (with lists the caller has made sure of vectors)
         shrink_any_kernel<<<(unsigned)((N + 7) / 8), 256, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S,
@@ -754,11 +767,12 @@ cudaError_t shrink_bf16(const Adapters &q, const void *X, const void *W, long lo
         return cudaGetLastError();
     }
     const int row_blocks = (int)((N + 31) / 32), list_blocks = lists ? (int)((list_tiles(N) + 7) / 8) : 0;
-    const int nt = ldh <= 8 ? 1 : ldh <= 16 ? 2 : ldh <= 32 ? 4 : 8;
-    const dim3 grid((unsigned)(row_blocks + list_blocks), (unsigned)((ldh + 8 * nt - 1) / (8 * nt)));
+    const int plane_r = round_up(q.R, 16), cols = std::max(H ? ldh : 0, planes ? plane_r : 0);
+    const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
+    const dim3 grid((unsigned)(row_blocks + list_blocks), (unsigned)((cols + 8 * nt - 1) / (8 * nt)));
     const auto go = [&](auto kernel) {
         kernel<<<grid, 256, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S, device_status_ptr(), row_blocks,
-                                       lists, list_stride(q.S));
+                                       lists, list_stride(q.S), planes, plane_r);
     };
     switch (nt) {
         case 1: go(shrink_mma_kernel<1, O>); break;
@@ -771,7 +785,7 @@ cudaError_t shrink_bf16(const Adapters &q, const void *X, const void *W, long lo
 
 // H = scale X W^T, fp32.
 cudaError_t shrink_fp32_out(const Adapters &q, const void *X, const void *W, long long N, int F, float *H, int ldh) {
-    if (q.bf16) return shrink_bf16<float>(q, X, W, N, F, H, ldh, nullptr);
+    if (q.bf16) return shrink_bf16<float>(q, X, W, N, F, H, ldh, nullptr, nullptr);
     const auto *x = static_cast<const float *>(X), *w = static_cast<const float *>(W);
     if (shrink_vec(q, X, W, F))
         shrink_fp32_kernel<<<(unsigned)((N + 31) / 32), 128, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S,
@@ -941,7 +955,8 @@ bool fuses(const Adapters &q, Problem p, const void *A, int F, const void *bias)
     Plan plan;
     const char *why = "";
     const int ldh = round_up(q.R, 8);
-    const TcAdapters tc{dummy, dummy, nullptr, q.S, ldh, ldh, 0};
+    const TcAdapters tc{dummy, dummy, nullptr, q.S, ldh, 0};
+    p.ad = &tc;
     return make_plan(p, KS_VARIANT_AUTO, &plan, &why) && plan.variant == KS_VARIANT_TC &&
            tc_adapters_supported(p, tc) && shrink_vec(q, p.X, A, F);
 }
@@ -994,15 +1009,15 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         // the adapters as K steps of the tensor-core product, with its bias and activation
         Layout m;
         const int ldh = round_up(q.R, 8);
-        const size_t h = m.add((size_t)batch * ldh * 2), l = m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4);
+        const size_t h = m.add(plane_bytes(batch, q.R)), l = m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4);
         const bool packed = q.R != ldh || !aligned(B, 16);
         const size_t b_at = packed ? m.add((size_t)q.S * out_f * ldh * 2) : 0;
         if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
-        const TcAdapters tc{packed ? w + b_at : B, w + h, reinterpret_cast<int *>(w + l), q.S, ldh, ldh, list_stride(q.S)};
+        const TcAdapters tc{packed ? w + b_at : B, w + h, reinterpret_cast<int *>(w + l), q.S, ldh, list_stride(q.S)};
         e = packed ? pack(q, B, w + b_at, out_f, ldh, false) : cudaSuccess;
         if (e == cudaSuccess)
-            e = shrink_bf16(q, X, A, batch, in_f, reinterpret_cast<__nv_bfloat16 *>(w + h), ldh,
-                            reinterpret_cast<int *>(w + l));
+            e = shrink_bf16<__nv_bfloat16>(q, X, A, batch, in_f, nullptr, 0, reinterpret_cast<int *>(w + l),
+                                           reinterpret_cast<unsigned short *>(w + h));
         if (e == cudaSuccess) {
             p.bias = bias;
             p.act = activation;
@@ -1076,6 +1091,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     }
     const size_t h_bytes = (size_t)batch * ldh * (fused ? 2 : 4);
     const size_t g_at = dX || dA ? m.add(h_bytes) : 0, h_at = dB ? m.add(h_bytes) : 0;
+    const size_t p_at = fused ? m.add(plane_bytes(batch, q.R)) : 0;
     const size_t l_at = fused ? m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4) : 0;
     const size_t ap = fused ? m.add((size_t)q.S * in_f * ldh * 2) : 0;
     const bool sorted = ids && (dA || dB);
@@ -1095,14 +1111,15 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
         then([&] { return launch_transpose_blocks(B, w + bt, q.S, o.out_f, q.R, dtype, q.st); });
         then([&] {
             int *lists = fused ? reinterpret_cast<int *>(w + l_at) : nullptr;
-            return fused ? shrink_bf16(q, dY, w + bt, batch, out_f, b16(g_at), ldh, lists)
+            return fused ? shrink_bf16(q, dY, w + bt, batch, out_f, dA ? b16(g_at) : nullptr, ldh, lists,
+                                       reinterpret_cast<unsigned short *>(w + p_at))
                          : shrink_fp32_out(q, dY, w + bt, batch, out_f, f32(g_at), ldh);
         });
     }
     if (dX) {
         then([&] { return launch_transpose_blocks(values, w + vt, a * d, b, c, dtype, q.st); });
         p.V = w + vt;
-        const TcAdapters tc{w + ap, w + g_at, reinterpret_cast<int *>(w + l_at), q.S, ldh, ldh, list_stride(q.S)};
+        const TcAdapters tc{w + ap, w + p_at, reinterpret_cast<int *>(w + l_at), q.S, ldh, list_stride(q.S)};
         if (fused) {
             then([&] { return pack(q, A, w + ap, in_f, ldh, true); });
             p.ad = &tc;
@@ -1127,7 +1144,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
         });
     if (dB) {
         then([&] {
-            return fused ? shrink_bf16(q, X, A, batch, in_f, b16(h_at), ldh, nullptr)
+            return fused ? shrink_bf16(q, X, A, batch, in_f, b16(h_at), ldh, nullptr, nullptr)
                          : shrink_fp32_out(q, X, A, batch, in_f, f32(h_at), ldh);
         });
         then([&] {

@@ -10,14 +10,19 @@
 namespace ks {
 
 // Low-rank adapters that the tensor-core kernel adds to a bf16 product:
-// Y[n] += H[n] W[s]^T for the rows n of adapter s.  lists, per 128 rows: [0] the
-// number of adapters among them, then from [8] on eight words for each: s, three
-// unused, and a bit for each of the 128 rows that does NOT take it.
+// Y[n] += H[n] W[s]^T for the rows n of adapter s.
+//   planes: H in bf16 as MN-major operand planes, for each 128 rows the ranks in
+//     whole 16s: row n, rank r at byte (r / 8) * 2048 + (n % 128 / 8) * 128 +
+//     (r % 8) * 16 + (n % 8) * 2 of the 128 rows'.  Ranks past R are zeros in rows that take an
+//     adapter; other rows may hold anything.
+//   lists: for each 128 rows [0] the number of adapters among them, [1] the first,
+//     then from [8] on eight words for each: s, three unused, and a bit for each of
+//     the 128 rows that does NOT take it.
 struct TcAdapters {
-    const void *W;      // S x out_features x R bf16, R a multiple of 8, 16-byte aligned
-    const void *H;      // batch x ldh bf16, ldh a multiple of 8, 16-byte aligned
-    const int *lists;   // list_stride words for each 128 rows, 16-byte aligned
-    int S, R, ldh, list_stride;
+    const void *W;       // S x out_features x R bf16, R a multiple of 8, 16-byte aligned
+    const void *planes;  // 16-byte aligned
+    const int *lists;    // list_stride words for each 128 rows, 16-byte aligned
+    int S, R, list_stride;
 };
 
 // One KS product, after validation: Y = X K^T with K of pattern (a,b,c,d).

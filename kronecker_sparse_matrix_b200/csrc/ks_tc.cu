@@ -147,7 +147,7 @@ struct TcParams {
     int stages;                      // X ring depth
     int vstages;                     // values ring depth
     int off_v, off_epi, off_bar;     // shared-memory carve-up (ring at offset 0)
-    int v_stage_bytes;
+    int v_stage_bytes, v_stride;     // of a values stage; with adapters a plane of H follows the values
     int box_elems, box_sw128;        // epilogue staging box: elements per row, swizzled
     int box_row_bytes;               // staging row stride when not swizzled (an odd number of 16-byte units)
     int ytma;                        // the staging box goes to Y as one TMA store: 2-D (d == DLS) or,
@@ -157,20 +157,24 @@ struct TcParams {
 
 // Low-rank adapters beside the product (bf16): Y[n] += H[n] W[s]^T for the rows n
 // of each adapter s, as further K steps of the same accumulation.  After a tile's
-// X chunks come, for each adapter that its 128 rows hold (lists), chunks of
-// CTJ ranks: the transposer warps copy the rows' H into the ring slot as one
-// operand plane (the same for every l), the producer fetches W[s] of the tile's
-// outputs into the values ring in the values' own layout, and the MMAs leave
+// X chunks come, 16 ranks at a time and for each adapter that its 128 rows hold
+// (lists), one more stage of the values ring: W[s] of the tile's outputs (a box
+// like the values', 32-byte rows) and behind it the rows' H, which already lies in
+// global memory as the MN-major operand plane (the same for every l; TcAdapters),
+// so that the transposer warps and the X ring know nothing of it.  The MMAs leave
 // out the lanes of the rows of other adapters, so that nothing an adapter holds
 // (infinities, NaN) reaches a row that does not take it.  Y is still written once.
+constexpr int kRankStep = 16;                        // ranks of a stage: one K step
+constexpr int kPlaneBytes = kRows * kRankStep * 2;   // H of a stage
 template <bool AD>
 struct TcAd {};
 template <>
 struct TcAd<true> {
-    CUtensorMap wmap;        // W viewed as (rank, k, l, i + a * s)
-    const uint16_t *H;       // N x ldh bf16
-    const int *lists;        // per 128 rows: see TcAdapters
-    int R, ldh, list_stride;
+    CUtensorMap wmap;       // W viewed as (rank, k, l, i + a * s)
+    const uint8_t *planes;  // H as operand planes: plane_stride bytes for each 128 rows
+    const int *lists;       // per 128 rows: see TcAdapters
+    int R, list_stride;
+    long long plane_stride;
 };
 
 // Element type T: __nv_bfloat16 (kind::f16) or float (kind::tf32).
@@ -279,6 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const long long rb = t2 / p.n_g;
                 const int i = g / groups_per_i, l0 = (g % groups_per_i) * DLS;
                 const int n0 = (int)(rb * kRows);
+                int2 head = make_int2(0, 0);  // the tile's adapters: how many, the first
+                if constexpr (AD) head = *reinterpret_cast<const int2 *>(ad.lists + rb * ad.list_stride);
                 for (int ch = 0; ch < n_chunks && ok; ++ch) {
                     const int xs = xq % S;
                     ok = mbar_wait(&x_empty[xs], ((xq / S) & 1) ^ 1, abort_flag, p.status, wait_ns);
@@ -294,29 +300,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = mbar_wait(&v_empty[vs], ((vq / VS) & 1) ^ 1, abort_flag, p.status, wait_ns);
                     if (!ok) break;
                     mbar_expect_tx(&v_full[vs], (uint32_t)p.v_stage_bytes);
-                    tma_load_3d(sV + vs * p.v_stage_bytes, &vmap, &v_full[vs], ch * CTJ, ps * p.bp, i * p.d + l0);
+                    tma_load_3d(sV + vs * p.v_stride, &vmap, &v_full[vs], ch * CTJ, ps * p.bp, i * p.d + l0);
                     ++vq;
                 }
                 if constexpr (AD) {
-                    const int *list = ad.lists + rb * ad.list_stride;
-                    const int count = list[0];
-                    for (int q = 0; q < count && ok; ++q) {
-                        const int is = i + p.a * list[8 + 8 * q];
-                        for (int r0 = 0; r0 < ad.R && ok; r0 += CTJ) {
-                            // the slot is free: the transposer warps may write the rows' H there
-                            const int xs = xq % S;
-                            ok = mbar_wait(&x_empty[xs], ((xq / S) & 1) ^ 1, abort_flag, p.status, wait_ns);
-                            if (!ok) break;
-                            mbar_arrive(&x_full[xs]);
-                            ++xq;
+                    constexpr uint32_t wb = DLS * 32;  // bytes of W for one k
+                    for (int r0 = 0; r0 < ad.R && ok; r0 += kRankStep)
+                        for (int q = 0; q < head.x && ok; ++q) {
+                            const int s = q == 0 ? head.y : ad.lists[rb * ad.list_stride + 8 + 8 * q];
                             const int vs = vq % VS;
                             ok = mbar_wait(&v_empty[vs], ((vq / VS) & 1) ^ 1, abort_flag, p.status, wait_ns);
                             if (!ok) break;
-                            mbar_expect_tx(&v_full[vs], (uint32_t)p.v_stage_bytes);
-                            tma_load_4d(sV + vs * p.v_stage_bytes, &ad.wmap, &v_full[vs], r0, ps * p.bp, l0, is);
+                            uint8_t *dst = sV + vs * p.v_stride;
+                            mbar_expect_tx(&v_full[vs], wb * p.bp + kPlaneBytes);
+                            tma_load_4d(dst, &ad.wmap, &v_full[vs], r0, ps * p.bp, l0, i + p.a * s);
+                            bulk_load(dst + p.v_stage_bytes,
+                                      ad.planes + rb * ad.plane_stride + (r0 / kRankStep) * kPlaneBytes, kPlaneBytes,
+                                      &v_full[vs]);
                             ++vq;
                         }
-                    }
                 }
             }
             // On abort, copies already issued may still be landing in shared
@@ -340,14 +342,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (a_major << 15) |
                                    ((uint32_t)(p.bp >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
             uint32_t xq = 0, vq = 0, accq = 0;
-            uint32_t ad_phase = 0;  // DLS == 1: a_ready's parity of each slot (only adapter chunks use it)
             bool ok = true;
             for (long long tile = blockIdx.x; tile < p.n_tiles && ok; tile += gridDim.x, ++accq) {
                 const int *list = nullptr;
                 int count = 0;
+                int4 off0 = make_int4(0, 0, 0, 0);
                 if constexpr (AD) {
                     list = ad.lists + tile / p.passes / p.n_g * ad.list_stride;
                     count = list[0];
+                    off0 = *reinterpret_cast<const int4 *>(list + 12);  // the first entry's rows
                 }
                 const int buf = (int)(accq % p.nbuf);
                 ok = mbar_wait(&acc_empty[buf], ((accq / p.nbuf) & 1) ^ 1, abort_flag, p.status, wait_ns);
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t stage = su32(sR) + xs * SB;
-                    const uint32_t vstage = su32(sV) + vs * p.v_stage_bytes;
+                    const uint32_t vstage = su32(sV) + vs * p.v_stride;
                     for (int s = ch * CTJ / KJ; s < n_steps && s < (ch + 1) * CTJ / KJ; ++s) {
                         const int sl = s - ch * CTJ / KJ;  // K step within the chunk
 #pragma unroll
@@ -390,38 +393,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(&x_empty[xs]);
                 }
                 if constexpr (AD) {
-                    for (int q = 0; q < count && ok; ++q) {
-                        const int4 m = *reinterpret_cast<const int4 *>(list + 8 + 8 * q + 4);
-                        const uint32_t off[4] = {(uint32_t)m.x, (uint32_t)m.y, (uint32_t)m.z, (uint32_t)m.w};
-                        for (int r0 = 0; r0 < ad.R && ok; r0 += CTJ, ++xq) {
-                            const int xs = xq % S;
-                            const uint32_t par = DLS == 1 ? (ad_phase >> xs) & 1 : (xq / S) & 1;
-                            ok = mbar_wait(&a_ready[xs], par, abort_flag, p.status, wait_ns);
-                            if (!ok) break;
-                            ad_phase ^= 1u << xs;
+                    for (int r0 = 0; r0 < ad.R && ok; r0 += kRankStep)
+                        for (int q = 0; q < count && ok; ++q) {
+                            const int4 m = q == 0 ? off0 : *reinterpret_cast<const int4 *>(list + 8 + 8 * q + 4);
+                            const uint32_t off[4] = {(uint32_t)m.x, (uint32_t)m.y, (uint32_t)m.z, (uint32_t)m.w};
                             const int vs = vq % VS;
                             ok = mbar_wait(&v_full[vs], (vq / VS) & 1, abort_flag, p.status, wait_ns);
                             ++vq;
                             if (!ok) break;
                             tc_fence_after();
-                            const uint32_t stage = su32(sR) + xs * SB;
-                            const uint32_t vstage = su32(sV) + vs * p.v_stage_bytes;
-                            const int steps = (min(CTJ, ad.R - r0) + KJ - 1) / KJ;
-                            for (int sl = 0; sl < steps; ++sl) {
-                                const uint64_t adsc = DLS == 1    ? smem_desc_sw128(stage + sl * 32, 1024)
-                                                      : DLS == 16 ? smem_desc(stage, 128, kG16)
-                                                                  : smem_desc(stage + sl * 2 * OS, OS, GS);
+                            const uint32_t vstage = su32(sV) + vs * p.v_stride;
+                            // H: core matrices of 8 ranks x 8 rows, row groups 128 bytes apart, rank octets 2048
+                            const uint64_t adsc = smem_desc(vstage + p.v_stage_bytes, 2048, 128);
 #pragma unroll
-                                for (int l = 0; l < DLS; ++l) {
-                                    const uint32_t b_addr = vstage + l * (p.bp * CTJ * ES) + sl * 32;
-                                    const uint64_t bd = smem_desc_sw(b_addr, 8 * CTJ * ES, v_layout(DLS, ES));
-                                    mma_bf16_lanes(d_base + l * p.bp, adsc, bd, idesc, off);
-                                }
+                            for (int l = 0; l < DLS; ++l) {
+                                const uint64_t bd = smem_desc_sw(vstage + l * (p.bp * 32), 8 * 32, 6u);
+                                mma_bf16_lanes(d_base + l * p.bp, adsc, bd, idesc | (1u << 15), off);
                             }
                             mma_commit(&v_empty[vs]);
-                            mma_commit(&x_empty[xs]);
                         }
-                    }
                 }
                 if (ok) mma_commit(&acc_full[buf]);
             }
@@ -431,59 +421,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kEpiWarp0) {
         // ------------------------------------------------ in-place transpose (DLS > 1)
-        // Adapter chunks of a tile: the 128 rows' H, CTJ ranks at a time, into the
-        // ring slot, as the K-major tile (DLS == 1) or as plane 0 of the transposed
-        // chunks (a task is 8 rows x 8 ranks).  Ranks past R and rows past N are
-        // zeros.  The loads are issued before the slot is waited for.
-        auto adapter_chunks = [&](long long tile, uint32_t &xq) -> bool {
-            if constexpr (AD) {
-                const int t = threadIdx.x - kLoadWarp0 * 32;  // 0..127
-                const long long rb = tile / p.passes / p.n_g;
-                const int count = ad.lists[rb * ad.list_stride];
-                const int octet = DLS == 1 ? 0 : t >> 4, g = DLS == 1 ? 0 : t & 15;
-                const bool task = DLS == 1 || octet < CTJ / 8;
-                for (int q = 0; q < count; ++q) {
-                    for (int r0 = 0; r0 < ad.R; r0 += CTJ, ++xq) {
-                        uint4 in[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            // DLS == 1: row t, ranks r0 + 8 e ..; else row 8 g + e, ranks r0 + 8 octet ..
-                            const long long n = rb * kRows + (DLS == 1 ? t : 8 * g + e);
-                            const int r = r0 + 8 * (DLS == 1 ? e : octet);
-                            in[e] = make_uint4(0u, 0u, 0u, 0u);
-                            if (task && n < p.N && r < ad.R)
-                                in[e] = *reinterpret_cast<const uint4 *>(ad.H + n * ad.ldh + r);
-                        }
-                        const int xs = xq % S;
-                        const bool w = mbar_wait(&x_full[xs], (xq / S) & 1, abort_flag, p.status, wait_ns);
-                        if (!bar_and(1, 128, w)) return false;
-                        uint8_t *st = sR + xs * SB;
-                        if constexpr (DLS == 1) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4 *>(st + t * 128 + ((e ^ (t & 7)) << 4)) = in[e];
-                        } else if (task) {
-                            uint4 out[8];
-                            transpose8x8_b16(in, out);
-                            uint8_t *base = DLS == 16 ? st + g * kG16 + octet * 128 : st + octet * OS + g * GS;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(base + e * 16) = out[e];
-                        }
-                        fence_proxy_async();
-                        mbar_arrive(&a_ready[xs]);
-                    }
-                }
-            }
-            return true;
-        };
-        if constexpr (DLS == 1 && AD) {
-            uint32_t xq = 0;
-            bool ok = true;
-            for (long long tile = blockIdx.x; tile < p.n_tiles && ok; tile += gridDim.x) {
-                xq += n_chunks;  // the TMA tiles are the operands
-                ok = adapter_chunks(tile, xq);
-            }
-        }
         if constexpr (DLS == 16) {
             // bf16, 16 l: raw row = 32 units of 16 bytes, unit q = (j = q / 2,
             // l half q % 2).  Warp tw takes row groups tw, tw + 4, tw + 8, tw + 12;
@@ -522,7 +459,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async();
                     mbar_arrive(&a_ready[xs]);
                 }
-                if (ok) ok = adapter_chunks(tile, xq);
             }
         } else if (DLS > 1 && ES == 2) {
             const int t = threadIdx.x - kLoadWarp0 * 32;  // 0..127
@@ -577,7 +513,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async();
                     mbar_arrive(&a_ready[xs]);
                 }
-                if (ok) ok = adapter_chunks(tile, xq);
             }
         } else if (DLS > 1) {
             // fp32: per l a K-major plane of 32-byte rows (8 j) with the 32-byte
@@ -961,7 +896,7 @@ int tc_bp(int dls, int64_t b) {
 }
 
 struct TcLayout {
-    int stages, vstages, v_stage_bytes, off_v, off_epi, off_bar, total;
+    int stages, vstages, v_stage_bytes, v_stride, off_v, off_epi, off_bar, total;
 };
 
 constexpr int kBarBytes = (3 * kMaxStages + 2 * kVStages + 2 + 2 + 1) * 8 + 16;
@@ -970,19 +905,20 @@ constexpr int kBarBytes = (3 * kMaxStages + 2 * kVStages + 2 + 2 + 1) * 8 + 16;
 // (one stage per X chunk: DLS planes x bp k x CTJ j, 3..4 deep), the epilogue
 // staging (and, with a fused bias and DLS >= 4, two tiles of bias per epilogue
 // warp), barriers.
-bool tc_layout(int dls, int bp, int es, bool bias, TcLayout *out) {
+bool tc_layout(int dls, int bp, int es, bool bias, bool ad, TcLayout *out) {
     const bool ep = bias && dls >= 4;
     TcLayout L;
     auto up = [](int x, int a) { return (x + a - 1) / a * a; };
     const int cb = slot_bytes(dls, es);
     L.v_stage_bytes = es * bp * chunk_j(dls, es) * dls;
+    L.v_stride = L.v_stage_bytes + (ad ? kPlaneBytes : 0);
     if (bp * dls * es > kBiasBytes) return false;
     const int epi = 4 * kEpiWarpBytes + (ep ? 4 * 2 * kBiasBytes : 0);
     const int budget = kSmemLimit - 2048 - 4 * kEpiWarpBytes - kBarBytes;  // alignment slack
     auto x_stages = [&](int bud, int vs) {
-        return std::min(kMaxStages, (bud - up(vs * L.v_stage_bytes, 128)) / cb);
+        return std::min(kMaxStages, (bud - up(vs * L.v_stride, 128)) / cb);
     };
-    L.vstages = (kVStages * L.v_stage_bytes + 3 * cb <= budget) ? kVStages : 3;
+    L.vstages = (kVStages * L.v_stride + 3 * cb <= budget) ? kVStages : 3;
     L.stages = x_stages(budget, L.vstages);
     if (ep) {  // the bias buffers come out of a values stage rather than an X stage where possible
         const int bud = budget - 4 * 2 * kBiasBytes;
@@ -993,7 +929,7 @@ bool tc_layout(int dls, int bp, int es, bool bias, TcLayout *out) {
     }
     if (L.stages < 2) return false;
     L.off_v = L.stages * cb;
-    L.off_epi = up(L.off_v + L.vstages * L.v_stage_bytes, 1024);
+    L.off_epi = up(L.off_v + L.vstages * L.v_stride, 1024);
     L.off_bar = up(L.off_epi + epi, 128);
     L.total = L.off_bar + kBarBytes + 1024;
     if (L.total > kSmemLimit) return false;
@@ -1036,12 +972,12 @@ bool tc_supported(const Problem &p, const char **why) {
     const int bp = tc_bp(dls, p.b);
     TcLayout L;
     if (bp == 0 || tc_kc(dls, bp, es) == 0) { *why = "b has no pass width (a multiple of 16 dividing it)"; return false; }
-    if (!tc_layout(dls, bp, es, p.bias != nullptr, &L)) { *why = "shared memory budget"; return false; }
+    if (!tc_layout(dls, bp, es, p.bias != nullptr, p.ad != nullptr, &L)) { *why = "shared memory budget"; return false; }
     if (p.batch > (1LL << 31) - 256 || p.a * p.d > (1LL << 31)) { *why = "sizes exceed tensor-map coordinates"; return false; }
     return true;
 }
 
-// ranks in 16-byte units (W's strides and H's loads), W aligned, map coordinates in range
+// ranks in 16-byte units (W's strides), W aligned, map coordinates in range
 bool tc_adapters_supported(const Problem &p, const TcAdapters &q) {
     return p.dtype == KS_BF16 && q.R % 8 == 0 && reinterpret_cast<uintptr_t>(q.W) % 16 == 0 &&
            p.a * q.S < (1LL << 31) && p.b * p.d * q.R * 2 < (1LL << 40);
@@ -1055,7 +991,7 @@ static cudaError_t launch_dls(const Problem &pr, const TcConfig &cfg) {
     if (!encode) return cudaErrorNotSupported;
     const int bp = cfg.bk;
     TcLayout L;
-    if (bp == 0 || !tc_layout(DLS, bp, ES, pr.bias != nullptr, &L)) return cudaErrorInvalidConfiguration;
+    if (bp == 0 || !tc_layout(DLS, bp, ES, pr.bias != nullptr, pr.ad != nullptr, &L)) return cudaErrorInvalidConfiguration;
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUtensorMap xmap, vmap;
     CUresult r;
@@ -1164,31 +1100,29 @@ static cudaError_t launch_dls(const Problem &pr, const TcConfig &cfg) {
     p.off_epi = L.off_epi;
     p.off_bar = L.off_bar;
     p.v_stage_bytes = L.v_stage_bytes;
+    p.v_stride = L.v_stride;
     const bool ep = pr.bias || pr.act;
     const long long grid = std::min<long long>(p.n_tiles, (long long)sm_count());
     if constexpr (ES == 2) {
         if (pr.ad) {
             // W[s] (out_f x R, ranks contiguous) viewed as (rank, k, l, i + a * s): a box
-            // (CTJ ranks, bp k, DLS l) lands like the values of CTJ j; ranks past R are
-            // filled with zeros.  Always with the epilogue: without a bias and an
-            // activation it measured the same as the kernel that leaves it out.
+            // (16 ranks, bp k, DLS l) lands as DLS planes of 32-byte rows; ranks past R are
+            // filled with zeros.  Always the kernel with the epilogue.
             const TcAdapters &q = *pr.ad;
             TcAd<true> ad;
             cuuint64_t dims[4] = {(cuuint64_t)q.R, (cuuint64_t)pr.b, (cuuint64_t)pr.d, (cuuint64_t)(pr.a * q.S)};
             cuuint64_t strides[3] = {(cuuint64_t)pr.d * q.R * ES, (cuuint64_t)q.R * ES,
                                      (cuuint64_t)pr.b * pr.d * q.R * ES};
-            cuuint32_t box[4] = {(cuuint32_t)chunk_j(DLS, ES), (cuuint32_t)bp, (cuuint32_t)DLS, 1};
-            const int rb = v_row_bytes(DLS, ES);
+            cuuint32_t box[4] = {(cuuint32_t)kRankStep, (cuuint32_t)bp, (cuuint32_t)DLS, 1};
             r = encode(&ad.wmap, kType, 4, const_cast<void *>(q.W), dims, strides, box, estr,
                        CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       rb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                       : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                  : CU_TENSOR_MAP_SWIZZLE_32B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                       CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
             if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-            ad.H = static_cast<const uint16_t *>(q.H);
+            ad.planes = static_cast<const uint8_t *>(q.planes);
+            ad.plane_stride = (long long)((q.R + kRankStep - 1) / kRankStep) * kPlaneBytes;
             ad.lists = q.lists;
-            ad.R = q.R, ad.ldh = q.ldh, ad.list_stride = q.list_stride;
+            ad.R = q.R, ad.list_stride = q.list_stride;
             auto kern = tc_kernel<DLS, T, true, false, true>;
             if constexpr (kY4)
                 if (y4d) kern = tc_kernel<DLS, T, true, true, true>;
