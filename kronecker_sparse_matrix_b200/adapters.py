@@ -5,11 +5,11 @@ marshals torch tensors into the C ABI (ks_adapter_matmul, ks_adapter_backward).
 """
 from __future__ import annotations
 
-from typing import Optional, Tuple
+from typing import Optional
 
 import torch
 
-from . import KSLinear, Pattern, _act, _bias_ptr, _lib, _stream_ptr, bias_grad, ks_dtype_of, matmul_dv
+from . import KS_BF16, KS_F32, KS_TF32, KSLinear, Pattern, _act, _lib, _stream_ptr, bias_grad, matmul_dv
 
 
 def _empty(shape, like: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
@@ -20,33 +20,26 @@ def _empty(shape, like: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> to
         return torch.empty(shape, dtype=like.dtype, device=like.device)
 
 
-def _check_adapters(x: torch.Tensor, values: Optional[torch.Tensor], pattern: Pattern, A: torch.Tensor,
-                    B: torch.Tensor, ids: Optional[torch.Tensor], scales: Optional[torch.Tensor], width: int,
-                    name: str) -> Tuple[int, int, int, int, int, int]:
-    a, b, c, d = (int(v) for v in pattern)
-    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous() or x.shape[1] != width:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of shape (batch, {width})")
-    if A.dim() != 3 or A.shape[2] != a * c * d or A.shape[0] == 0 or A.shape[1] == 0:
-        raise ValueError(f"A must have shape (adapters, rank, {a * c * d})")
-    s, r = A.shape[0], A.shape[1]
-    if B.shape != (s, a * b * d, r):
-        raise ValueError(f"B must have shape ({s}, {a * b * d}, {r})")
-    for t in (A, B, values):
-        if t is not None and (t.dtype != x.dtype or t.device != x.device or not t.is_contiguous()):
-            raise ValueError(f"values, A and B must be contiguous, with {name}'s dtype and device")
-    if values is not None and values.numel() != a * b * c * d:
-        raise ValueError(f"values must have {a * b * c * d} elements")
-    if ids is not None and (ids.dtype != torch.int32 or ids.device != x.device or ids.shape != (x.shape[0],)
-                            or not ids.is_contiguous()):
-        raise ValueError("ids must be a contiguous int32 tensor with one entry per row, on the same device")
-    if scales is not None and (scales.dtype != torch.float32 or scales.device != x.device or scales.shape != (s,)
-                               or not scales.is_contiguous()):
-        raise ValueError("scales must be a contiguous float32 tensor with one entry per adapter, on the same device")
-    return a, b, c, d, s, r
-
-
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+def _dtype_of(kind: int, tf32: bool) -> int:
+    """ks_dtype of a kind of _ks_marshal (0 float32, 1 bfloat16)."""
+    if kind == 1 and tf32:
+        raise ValueError("tf32 applies to fp32 tensors only")
+    return KS_BF16 if kind == 1 else KS_TF32 if tf32 else KS_F32
+
+
+def _call(device: int, stream: Optional[torch.cuda.Stream], function: str, *args) -> None:
+    """The entry point on the given device, its current stream if none is given."""
+    dev = torch.device("cuda", device)
+    if torch.cuda.current_device() == device:
+        st = getattr(_lib.load(), function)(*args, _stream_ptr(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(_lib.load(), function)(*args, _stream_ptr(stream, dev))
+    _lib.check(st)
 
 
 def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: torch.Tensor, B: torch.Tensor,
@@ -61,19 +54,19 @@ def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: t
     scales: float32, one per adapter (None: ones).  An id that is too large
     takes no adapter, and the next ``sync_status`` raises.  Rows of one adapter
     next to each other run fastest.  Asynchronous on ``stream``."""
-    fin = int(pattern[0]) * int(pattern[2]) * int(pattern[3])
-    a, b, c, d, s, r = _check_adapters(x, values, pattern, A, B, ids, scales, fin, "x")
-    dt = ks_dtype_of(x, tf32)
-    batch, fout = x.shape[0], a * b * d
+    from ._ks_marshal import adapter_args  # built with the library
+    a, b, c, d = (int(v) for v in pattern)
+    fin, fout = a * c * d, a * b * d
+    if values is None:
+        raise ValueError("values must be a tensor")
+    batch, s, r, kind, dev, px, pv, pa, pb, pids, pscales, pbias = adapter_args(
+        x, values, A, B, ids, scales, bias, fin, fin, fout, a * b * c * d, "x")
     if out is None:
         out = _empty((batch, fout), x, stream)
     elif not out.is_contiguous() or out.dtype != x.dtype or out.device != x.device or out.shape != (batch, fout):
         raise ValueError(f"out must be a contiguous ({batch}, {fout}) tensor with x's dtype and device")
-    with torch.cuda.device(x.device):
-        st = _lib.load().ks_adapter_matmul(x.data_ptr(), values.data_ptr(), a, b, c, d, batch, out.data_ptr(), dt,
-                                           _bias_ptr(bias, x, fout), _act(act), A.data_ptr(), B.data_ptr(),
-                                           _ptr(scales), _ptr(ids), s, r, _stream_ptr(stream, x.device))
-    _lib.check(st)
+    _call(dev, stream, "ks_adapter_matmul", px, pv, a, b, c, d, batch, out.data_ptr(), _dtype_of(kind, tf32), pbias,
+          _act(act), pa, pb, pscales, pids, s, r)
     return out
 
 
@@ -85,9 +78,11 @@ def adapter_backward(dy: torch.Tensor, x: Optional[torch.Tensor], values: Option
     dY (batch, a*b*d); None in the place of one that is not needed (values may
     be None without dX, x without dA and dB).  An adapter without rows gets
     zeros.  Deterministic; fp32 sums, bf16 gradients rounded once."""
-    fout = int(pattern[0]) * int(pattern[1]) * int(pattern[3])
-    a, b, c, d, s, r = _check_adapters(dy, values, pattern, A, B, ids, scales, fout, "dy")
-    batch, fin = dy.shape[0], a * c * d
+    from ._ks_marshal import adapter_args  # built with the library
+    a, b, c, d = (int(v) for v in pattern)
+    fin, fout = a * c * d, a * b * d
+    batch, s, r, kind, dev, pdy, pv, pa, pb, pids, pscales, _ = adapter_args(
+        dy, values, A, B, ids, scales, None, fout, fin, fout, a * b * c * d, "dy")
     if need_dx and values is None:
         raise ValueError("dX needs the values")
     if need_da or need_db:
@@ -97,12 +92,8 @@ def adapter_backward(dy: torch.Tensor, x: Optional[torch.Tensor], values: Option
     dx = _empty((batch, fin), dy, stream) if need_dx else None
     da = _empty(A.shape, A, stream) if need_da else None
     db = _empty(B.shape, B, stream) if need_db else None
-    with torch.cuda.device(dy.device):
-        st = _lib.load().ks_adapter_backward(dy.data_ptr(), _ptr(x), _ptr(values), a, b, c, d, batch,
-                                             ks_dtype_of(dy, tf32), A.data_ptr(), B.data_ptr(), _ptr(scales),
-                                             _ptr(ids), s, r, _ptr(dx), _ptr(da), _ptr(db),
-                                             _stream_ptr(stream, dy.device))
-    _lib.check(st)
+    _call(dev, stream, "ks_adapter_backward", pdy, _ptr(x), pv, a, b, c, d, batch, _dtype_of(kind, tf32), pa, pb,
+          pscales, pids, s, r, _ptr(dx), _ptr(da), _ptr(db))
     return dx, da, db
 
 

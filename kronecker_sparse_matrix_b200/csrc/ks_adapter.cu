@@ -15,26 +15,14 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
+#include "ks_adapter.cuh"
 #include "ks_epilogue.cuh"
 #include "ks_internal.h"
 
 namespace ks {
 namespace {
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float *p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
-
-__device__ __forceinline__ int adapter_of(const int *ids, long long n, int adapters, unsigned *status) {
-    const int s = ids ? ids[n] : 0;
-    if (s >= adapters) {
-        atomicOr(status, kDevBadIndex);
-        return -1;
-    }
-    return s < 0 ? -1 : s;
-}
 
 // ---------------------------------------------------------------- H = scale X W^T
 //
@@ -53,7 +41,7 @@ __global__ void __launch_bounds__(256)
     const int lane = threadIdx.x & 31;
     const long long n = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (n >= N) return;
-    const int s = adapter_of(ids, n, S, status);
+    const int s = row_adapter(ids, n, N, S, status);
     O *h = H + n * ldh;
     if (s < 0) {
         for (int r = lane; r < ldh; r += 32) put(h + r, 0.f);
@@ -95,7 +83,7 @@ __global__ void __launch_bounds__(128)
     const int lane = threadIdx.x & 31;
     const long long n0 = ((long long)blockIdx.x * 4 + (threadIdx.x >> 5)) * 8;
     if (n0 >= N) return;
-    const int id = lane < 8 && n0 + lane < N ? adapter_of(ids, n0 + lane, S, status) : -1;
+    const int id = lane < 8 ? row_adapter(ids, n0 + lane, N, S, status) : -1;
     const int row = lane >> 2;  // the row and ranks (2 q, 2 q + 1) whose sums end in this lane
     const long long n = n0 + row;
     if (__shfl_sync(0xFFFFFFFFu, id, row) < 0 && n < N)
@@ -103,6 +91,22 @@ __global__ void __launch_bounds__(128)
             H[n * ldh + r] = 0.f;
             if (r + 1 < ldh) H[n * ldh + r + 1] = 0.f;
         }
+    int found = 0;
+    for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) ++found;
+    if (found > 2) {  // each pass computes all eight rows: more than two cost more than row by row
+        for (int m = 0; m < 8; ++m) {
+            const int s = __shfl_sync(0xFFFFFFFFu, id, m);
+            if (s < 0) continue;
+            for (int r = 0; r < ldh; r += 4) {
+                float h[4] = {0.f, 0.f, 0.f, 0.f};
+                if (r < R) dot4(X + (n0 + m) * F, W + ((long long)s * R + r) * F, F, R - r, lane, h);
+                const float v = lane == 0 ? h[0] : lane == 1 ? h[1] : lane == 2 ? h[2] : h[3];
+                if (lane < 4 && r + lane < ldh)
+                    H[(n0 + m) * ldh + r + lane] = r + lane < R ? (scales ? scales[s] : 1.f) * v : 0.f;
+            }
+        }
+        return;
+    }
     for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
         const bool mine = __shfl_sync(0xFFFFFFFFu, id, row) == s;
         const float sc = scales ? scales[s] : 1.f;
@@ -207,6 +211,10 @@ __device__ __forceinline__ unsigned short *plane_at(unsigned short *planes, long
     return planes + n / 128 * (plane_r * 128) + (r >> 3) * 1024 + (int)(n % 128 >> 3) * 64 + (r & 7) * 8 + (int)(n & 7);
 }
 
+// Blocks of 32 rows with more adapters than this go row by row: a pass takes about
+// as long as six rows' dot products.
+constexpr int kMixed = 6;
+
 template <int NT, typename O>
 __global__ void __launch_bounds__(256)
     shrink_mma_kernel(const __nv_bfloat16 *__restrict__ X, const __nv_bfloat16 *__restrict__ W,
@@ -225,7 +233,7 @@ __global__ void __launch_bounds__(256)
     const long long n0 = (long long)blockIdx.x * ROWS;
     const int r0 = blockIdx.y * RC;
     if (warp == 0) {
-        const int id = n0 + lane < N ? adapter_of(ids, n0 + lane, S, status) : -1;
+        const int id = row_adapter(ids, n0 + lane, N, S, status);
         row_id[lane] = id;
         int count = 0;
         for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
@@ -240,13 +248,29 @@ __global__ void __launch_bounds__(256)
         const int m = q / RC, r = r0 + q % RC;
         if (H && row_id[m] < 0 && n0 + m < N && r < ldh) put(H + (n0 + m) * ldh + r, 0.f);
     }
+    const int n_s = n_found;
+    if (n_s > kMixed) {  // too many passes: row by row
+        for (int q = warp; q < ROWS * RC / 4; q += 8) {
+            const int m = q / (RC / 4), r = r0 + q % (RC / 4) * 4, s = row_id[m];
+            if (s < 0) continue;
+            float h[4] = {0.f, 0.f, 0.f, 0.f};
+            if (r < R) dot4(X + (n0 + m) * F, W + ((long long)s * R + r) * F, F, R - r, lane, h);
+            if (lane < 4) {
+                const float v = (lane == 0 ? h[0] : lane == 1 ? h[1] : lane == 2 ? h[2] : h[3]);
+                const float hv = r + lane < R ? (scales ? scales[s] : 1.f) * v : 0.f;
+                if (H && r + lane < ldh) put(H + (n0 + m) * ldh + r + lane, hv);
+                if (planes && r + lane < plane_r)
+                    *plane_at(planes, n0 + m, r + lane, plane_r) = __bfloat16_as_ushort(__float2bfloat16_rn(hv));
+            }
+        }
+        return;
+    }
     const uint4 *x[2 * MT];
 #pragma unroll
     for (int m = 0; m < 2 * MT; ++m) {  // rows past the last are read as the last one
         const long long n = n0 + 8 * m + g < N ? n0 + 8 * m + g : N - 1;
         x[m] = reinterpret_cast<const uint4 *>(X + n * F);
     }
-    const int n_s = n_found;
     for (int k = 0; k < n_s; ++k) {
         const int s = found[k];
         const uint4 *w[NT];
@@ -756,6 +780,13 @@ bool shrink_vec(const Adapters &q, const void *X, const void *W, int F) {
     return aligned(X, 16) && aligned(W, 16) && F % (q.bf16 ? 8 : 4) == 0;
 }
 
+// One warp for four ranks of a row, W[s] read again for each row, while that is at
+// most 16 MB (fp32: 64 MB, its tiles are slower) from L2: more warps than the
+// tiles have.
+bool by_rows(const Adapters &q, long long N, int F) {
+    return (double)N * q.R * F * (q.bf16 ? 2 : 4) <= (q.bf16 ? 16e6 : 64e6);
+}
+
 // lists, planes: null, or for the tensor-core product; H may then be null.
 template <typename O>
 cudaError_t shrink_bf16(const Adapters &q, const void *X, const void *W, long long N, int F, O *H, int ldh,
@@ -766,6 +797,9 @@ cudaError_t shrink_bf16(const Adapters &q, const void *X, const void *W, long lo
                                                                      device_status_ptr());
         return cudaGetLastError();
     }
+    if (by_rows(q, N, F) && !planes)
+        return launch_shrink_rows(X, W, q.scales, q.ids, H, std::is_same_v<O, __nv_bfloat16>, N, F, q.R, ldh, q.S, true,
+                                  q.st);
     const int row_blocks = (int)((N + 31) / 32), list_blocks = lists ? (int)((list_tiles(N) + 7) / 8) : 0;
     const int plane_r = round_up(q.R, 16), cols = std::max(H ? ldh : 0, planes ? plane_r : 0);
     const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
@@ -787,6 +821,8 @@ cudaError_t shrink_bf16(const Adapters &q, const void *X, const void *W, long lo
 cudaError_t shrink_fp32_out(const Adapters &q, const void *X, const void *W, long long N, int F, float *H, int ldh) {
     if (q.bf16) return shrink_bf16<float>(q, X, W, N, F, H, ldh, nullptr, nullptr);
     const auto *x = static_cast<const float *>(X), *w = static_cast<const float *>(W);
+    if (by_rows(q, N, F) && shrink_vec(q, X, W, F))
+        return launch_shrink_rows(X, W, q.scales, q.ids, H, false, N, F, q.R, ldh, q.S, false, q.st);
     if (shrink_vec(q, X, W, F))
         shrink_fp32_kernel<<<(unsigned)((N + 31) / 32), 128, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S,
                                                                         device_status_ptr());
@@ -1005,7 +1041,21 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
     const int in_f = (int)o.in_f, out_f = (int)o.out_f;
     cudaError_t e;
     char *w = nullptr;
-    if (fuses(q, p, A, in_f, bias)) {
+    const int row_ldh = round_up(q.R, 4);
+    if (adapter_rows_supported(p, A, row_ldh)) {
+        // few rows: one launch, or two where A[s] is more than a block should read for itself
+        const bool apart = (size_t)q.R * in_f * o.elem > 64 * 1024;
+        p.bias = bias;
+        p.act = activation;
+        if (!apart) {
+            e = launch_adapter_rows(p, A, B, scales, ids, q.S, q.R, nullptr, row_ldh);
+            return e == cudaSuccess ? KS_OK : cuda_fail(e, "adapter launch");
+        }
+        if ((s = alloc(&w, (size_t)batch * row_ldh * 4, q.st)) != KS_OK) return s;
+        float *H = reinterpret_cast<float *>(w);
+        e = launch_shrink_rows(X, A, scales, ids, H, false, batch, in_f, q.R, row_ldh, q.S, q.bf16, q.st);
+        if (e == cudaSuccess) e = launch_adapter_rows(p, A, B, scales, ids, q.S, q.R, H, row_ldh);
+    } else if (fuses(q, p, A, in_f, bias)) {
         // the adapters as K steps of the tensor-core product, with its bias and activation
         Layout m;
         const int ldh = round_up(q.R, 8);

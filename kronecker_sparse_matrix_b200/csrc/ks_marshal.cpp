@@ -1,9 +1,10 @@
-// Reads lists of torch tensors into the table of ks_adamw_step, for the Python
-// binding: type, device, contiguity, element count and address of each tensor
-// through the DLPack exchange functions that torch.Tensor publishes
-// (__dlpack_c_exchange_api__), so that no torch type is needed here.  The same
-// checks as attribute reads from Python take 18 us for a list of 60 tensors, an
-// order of magnitude more than here, and a step has up to seven lists.
+// Checks and reads torch tensors for the Python binding (the table of
+// ks_adamw_step, the arguments of the adapter calls): type, device, contiguity,
+// shape and address of each tensor through the DLPack exchange functions that
+// torch.Tensor publishes (__dlpack_c_exchange_api__), so that no torch type is
+// needed here.  The same checks as attribute reads from Python take 18 us for a
+// list of 60 tensors, an order of magnitude more than here, and a step has up to
+// seven lists; for one adapter call they take half of a single token's time.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -18,12 +19,13 @@ const DLPackExchangeAPI *g_api = nullptr;
 PyTypeObject *g_tensor = nullptr;
 
 // Type codes of the table: what ks_dtype and state_bits are chosen by.
-enum Kind { kNone = -1, kF32 = 0, kBF16 = 1, kE4M3 = 2 };
+enum Kind { kNone = -1, kF32 = 0, kBF16 = 1, kE4M3 = 2, kI32 = 3 };
 
 int kind_of(const DLDataType &t) {
     if (t.lanes != 1) return kNone;
     if (t.code == kDLFloat && t.bits == 32) return kF32;
     if (t.code == kDLBfloat && t.bits == 16) return kBF16;
+    if (t.code == kDLInt && t.bits == 32) return kI32;
     if (t.code == kDLFloat8_e4m3fn && t.bits == 8) return kE4M3;
     return kNone;
 }
@@ -36,6 +38,8 @@ struct Info {
     uint64_t ptr;
     int64_t numel;
     int kind, device;  // device: CUDA index, or -1
+    int ndim;
+    int64_t shape[3];  // of the first three dimensions
     bool contiguous;
 };
 
@@ -55,6 +59,8 @@ bool read(PyObject *o, Info *out) {
         if (t.strides && t.shape[d] > 1 && t.strides[d] != n) c = false;
         n *= t.shape[d];
     }
+    out->ndim = t.ndim;
+    for (int d = 0; d < 3; ++d) out->shape[d] = d < t.ndim ? t.shape[d] : 1;
     out->numel = n;
     out->contiguous = c || n == 0;
     return true;
@@ -142,7 +148,57 @@ done:
     return result;
 }
 
+// adapter_args(x, values, A, B, ids, scales, bias, width, in_f, out_f, nvals, name)
+//   -> (rows, adapters, rank, dtype kind, device, x, values, A, B, ids, scales, bias)
+// x: (rows, width), called `name` in messages; values, ids, scales and bias may be None (0).
+PyObject *adapter_args(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    if (nargs != 12) return PyErr_Format(PyExc_TypeError, "adapter_args takes 12 arguments");
+    long long size[4];
+    for (int k = 0; k < 4; ++k) {
+        size[k] = PyLong_AsLongLong(args[7 + k]);
+        if (size[k] == -1 && PyErr_Occurred()) return nullptr;
+    }
+    const long long width = size[0], in_f = size[1], out_f = size[2], nvals = size[3];
+    Info t[7];
+    for (int k = 0; k < 7; ++k) {
+        t[k] = Info{};
+        if (args[k] == Py_None && k != 0 && k != 2 && k != 3) continue;
+        if (!read(args[k], &t[k])) return nullptr;
+    }
+    const Info &x = t[0], &A = t[2], &B = t[3];
+    const auto given = [&](int k) { return args[k] != Py_None; };
+    const auto like_x = [&](const Info &o) { return o.kind == x.kind && o.device == x.device && o.contiguous; };
+    if (x.kind != kF32 && x.kind != kBF16)
+        return PyErr_Format(PyExc_TypeError, "unsupported dtype of %U: use float32 or bfloat16", args[11]);
+    if (x.ndim != 2 || x.device < 0 || !x.contiguous || x.shape[1] != width)
+        return PyErr_Format(PyExc_ValueError, "%U must be a contiguous CUDA tensor of shape (batch, %lld)", args[11], width);
+    if (A.ndim != 3 || A.shape[2] != in_f || A.shape[0] == 0 || A.shape[1] == 0)
+        return PyErr_Format(PyExc_ValueError, "A must have shape (adapters, rank, %lld)", in_f);
+    const long long s = A.shape[0], r = A.shape[1];
+    if (B.ndim != 3 || B.shape[0] != s || B.shape[1] != out_f || B.shape[2] != r)
+        return PyErr_Format(PyExc_ValueError, "B must have shape (%lld, %lld, %lld)", s, out_f, r);
+    if (!like_x(A) || !like_x(B) || (given(1) && !like_x(t[1])))
+        return PyErr_Format(PyExc_ValueError, "values, A and B must be contiguous, with %U's dtype and device", args[11]);
+    if (given(1) && t[1].numel != nvals) return PyErr_Format(PyExc_ValueError, "values must have %lld elements", nvals);
+    if (given(4) && (t[4].kind != kI32 || t[4].device != x.device || t[4].ndim != 1 || t[4].shape[0] != x.shape[0] ||
+                     !t[4].contiguous))
+        return PyErr_Format(PyExc_ValueError,
+                            "ids must be a contiguous int32 tensor with one entry per row, on the same device");
+    if (given(5) && (t[5].kind != kF32 || t[5].device != x.device || t[5].ndim != 1 || t[5].shape[0] != s ||
+                     !t[5].contiguous))
+        return PyErr_Format(PyExc_ValueError,
+                            "scales must be a contiguous float32 tensor with one entry per adapter, on the same device");
+    if (given(6) && (!like_x(t[6]) || t[6].numel != out_f))
+        return PyErr_Format(PyExc_ValueError,
+                            "bias must be a contiguous tensor of %lld elements with x's dtype and device", out_f);
+    return Py_BuildValue("LLLiiKKKKKKK", (long long)x.shape[0], s, r, x.kind, x.device, (unsigned long long)x.ptr,
+                         (unsigned long long)t[1].ptr, (unsigned long long)A.ptr, (unsigned long long)B.ptr,
+                         (unsigned long long)t[4].ptr, (unsigned long long)t[5].ptr, (unsigned long long)t[6].ptr);
+}
+
 PyMethodDef kMethods[] = {
+    {"adapter_args", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adapter_args)), METH_FASTCALL,
+     "Checked arguments of the adapter calls."},
     {"adamw_table", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adamw_table)), METH_FASTCALL,
      "The table of ks_adamw_step from lists of tensors."},
     {nullptr, nullptr, 0, nullptr}};
