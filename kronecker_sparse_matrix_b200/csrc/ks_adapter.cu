@@ -200,7 +200,7 @@ __device__ void tile_list(const int *__restrict__ ids, int *__restrict__ lists, 
 // bf16, F a multiple of 8 and 16-byte aligned, on the tensor cores (mma.sync: the
 // operands of so narrow a product are read once each, straight into registers,
 // and a tcgen05 tile would first have to pass through shared memory).  A block
-// takes 32 rows and NT * 8 ranks, its eight warps every eighth 32 features.  Both
+// takes 16 MT rows and NT * 8 ranks, its eight warps every eighth 32 features.  Both
 // operands have the features contiguous, and a sum does not care which of them an
 // MMA calls its k: lane (g, t) loads the eight features 8 t .. 8 t + 7 of rows g
 // (X, and W) as one 16-byte vector, which is its share of two MMA steps.  The
@@ -211,17 +211,17 @@ __device__ __forceinline__ unsigned short *plane_at(unsigned short *planes, long
     return planes + n / 128 * (plane_r * 128) + (r >> 3) * 1024 + (int)(n % 128 >> 3) * 64 + (r & 7) * 8 + (int)(n & 7);
 }
 
-// Blocks of 32 rows with more adapters than this go row by row: a pass takes about
+// Blocks of rows with more adapters than this go row by row: a pass takes about
 // as long as six rows' dot products.
 constexpr int kMixed = 6;
 
-template <int NT, typename O>
+template <int MT, int NT, typename O>
 __global__ void __launch_bounds__(256)
     shrink_mma_kernel(const __nv_bfloat16 *__restrict__ X, const __nv_bfloat16 *__restrict__ W,
                       const float *__restrict__ scales, const int *__restrict__ ids, O *__restrict__ H, long long N,
                       int F, int R, int ldh, int S, unsigned *status, int row_blocks, int *__restrict__ lists,
                       int list_stride, unsigned short *__restrict__ planes, int plane_r) {
-    constexpr int MT = 2, ROWS = 16 * MT, RC = 8 * NT, LD = RC + 1;
+    constexpr int ROWS = 16 * MT, RC = 8 * NT, LD = RC + 1;
     __shared__ float red[4][ROWS][LD];
     __shared__ int row_id[ROWS], found[ROWS], n_found;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(256)
     const long long n0 = (long long)blockIdx.x * ROWS;
     const int r0 = blockIdx.y * RC;
     if (warp == 0) {
-        const int id = row_adapter(ids, n0 + lane, N, S, status);
-        row_id[lane] = id;
+        const int id = lane < ROWS ? row_adapter(ids, n0 + lane, N, S, status) : -1;
+        if (lane < ROWS) row_id[lane] = id;
         int count = 0;
         for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
             if (lane == 0) found[count] = s;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(256)
             const bool in = f < F;
             uint4 xv[2 * MT], wv[NT];
 #pragma unroll
-            for (int m = 0; m < 2 * MT; ++m) xv[m] = in ? x[m][f >> 3] : make_uint4(0u, 0u, 0u, 0u);
+            for (int m = 0; m < 2 * MT; ++m) xv[m] = in ? __ldg(x[m] + (f >> 3)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int j = 0; j < NT; ++j) wv[j] = in ? __ldg(w[j] + (f >> 3)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -355,6 +355,8 @@ __global__ void __launch_bounds__(256)
     put(Y + at, ep_apply(y, bias, f, act));
 }
 
+constexpr int kExpandRows = 8;
+
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
     const uint2 v = *reinterpret_cast<const uint2 *>(p);
@@ -368,17 +370,18 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
         make_uint2(*reinterpret_cast<const unsigned *>(&a), *reinterpret_cast<const unsigned *>(&b));
 }
 
-// F a multiple of 4 and vectors of four aligned: a thread owns four outputs of 16
+// F a multiple of 4 and vectors of four aligned: a thread owns four outputs of eight
 // rows and passes once over the weights of each adapter among them, four ranks at
-// a time; H is read from shared memory (the same address in a warp).
+// a time; H is read from shared memory (the same address in a warp), Y before the
+// products, so that its latency is theirs.
 // RC: the ranks are contiguous in W (B) and come in whole fours; otherwise the
 // features are (A).
-template <typename T, bool RC>
-__global__ void __launch_bounds__(128)
+template <typename T, bool RC, int ACT>
+__global__ void __launch_bounds__(128, 6)
     expand_kernel(T *__restrict__ Y, const T *__restrict__ W, const int *__restrict__ ids,
-                  const float *__restrict__ H, long long N, int F, int R, int ldh, int S, const T *__restrict__ bias,
-                  int act) {
-    constexpr int ROWS = 16;
+                  const float *__restrict__ H, long long N, int F, int R, int ldh, int S,
+                  const T *__restrict__ bias) {
+    constexpr int ROWS = kExpandRows;
     extern __shared__ float4 hs[];  // [rank / 4][row]
     __shared__ int row_id[ROWS];
     const long long n0 = (long long)blockIdx.x * ROWS;
@@ -393,9 +396,19 @@ __global__ void __launch_bounds__(128)
     __syncthreads();
     const int f = (blockIdx.y * 128 + threadIdx.x) * 4;
     const bool in = f < F;
+    T *y = Y + n0 * F + f;
     float4 acc[ROWS];
+    {
+        const float4 b = bias && in ? load4(bias + f) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int m = 0; m < ROWS; ++m) acc[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int m = 0; m < ROWS; ++m) {
+            acc[m] = b;
+            if (in && m < rows) {
+                const float4 v = load4(y + (long long)m * F);
+                acc[m] = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
+            }
+        }
+    }
     const int lane = threadIdx.x & 31;
     const int id = lane < ROWS ? row_id[lane] : -1;
     for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
@@ -434,17 +447,16 @@ __global__ void __launch_bounds__(128)
         }
     }
     if (!in) return;
-    float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (bias) b = load4(bias + f);
-    T *y = Y + n0 * F + f;
 #pragma unroll
     for (int m = 0; m < ROWS; ++m) {
         if (m < rows) {
-            float4 v = load4(y + (long long)m * F);
-            v.x = ep_act_fn(v.x + acc[m].x + b.x, act);
-            v.y = ep_act_fn(v.y + acc[m].y + b.y, act);
-            v.z = ep_act_fn(v.z + acc[m].z + b.z, act);
-            v.w = ep_act_fn(v.w + acc[m].w + b.w, act);
+            float4 v = acc[m];
+            if constexpr (ACT != KS_ACT_NONE) {
+                v.x = ep_act_fn(v.x, ACT);
+                v.y = ep_act_fn(v.y, ACT);
+                v.z = ep_act_fn(v.z, ACT);
+                v.w = ep_act_fn(v.w, ACT);
+            }
             store4(y + (long long)m * F, v);
         }
     }
@@ -549,7 +561,7 @@ __global__ void __launch_bounds__(128)
         float4 acc[RC];
 #pragma unroll
         for (int r = 0; r < RC; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
         for (int k = lo + warp; k < hi; k += 4) {
             const long long n = perm ? perm[k] : k;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -665,7 +677,7 @@ __global__ void __launch_bounds__(256)
                 for (int e = 0; e < 8; ++e) qs[r + e][k] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
             }
             __syncthreads();
-#pragma unroll 2
+#pragma unroll MT == 1 ? 4 : 2
             for (int k = 0; k < here; k += 16) {
                 uint4 x[4];
 #pragma unroll
@@ -717,23 +729,38 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// out = the sums of the slots of each adapter, in order of the chunks; r * rs + f * fs
-// is an entry's place in out[s].
+// out = the sums of the slots of each adapter.  A block takes 32 features and eight
+// ranks of one adapter; its eight warps every eighth chunk, and their sums are
+// added in order.  r * rs + f * fs is an entry's place in out[s].
 template <typename T>
 __global__ void __launch_bounds__(256)
     reduce_kernel(const float *__restrict__ W, const int *__restrict__ offsets, T *__restrict__ out, int N, int F,
                   int R, int rs, int fs, int chunk) {
-    const int s = blockIdx.y;
+    __shared__ float part[8][8][33];
+    const int s = blockIdx.y, r0 = blockIdx.z * 8, f0 = blockIdx.x * 32;
     const int lo = offsets ? offsets[s] : 0, hi = offsets ? offsets[s + 1] : s == 0 ? N : 0;
-    const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (at >= (long long)R * F) return;
-    float sum = 0.f;
-    if (lo < hi) {
-        const float *w = W + (long long)s * R * F + at;
-        for (int z = lo / chunk; z <= (hi - 1) / chunk; ++z) sum += w[(long long)z * R * F];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float sum[8] = {};
+    if (lo < hi && f0 + lane < F) {
+        const float *w = W + ((long long)s * R + r0) * F + f0 + lane;
+        const int last = (hi - 1) / chunk;
+#pragma unroll 2
+        for (int z = lo / chunk + warp; z <= last; z += 8)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (r0 + e < R) sum[e] += w[((long long)z * R + e) * F];
     }
-    const int r = (int)(at / F), f = (int)(at - (long long)r * F);
-    put(out + (long long)s * R * F + (long long)r * rs + (long long)f * fs, sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[warp][e][lane] = sum[e];
+    __syncthreads();
+    // neighbouring threads take neighbouring entries of out
+    const int r = rs == 1 ? threadIdx.x & 7 : threadIdx.x >> 5, f = rs == 1 ? threadIdx.x >> 3 : threadIdx.x & 31;
+    if (r0 + r < R && f0 + f < F) {
+        float v = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v += part[q][r][f];
+        put(out + (long long)s * R * F + (long long)(r0 + r) * rs + (long long)(f0 + f) * fs, v);
+    }
 }
 
 // The adapters' weights as the tensor-core product reads them: out[s][f][r], r < Rp
@@ -800,19 +827,21 @@ cudaError_t shrink_bf16(const Adapters &q, const void *X, const void *W, long lo
     if (by_rows(q, N, F) && !planes)
         return launch_shrink_rows(X, W, q.scales, q.ids, H, std::is_same_v<O, __nv_bfloat16>, N, F, q.R, ldh, q.S, true,
                                   q.st);
-    const int row_blocks = (int)((N + 31) / 32), list_blocks = lists ? (int)((list_tiles(N) + 7) / 8) : 0;
     const int plane_r = round_up(q.R, 16), cols = std::max(H ? ldh : 0, planes ? plane_r : 0);
     const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
+    // 16 rows a block for few ranks (more warps for X's latency), 32 for many (W is read half as often)
+    const int rows = nt <= 2 ? 16 : 32;
+    const int row_blocks = (int)((N + rows - 1) / rows), list_blocks = lists ? (int)((list_tiles(N) + 7) / 8) : 0;
     const dim3 grid((unsigned)(row_blocks + list_blocks), (unsigned)((cols + 8 * nt - 1) / (8 * nt)));
     const auto go = [&](auto kernel) {
         kernel<<<grid, 256, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S, device_status_ptr(), row_blocks,
                                        lists, list_stride(q.S), planes, plane_r);
     };
     switch (nt) {
-        case 1: go(shrink_mma_kernel<1, O>); break;
-        case 2: go(shrink_mma_kernel<2, O>); break;
-        case 4: go(shrink_mma_kernel<4, O>); break;
-        default: go(shrink_mma_kernel<8, O>); break;
+        case 1: go(shrink_mma_kernel<1, 1, O>); break;
+        case 2: go(shrink_mma_kernel<1, 2, O>); break;
+        case 4: go(shrink_mma_kernel<2, 4, O>); break;
+        default: go(shrink_mma_kernel<2, 8, O>); break;
     }
     return cudaGetLastError();
 }
@@ -838,15 +867,21 @@ cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long 
                    const void *bias, int act) {
     T *y = static_cast<T *>(Y);
     const T *w = static_cast<const T *>(W), *b = static_cast<const T *>(bias);
-    const size_t smem = (size_t)ldh * 16 * 4;
+    const size_t smem = (size_t)ldh * kExpandRows * 4;
     if (F % 4 == 0 && aligned(Y, 4 * sizeof(T)) && aligned(W, 4 * sizeof(T)) && aligned(bias, 4 * sizeof(T)) &&
-        (with_a || q.R % 4 == 0) && smem <= 40 * 1024 && (F + 511) / 512 <= 65535) {
-        const dim3 grid((unsigned)((N + 15) / 16), (unsigned)((F + 511) / 512));
-        if (with_a)
-            expand_kernel<T, false><<<grid, 128, smem, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, b, act);
-        else
-            expand_kernel<T, true><<<grid, 128, smem, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, b, act);
-        return cudaGetLastError();
+        (with_a || q.R % 4 == 0) && (F + 511) / 512 <= 65535) {
+        const dim3 grid((unsigned)((N + kExpandRows - 1) / kExpandRows), (unsigned)((F + 511) / 512));
+        const auto go = [&](auto kernel) {
+            kernel<<<grid, 128, smem, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, b);
+            return cudaGetLastError();
+        };
+        if (with_a) return go(expand_kernel<T, false, KS_ACT_NONE>);
+        switch (act) {
+            case KS_ACT_NONE: return go(expand_kernel<T, true, KS_ACT_NONE>);
+            case KS_ACT_RELU: return go(expand_kernel<T, true, KS_ACT_RELU>);
+            case KS_ACT_GELU_TANH: return go(expand_kernel<T, true, KS_ACT_GELU_TANH>);
+            default: return go(expand_kernel<T, true, KS_ACT_GELU_ERF>);
+        }
     }
     const int rs = with_a ? F : 1, fs = with_a ? 1 : q.R;
     const long long blocks = (N * F + 255) / 256;
@@ -922,7 +957,7 @@ cudaError_t grad(const Adapters &q, const GradPlan &g, const void *P, const Q *V
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int rs = with_a ? F : 1, fs = with_a ? 1 : q.R;
-    const dim3 rgrid((unsigned)(((long long)q.R * F + 255) / 256), (unsigned)q.S);
+    const dim3 rgrid((unsigned)((F + 31) / 32), (unsigned)q.S, (unsigned)((q.R + 7) / 8));
     if (q.bf16)
         reduce_kernel<<<rgrid, 256, 0, q.st>>>(W, offsets, static_cast<__nv_bfloat16 *>(out), n, F, q.R, rs, fs, g.chunk);
     else
