@@ -324,10 +324,11 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
  *     dB[s] = sum over the same rows of dY[n]^T H[n],
  * written, not accumulated, in the layouts of X, A and B; an adapter without
  * rows gets zeros.  Each of dX, dA, dB may be NULL: it is not computed (values
- * may be NULL without dX, X without dA and dB).  The gradients of the values
+ * may be NULL without dX, X without dA and dB), and the others have the bits that
+ * they have beside it.  The gradients of the values
  * and of the bias are ks_matmul_dv's and ks_bias_grad's.  Sums are fp32 in an
- * order that depends on the sizes and ids alone, so the results are
- * deterministic; bf16 gradients are rounded once.  No output may overlap an
+ * order that depends on the sizes, the ids and the alignment of the buffers alone, so
+ * the results are deterministic; bf16 gradients are rounded once.  No output may overlap an
  * input or another output.  batch == 0 writes zeros to dA and dB.  Limits, ids
  * and workspace are as for ks_adapter_matmul. */
 ks_status ks_adapter_backward(const void *dY, const void *X, const void *values, int64_t a, int64_t b, int64_t c,

@@ -34,15 +34,16 @@ namespace {
 
 // Any size, type and alignment: one warp per row.
 template <typename T, typename O>
-__global__ void __launch_bounds__(256)
-    shrink_any_kernel(const T *__restrict__ X, const T *__restrict__ W, const float *__restrict__ scales,
-                      const int *__restrict__ ids, O *__restrict__ H, long long N, int F, int R, int ldh, int S,
-                      unsigned *status) {
+__global__ void __launch_bounds__(256) shrink_any_kernel(const ShrinkArgs p) {
+    const ShrinkJob &job = p.job[blockIdx.z];
+    const T *const X = static_cast<const T *>(job.X), *const W = static_cast<const T *>(job.W);
+    const float *const scales = p.scales;
+    const int F = job.F, R = p.R, ldh = p.ldh;
     const int lane = threadIdx.x & 31;
     const long long n = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (n >= N) return;
-    const int s = row_adapter(ids, n, N, S, status);
-    O *h = H + n * ldh;
+    if (n >= p.N) return;
+    const int s = row_adapter(p.ids, n, p.N, p.S, p.status);
+    O *h = static_cast<O *>(job.H) + n * ldh;
     if (s < 0) {
         for (int r = lane; r < ldh; r += 32) put(h + r, 0.f);
         return;
@@ -76,14 +77,18 @@ __device__ __forceinline__ int next_id(int id, int last) {
 // the end: 62 shuffles for the 64 sums, each exchange halving what a lane holds.
 // An adapter's pass runs over all eight rows and keeps those that take it.
 // Bound by X for few ranks (16 FMAs for each 16 bytes a lane loads).
-__global__ void __launch_bounds__(128)
-    shrink_fp32_kernel(const float *__restrict__ X, const float *__restrict__ W, const float *__restrict__ scales,
-                       const int *__restrict__ ids, float *__restrict__ H, long long N, int F, int R, int ldh, int S,
-                       unsigned *status) {
+__global__ void __launch_bounds__(128) shrink_fp32_kernel(const ShrinkArgs p) {
+    const ShrinkJob &job = p.job[blockIdx.z];
+    const float *__restrict__ const X = static_cast<const float *>(job.X);
+    const float *__restrict__ const W = static_cast<const float *>(job.W);
+    float *__restrict__ const H = static_cast<float *>(job.H);
+    const float *const scales = p.scales;
+    const long long N = p.N;
+    const int F = job.F, R = p.R, ldh = p.ldh;
     const int lane = threadIdx.x & 31;
     const long long n0 = ((long long)blockIdx.x * 4 + (threadIdx.x >> 5)) * 8;
     if (n0 >= N) return;
-    const int id = lane < 8 ? row_adapter(ids, n0 + lane, N, S, status) : -1;
+    const int id = lane < 8 ? row_adapter(p.ids, n0 + lane, N, p.S, p.status) : -1;
     const int row = lane >> 2;  // the row and ranks (2 q, 2 q + 1) whose sums end in this lane
     const long long n = n0 + row;
     if (__shfl_sync(0xFFFFFFFFu, id, row) < 0 && n < N)
@@ -217,23 +222,29 @@ constexpr int kMixed = 6;
 
 template <int MT, int NT, typename O>
 __global__ void __launch_bounds__(256)
-    shrink_mma_kernel(const __nv_bfloat16 *__restrict__ X, const __nv_bfloat16 *__restrict__ W,
-                      const float *__restrict__ scales, const int *__restrict__ ids, O *__restrict__ H, long long N,
-                      int F, int R, int ldh, int S, unsigned *status, int row_blocks, int *__restrict__ lists,
-                      int list_stride, unsigned short *__restrict__ planes, int plane_r) {
+    shrink_mma_kernel(const ShrinkArgs p, int row_blocks, int *__restrict__ lists, int list_stride) {
+    const ShrinkJob &job = p.job[blockIdx.z];
+    const __nv_bfloat16 *__restrict__ const X = static_cast<const __nv_bfloat16 *>(job.X);
+    const __nv_bfloat16 *__restrict__ const W = static_cast<const __nv_bfloat16 *>(job.W);
+    O *__restrict__ const H = static_cast<O *>(job.H);
+    unsigned short *__restrict__ const planes = job.planes;
+    const float *const scales = p.scales;
+    const long long N = p.N;
+    const int F = job.F, R = p.R, ldh = p.ldh, plane_r = p.plane_r;
     constexpr int ROWS = 16 * MT, RC = 8 * NT, LD = RC + 1;
     __shared__ float red[4][ROWS][LD];
     __shared__ int row_id[ROWS], found[ROWS], n_found;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((int)blockIdx.x >= row_blocks) {
         const long long tile = (long long)(blockIdx.x - row_blocks) * 8 + warp;
-        if (blockIdx.y == 0 && tile * 128 < N) tile_list(ids, lists, list_stride, N, S, tile, lane);
+        if (blockIdx.y == 0 && blockIdx.z == 0 && tile * 128 < N)
+            tile_list(p.ids, lists, list_stride, N, p.S, tile, lane);
         return;
     }
     const long long n0 = (long long)blockIdx.x * ROWS;
     const int r0 = blockIdx.y * RC;
     if (warp == 0) {
-        const int id = lane < ROWS ? row_adapter(ids, n0 + lane, N, S, status) : -1;
+        const int id = lane < ROWS ? row_adapter(p.ids, n0 + lane, N, p.S, p.status) : -1;
         if (lane < ROWS) row_id[lane] = id;
         int count = 0;
         for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
@@ -465,13 +476,13 @@ __global__ void __launch_bounds__(128, 6)
 // ---------------------------------------------------------------- dA and dB
 
 // The rows of each adapter in order: perm[offsets[s] .. offsets[s + 1]) holds the
-// rows with id s.  Block s counts the rows of smaller ids and of its own, then
+// rows with id s.  The block counts the rows of smaller ids and of its own, then
 // writes its own in row order.
-__global__ void __launch_bounds__(1024)
-    order_kernel(const int *__restrict__ ids, int *__restrict__ perm, int *__restrict__ offsets, int N, int S) {
+__device__ void order_rows(const int *__restrict__ ids, int *__restrict__ perm, int *__restrict__ offsets, int N, int S,
+                           int s) {
     __shared__ int warp_n[32];
     __shared__ int base_sh, total_sh;
-    const int s = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     int less = 0;
     for (int n = t; n < N; n += 1024) {
         const int id = ids[n];
@@ -515,6 +526,52 @@ __global__ void __launch_bounds__(1024)
 }
 
 
+// What a backward pass has to lay out first, in one launch of blocks of 1024 threads:
+// transposed copies out[q][c][r] = in[q][r][c] of `blocks` blocks of rows x cols (32 x
+// 32 tiles; out's rows are ld long, zeros past `rows`), and the rows of each adapter.
+struct Transpose {
+    const void *in;
+    void *out;
+    long long blocks;
+    int rows, cols, ld, tr, tc;  // tr, tc: tiles along ld and cols
+    long long tiles;
+};
+struct PrepareArgs {
+    Transpose job[3];
+    const int *ids;
+    int *perm, *offsets;
+    int N, S;
+    int sorted;  // blocks that order rows (S or 0), before the tiles
+};
+template <typename T>
+__global__ void __launch_bounds__(1024) prepare_kernel(const PrepareArgs p) {
+    if ((int)blockIdx.x < p.sorted) {
+        order_rows(p.ids, p.perm, p.offsets, p.N, p.S, (int)blockIdx.x);
+        return;
+    }
+    __shared__ T tile[32][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const long long step = gridDim.x - p.sorted;
+    long long at = blockIdx.x - p.sorted;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const Transpose &q = p.job[j];
+        for (; at < q.tiles; at += step) {
+            const long long blk = at / (q.tr * q.tc);
+            const int rest = (int)(at - blk * (q.tr * q.tc)), r0 = rest / q.tc * 32, c0 = rest % q.tc * 32;
+            const T *in = static_cast<const T *>(q.in) + blk * q.rows * q.cols;
+            T v{};
+            if (r0 + y < q.rows && c0 + x < q.cols) v = in[(long long)(r0 + y) * q.cols + c0 + x];
+            tile[y][x] = v;
+            __syncthreads();
+            if (c0 + y < q.cols && r0 + x < q.ld)
+                static_cast<T *>(q.out)[(blk * q.cols + c0 + y) * q.ld + r0 + x] = tile[x][y];
+            __syncthreads();
+        }
+        at -= q.tiles;
+    }
+}
+
 // A gradient is out[s][f][r] = sum over the rows n of adapter s of P[n][f] Q[n][r]
 // (dA: P = X, Q = G; dB: P = dY, Q = H).  The rows in the adapters' order are cut
 // into chunks of `chunk` positions; a block takes some features of one chunk and
@@ -540,17 +597,36 @@ __device__ __forceinline__ int adapter_at(const int *offsets, int S, int p) {
     return a;
 }
 
+// One or two gradients (dA, dB) of a launch: the features of both, one after the
+// other, are dealt to blockIdx.x.
+struct GradJob {
+    const void *P, *V;  // V: batch x ldh
+    float *W;           // partial sums: (chunks + S) x R x F
+    void *out;          // entry (r, f) of out[s] at r * rs + f * fs
+    int F, rs, fs;
+};
+struct GradArgs {
+    GradJob job[2];
+    const int *perm, *offsets;
+    int N, R, ldh, S, chunk;
+    int first;  // blocks of job[0]
+};
+
 // fp32: a warp takes 128 features (four a lane) and every fourth row of the chunk,
 // RC ranks of each; Q's row is the same address in a warp.  64 FMAs (RC = 16) for
 // each 16 bytes of P a lane loads.  Types and alignment: any (VEC: vectors of four).
 template <typename T, typename Q, int RC, bool VEC>
-__global__ void __launch_bounds__(128)
-    grad_kernel(const T *__restrict__ P, const Q *__restrict__ V, const int *__restrict__ perm,
-                const int *__restrict__ offsets, float *__restrict__ W, int N, int F, int R, int ldh, int S,
-                int chunk) {
+__global__ void __launch_bounds__(128) grad_kernel(const GradArgs a) {
+    const GradJob &job = a.job[(int)blockIdx.x >= a.first];
+    const int bx = (int)blockIdx.x >= a.first ? (int)blockIdx.x - a.first : (int)blockIdx.x;
+    const T *__restrict__ const P = static_cast<const T *>(job.P);
+    const Q *__restrict__ const V = static_cast<const Q *>(job.V);
+    const int *__restrict__ const perm = a.perm, *__restrict__ const offsets = a.offsets;
+    float *__restrict__ const W = job.W;
+    const int N = a.N, F = job.F, R = a.R, ldh = a.ldh, S = a.S, chunk = a.chunk;
     __shared__ float4 red[3][RC][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int f = (blockIdx.x * 32 + lane) * 4, r0 = blockIdx.z * RC;
+    const int f = (bx * 32 + lane) * 4, r0 = blockIdx.z * RC;
     const int total = offsets ? offsets[S] : N;
     const int begin = blockIdx.y * chunk, end = min(begin + chunk, total);
     if (begin >= end) return;
@@ -599,20 +675,20 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
             for (int r = 0; r < RC; ++r) {
                 if (r0 + r >= R) break;
-                float4 a = acc[r];
+                float4 v = acc[r];
 #pragma unroll
                 for (int q = 0; q < 3; ++q) {
                     const float4 b = red[q][r][lane];
-                    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+                    v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
                 }
                 float *d = w + (long long)(r0 + r) * F + f;
                 if (f + 3 < F && F % 4 == 0) {
-                    store4(d, a);
+                    store4(d, v);
                 } else {
-                    if (f < F) d[0] = a.x;
-                    if (f + 1 < F) d[1] = a.y;
-                    if (f + 2 < F) d[2] = a.z;
-                    if (f + 3 < F) d[3] = a.w;
+                    if (f < F) d[0] = v.x;
+                    if (f + 1 < F) d[1] = v.y;
+                    if (f + 2 < F) d[2] = v.z;
+                    if (f + 3 < F) d[3] = v.w;
                 }
             }
         }
@@ -642,15 +718,19 @@ __device__ __forceinline__ uint4 load8_bf16(const float *p) {
 // or so, is staged transposed in shared memory, 128 positions at a time.  Bound by
 // P's bytes.  Q is rounded to bf16 where it is fp32.
 template <int MT, typename Q>
-__global__ void __launch_bounds__(256)
-    grad_mma_kernel(const __nv_bfloat16 *__restrict__ P, const Q *__restrict__ V, const int *__restrict__ perm,
-                    const int *__restrict__ offsets, float *__restrict__ W, int N, int F, int R, int ldh, int S,
-                    int chunk) {
+__global__ void __launch_bounds__(256) grad_mma_kernel(const GradArgs a) {
+    const GradJob &job = a.job[(int)blockIdx.x >= a.first];
+    const int bx = (int)blockIdx.x >= a.first ? (int)blockIdx.x - a.first : (int)blockIdx.x;
+    const __nv_bfloat16 *__restrict__ const P = static_cast<const __nv_bfloat16 *>(job.P);
+    const Q *__restrict__ const V = static_cast<const Q *>(job.V);
+    const int *__restrict__ const perm = a.perm, *__restrict__ const offsets = a.offsets;
+    float *__restrict__ const W = job.W;
+    const int N = a.N, F = job.F, R = a.R, ldh = a.ldh, S = a.S, chunk = a.chunk;
     constexpr int RC = 16 * MT, POS = 128, LD = POS + 16;  // 72 words a row: 8-byte reads of four rows hit all banks
     __shared__ __align__(16) unsigned short qs[RC][LD];
     __shared__ int rows[POS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int f0 = (blockIdx.x * (blockDim.x >> 5) + warp) * 64, r0 = blockIdx.z * RC;
+    const int f0 = (bx * (blockDim.x >> 5) + warp) * 64, r0 = blockIdx.z * RC;
     const int total = offsets ? offsets[S] : N;
     const int begin = blockIdx.y * chunk, end = min(begin + chunk, total);
     if (begin >= end) return;
@@ -690,11 +770,11 @@ __global__ void __launch_bounds__(256)
                                            {x[1].x, x[1].y, x[1].z, x[1].w},
                                            {x[2].x, x[2].y, x[2].z, x[2].w},
                                            {x[3].x, x[3].y, x[3].z, x[3].w}};
-                uint2 a[MT][2];
+                uint2 qa[MT][2];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    a[m][0] = *reinterpret_cast<const uint2 *>(&qs[16 * m + g][k + 4 * t]);
-                    a[m][1] = *reinterpret_cast<const uint2 *>(&qs[16 * m + g + 8][k + 4 * t]);
+                    qa[m][0] = *reinterpret_cast<const uint2 *>(&qs[16 * m + g][k + 4 * t]);
+                    qa[m][1] = *reinterpret_cast<const uint2 *>(&qs[16 * m + g + 8][k + 4 * t]);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -703,7 +783,7 @@ __global__ void __launch_bounds__(256)
                     const unsigned b1 = __byte_perm(xw[2][j >> 1], xw[3][j >> 1], sel);
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
-                        mma16816(acc[m][j], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, b0, b1);
+                        mma16816(acc[m][j], qa[m][0].x, qa[m][1].x, qa[m][0].y, qa[m][1].y, b0, b1);
                 }
             }
         }
@@ -733,12 +813,15 @@ __global__ void __launch_bounds__(256)
 // ranks of one adapter; its eight warps every eighth chunk, and their sums are
 // added in order.  r * rs + f * fs is an entry's place in out[s].
 template <typename T>
-__global__ void __launch_bounds__(256)
-    reduce_kernel(const float *__restrict__ W, const int *__restrict__ offsets, T *__restrict__ out, int N, int F,
-                  int R, int rs, int fs, int chunk) {
+__global__ void __launch_bounds__(256) reduce_kernel(const GradArgs a) {
     __shared__ float part[8][8][33];
-    const int s = blockIdx.y, r0 = blockIdx.z * 8, f0 = blockIdx.x * 32;
-    const int lo = offsets ? offsets[s] : 0, hi = offsets ? offsets[s + 1] : s == 0 ? N : 0;
+    const GradJob &job = a.job[(int)blockIdx.x >= a.first];
+    const float *__restrict__ const W = job.W;
+    const int *__restrict__ const offsets = a.offsets;
+    const int F = job.F, R = a.R, rs = job.rs, fs = job.fs, chunk = a.chunk;
+    const int s = blockIdx.y, r0 = blockIdx.z * 8;
+    const int f0 = ((int)blockIdx.x >= a.first ? (int)blockIdx.x - a.first : (int)blockIdx.x) * 32;
+    const int lo = offsets ? offsets[s] : 0, hi = offsets ? offsets[s + 1] : s == 0 ? a.N : 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float sum[8] = {};
     if (lo < hi && f0 + lane < F) {
@@ -759,28 +842,24 @@ __global__ void __launch_bounds__(256)
         float v = 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) v += part[q][r][f];
-        put(out + (long long)s * R * F + (long long)(r0 + r) * rs + (long long)(f0 + f) * fs, v);
+        put(static_cast<T *>(job.out) + (long long)s * R * F + (long long)(r0 + r) * rs + (long long)(f0 + f) * fs, v);
     }
 }
 
-// The adapters' weights as the tensor-core product reads them: out[s][f][r], r < Rp
-// (a multiple of 8), zero past R, from W[s][r * rs + f * fs].
+// B as the tensor-core product reads it: out[s][f][r], r < Rp (a multiple of 8), zeros past R.
 __global__ void __launch_bounds__(256)
-    pack_kernel(const unsigned short *__restrict__ W, unsigned short *__restrict__ out, int S, int F, int R, int Rp,
-                int rs, int fs) {
+    pack_kernel(const unsigned short *__restrict__ W, unsigned short *__restrict__ out, int S, int F, int R, int Rp) {
     const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
     const int octets = Rp / 8;
     if (at >= (long long)S * octets * F) return;
-    const int f = (int)(at % F), o = (int)(at / F % octets);
-    const long long s = at / F / octets;
-    const unsigned short *w = W + s * R * F + (long long)f * fs;
+    const long long row = at / octets;
+    const int o = (int)(at - row * octets);
+    const unsigned short *w = W + row * R;
     unsigned v[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int r = 8 * o + e;
-        if (r < R) v[e >> 1] |= (unsigned)w[(long long)r * rs] << (16 * (e & 1));
-    }
-    *reinterpret_cast<uint4 *>(out + (s * F + f) * Rp + 8 * o) = make_uint4(v[0], v[1], v[2], v[3]);
+    for (int e = 0; e < 8; ++e)
+        if (8 * o + e < R) v[e >> 1] |= (unsigned)w[8 * o + e] << (16 * (e & 1));
+    *reinterpret_cast<uint4 *>(out + row * Rp + 8 * o) = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // ---------------------------------------------------------------- host side
@@ -814,51 +893,58 @@ bool by_rows(const Adapters &q, long long N, int F) {
     return (double)N * q.R * F * (q.bf16 ? 2 : 4) <= (q.bf16 ? 16e6 : 64e6);
 }
 
-// lists, planes: null, or for the tensor-core product; H may then be null.
-template <typename O>
-cudaError_t shrink_bf16(const Adapters &q, const void *X, const void *W, long long N, int F, O *H, int ldh,
-                        int *lists, unsigned short *planes) {
-    const auto *x = static_cast<const __nv_bfloat16 *>(X), *w = static_cast<const __nv_bfloat16 *>(W);
-    if (!shrink_vec(q, X, W, F)) {  // (with lists the caller has made sure of vectors)
-        shrink_any_kernel<<<(unsigned)((N + 7) / 8), 256, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S,
-                                                                     device_status_ptr());
+// H = scale X W^T of one or two jobs.  h_bf16: their H are bf16; lists: null, or the
+// lists of the tensor-core product to be built (its planes are job[0]'s; the caller
+// has made sure of vectors); few: row by row (by_rows).
+cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf16, long long N, int ldh, int *lists,
+                   bool few) {
+    ShrinkArgs p{};
+    bool vec = true;
+    for (int j = 0; j < jobs; ++j) {
+        p.job[j] = job[j];
+        vec = vec && shrink_vec(q, job[j].X, job[j].W, job[j].F);
+    }
+    p.scales = q.scales, p.ids = q.ids, p.N = N, p.R = q.R, p.ldh = ldh, p.S = q.S;
+    p.plane_r = round_up(q.R, 16);
+    p.status = device_status_ptr();
+    const unsigned z = (unsigned)jobs;
+    if (!vec && jobs == 2) {  // each as it can
+        const cudaError_t e = shrink(q, job, 1, h_bf16, N, ldh, lists, few);
+        return e == cudaSuccess ? shrink(q, job + 1, 1, h_bf16, N, ldh, nullptr, few) : e;
+    }
+    if (!vec) {
+        const dim3 grid((unsigned)((N + 7) / 8), 1, z);
+        if (!q.bf16)
+            shrink_any_kernel<float, float><<<grid, 256, 0, q.st>>>(p);
+        else if (h_bf16)
+            shrink_any_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, q.st>>>(p);
+        else
+            shrink_any_kernel<__nv_bfloat16, float><<<grid, 256, 0, q.st>>>(p);
         return cudaGetLastError();
     }
-    if (by_rows(q, N, F) && !planes)
-        return launch_shrink_rows(X, W, q.scales, q.ids, H, std::is_same_v<O, __nv_bfloat16>, N, F, q.R, ldh, q.S, true,
-                                  q.st);
-    const int plane_r = round_up(q.R, 16), cols = std::max(H ? ldh : 0, planes ? plane_r : 0);
+    if (few) return launch_shrink_rows(p, jobs, q.bf16, h_bf16, q.st);
+    if (!q.bf16) {
+        shrink_fp32_kernel<<<dim3((unsigned)((N + 31) / 32), 1, z), 128, 0, q.st>>>(p);
+        return cudaGetLastError();
+    }
+    const int cols = lists ? std::max(ldh, p.plane_r) : ldh;
     const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
     // 16 rows a block for few ranks (more warps for X's latency), 32 for many (W is read half as often)
     const int rows = nt <= 2 ? 16 : 32;
     const int row_blocks = (int)((N + rows - 1) / rows), list_blocks = lists ? (int)((list_tiles(N) + 7) / 8) : 0;
-    const dim3 grid((unsigned)(row_blocks + list_blocks), (unsigned)((cols + 8 * nt - 1) / (8 * nt)));
+    const dim3 grid((unsigned)(row_blocks + list_blocks), (unsigned)((cols + 8 * nt - 1) / (8 * nt)), z);
     const auto go = [&](auto kernel) {
-        kernel<<<grid, 256, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S, device_status_ptr(), row_blocks,
-                                       lists, list_stride(q.S), planes, plane_r);
+        kernel<<<grid, 256, 0, q.st>>>(p, row_blocks, lists, list_stride(q.S));
+        return cudaGetLastError();
     };
-    switch (nt) {
-        case 1: go(shrink_mma_kernel<1, 1, O>); break;
-        case 2: go(shrink_mma_kernel<1, 2, O>); break;
-        case 4: go(shrink_mma_kernel<2, 4, O>); break;
-        default: go(shrink_mma_kernel<2, 8, O>); break;
-    }
-    return cudaGetLastError();
-}
-
-// H = scale X W^T, fp32.
-cudaError_t shrink_fp32_out(const Adapters &q, const void *X, const void *W, long long N, int F, float *H, int ldh) {
-    if (q.bf16) return shrink_bf16<float>(q, X, W, N, F, H, ldh, nullptr, nullptr);
-    const auto *x = static_cast<const float *>(X), *w = static_cast<const float *>(W);
-    if (by_rows(q, N, F) && shrink_vec(q, X, W, F))
-        return launch_shrink_rows(X, W, q.scales, q.ids, H, false, N, F, q.R, ldh, q.S, false, q.st);
-    if (shrink_vec(q, X, W, F))
-        shrink_fp32_kernel<<<(unsigned)((N + 31) / 32), 128, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S,
-                                                                        device_status_ptr());
-    else
-        shrink_any_kernel<<<(unsigned)((N + 7) / 8), 256, 0, q.st>>>(x, w, q.scales, q.ids, H, N, F, q.R, ldh, q.S,
-                                                                     device_status_ptr());
-    return cudaGetLastError();
+    const auto ranks = [&](auto h) {
+        using O = decltype(h);
+        return nt == 1   ? go(shrink_mma_kernel<1, 1, O>)
+               : nt == 2 ? go(shrink_mma_kernel<1, 2, O>)
+               : nt == 4 ? go(shrink_mma_kernel<2, 4, O>)
+                         : go(shrink_mma_kernel<2, 8, O>);
+    };
+    return h_bf16 ? ranks(__nv_bfloat16{}) : ranks(float{});
 }
 
 // Y = act(Y + bias + H W); with_a: W is A (rank x F), else B (F x rank).
@@ -890,78 +976,83 @@ cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long 
     return cudaGetLastError();
 }
 
-// How a gradient of width F is cut: `bx` blocks of features, `bz` of ranks, chunks of
-// `chunk` of the N rows, about four blocks for each SM.
+// How the gradients (dA, dB; out null: not wanted) are cut: feature blocks of each,
+// `bz` blocks of ranks, chunks of `chunk` of the N rows, for about two blocks of
+// eight warps an SM.
 struct GradPlan {
-    bool mma;
-    int warps, bx, bz, rc, chunk, chunks;
-    size_t bytes;  // of the partial sums
+    bool mma, vec;
+    int warps, bx[2], bz, rc, chunk, chunks;
+    size_t at[2], bytes;  // partial sums of each, and of both
 };
-GradPlan grad_plan(const Adapters &q, const void *P, long long N, int F) {
+GradPlan grad_plan(const Adapters &q, const GradJob (&job)[2], long long N) {
     GradPlan g{};
-    g.mma = q.bf16 && F % 8 == 0 && aligned(P, 16);
-    if (g.mma) {
-        g.warps = std::min(8, (F + 63) / 64);
-        g.bx = (F + 64 * g.warps - 1) / (64 * g.warps);
-        g.rc = std::min(64, round_up(q.R, 16));
-        if (g.rc == 48) g.rc = 64;
-    } else {
-        g.warps = 4;
-        g.bx = (F + 127) / 128;
-        g.rc = q.R <= 8 ? 8 : 16;
-    }
+    const int widest = std::max(job[0].F, job[1].F);
+    const auto vectors = [&](int v) {
+        return job[0].F % v == 0 && job[1].F % v == 0 && aligned(job[0].P, 16) && aligned(job[1].P, 16);
+    };
+    g.mma = q.bf16 && vectors(8);
+    g.vec = !q.bf16 && vectors(4);
+    g.warps = g.mma ? std::min(8, (widest + 63) / 64) : 4;
+    const int features = g.mma ? 64 * g.warps : 128;
+    g.rc = g.mma ? (q.R <= 16 ? 16 : q.R <= 32 ? 32 : 64) : q.R <= 8 ? 8 : 16;
     g.bz = (q.R + g.rc - 1) / g.rc;
-    const long long wanted = std::max<long long>(1, 4LL * sm_count() * 4 / g.warps / ((long long)g.bx * g.bz));
-    const int least = 64;
-    long long chunk = std::max<long long>(least, (N + wanted - 1) / wanted);
-    chunk = std::min<long long>((chunk + 15) / 16 * 16, std::max<long long>(16, (N + 15) / 16 * 16));
+    long long blocks = 0;
+    for (int j = 0; j < 2; ++j) blocks += g.bx[j] = (job[j].F + features - 1) / features;
+    const long long wanted = std::max<long long>(1, 2LL * sm_count() * 8 / g.warps / (blocks * g.bz));
+    long long chunk = std::max<long long>(64, (N + wanted - 1) / wanted);
+    chunk = std::min<long long>((chunk + 15) / 16 * 16, (N + 15) / 16 * 16);
     chunk = std::max<long long>(chunk, (N + 65534) / 65535);  // grid limit
     g.chunk = (int)chunk;
     g.chunks = (int)((N + chunk - 1) / chunk);
-    g.bytes = (size_t)(g.chunks + q.S) * (size_t)q.R * (size_t)F * 4;
+    for (int j = 0; j < 2; ++j) {
+        if (!job[j].out) {
+            g.bx[j] = 0;
+            continue;
+        }
+        g.at[j] = g.bytes;
+        g.bytes += ((size_t)(g.chunks + q.S) * (size_t)q.R * (size_t)job[j].F * 4 + 255) / 256 * 256;
+    }
     return g;
 }
 
-template <typename Q>
-cudaError_t grad(const Adapters &q, const GradPlan &g, const void *P, const Q *V, int ldh, const int *perm,
-                 const int *offsets, void *out, bool with_a, long long N, int F, float *W) {
-    const dim3 grid((unsigned)g.bx, (unsigned)g.chunks, (unsigned)g.bz);
-    const int n = (int)N;
-    if (g.mma) {
-        const auto *p = static_cast<const __nv_bfloat16 *>(P);
-        const auto go = [&](auto kernel) {
-            kernel<<<grid, 32 * g.warps, 0, q.st>>>(p, V, perm, offsets, W, n, F, q.R, ldh, q.S, g.chunk);
-        };
-        if (g.rc == 16)
-            go(grad_mma_kernel<1, Q>);
-        else if (g.rc == 32)
-            go(grad_mma_kernel<2, Q>);
-        else
-            go(grad_mma_kernel<4, Q>);
-    } else {
-        const auto go = [&](auto kernel, const auto *p) {
-            kernel<<<grid, 128, 0, q.st>>>(p, V, perm, offsets, W, n, F, q.R, ldh, q.S, g.chunk);
-        };
-        if (q.bf16) {
-            const auto *p = static_cast<const __nv_bfloat16 *>(P);
-            g.rc == 8 ? go(grad_kernel<__nv_bfloat16, Q, 8, false>, p) : go(grad_kernel<__nv_bfloat16, Q, 16, false>, p);
-        } else {
-            const auto *p = static_cast<const float *>(P);
-            const bool vec = F % 4 == 0 && aligned(P, 16);
-            if (g.rc == 8)
-                vec ? go(grad_kernel<float, Q, 8, true>, p) : go(grad_kernel<float, Q, 8, false>, p);
-            else
-                vec ? go(grad_kernel<float, Q, 16, true>, p) : go(grad_kernel<float, Q, 16, false>, p);
-        }
+cudaError_t grads(const Adapters &q, const GradPlan &g, const GradJob (&job)[2], bool v_bf16, int ldh,
+                  const int *perm, const int *offsets, long long N, char *W) {
+    GradArgs p{};
+    int reduce_blocks[2] = {};
+    for (int j = 0; j < 2; ++j) {
+        p.job[j] = job[j];
+        p.job[j].W = reinterpret_cast<float *>(W + g.at[j]);
+        if (job[j].out) reduce_blocks[j] = (job[j].F + 31) / 32;
     }
-    cudaError_t e = cudaGetLastError();
+    p.perm = perm, p.offsets = offsets, p.N = (int)N, p.R = q.R, p.ldh = ldh, p.S = q.S, p.chunk = g.chunk;
+    p.first = g.bx[0];
+    const dim3 grid((unsigned)(g.bx[0] + g.bx[1]), (unsigned)g.chunks, (unsigned)g.bz);
+    const auto go = [&](auto kernel) {
+        kernel<<<grid, 32 * g.warps, 0, q.st>>>(p);
+        return cudaGetLastError();
+    };
+    const auto typed = [&](auto v) {
+        using V = decltype(v);
+        if (g.mma)
+            return g.rc == 16   ? go(grad_mma_kernel<1, V>)
+                   : g.rc == 32 ? go(grad_mma_kernel<2, V>)
+                                : go(grad_mma_kernel<4, V>);
+        if (q.bf16)
+            return g.rc == 8 ? go(grad_kernel<__nv_bfloat16, V, 8, false>) : go(grad_kernel<__nv_bfloat16, V, 16, false>);
+        if constexpr (std::is_same_v<V, float>) {
+            if (g.rc == 8) return g.vec ? go(grad_kernel<float, V, 8, true>) : go(grad_kernel<float, V, 8, false>);
+            return g.vec ? go(grad_kernel<float, V, 16, true>) : go(grad_kernel<float, V, 16, false>);
+        }
+        return cudaErrorInvalidConfiguration;
+    };
+    cudaError_t e = v_bf16 ? typed(__nv_bfloat16{}) : typed(float{});
     if (e != cudaSuccess) return e;
-    const int rs = with_a ? F : 1, fs = with_a ? 1 : q.R;
-    const dim3 rgrid((unsigned)((F + 31) / 32), (unsigned)q.S, (unsigned)((q.R + 7) / 8));
+    p.first = reduce_blocks[0];
+    const dim3 rgrid((unsigned)(reduce_blocks[0] + reduce_blocks[1]), (unsigned)q.S, (unsigned)((q.R + 7) / 8));
     if (q.bf16)
-        reduce_kernel<<<rgrid, 256, 0, q.st>>>(W, offsets, static_cast<__nv_bfloat16 *>(out), n, F, q.R, rs, fs, g.chunk);
+        reduce_kernel<__nv_bfloat16><<<rgrid, 256, 0, q.st>>>(p);
     else
-        reduce_kernel<<<rgrid, 256, 0, q.st>>>(W, offsets, static_cast<float *>(out), n, F, q.R, rs, fs, g.chunk);
+        reduce_kernel<float><<<rgrid, 256, 0, q.st>>>(p);
     return cudaGetLastError();
 }
 
@@ -1032,12 +1123,31 @@ bool fuses(const Adapters &q, Problem p, const void *A, int F, const void *bias)
            tc_adapters_supported(p, tc) && shrink_vec(q, p.X, A, F);
 }
 
-cudaError_t pack(const Adapters &q, const void *W, void *out, int F, int Rp, bool with_a) {
+cudaError_t pack(const Adapters &q, const void *W, void *out, int F, int Rp) {
     const long long n = (long long)q.S * F * (Rp / 8);
     if ((n + 255) / 256 > INT_MAX) return cudaErrorInvalidConfiguration;
     pack_kernel<<<(unsigned)((n + 255) / 256), 256, 0, q.st>>>(static_cast<const unsigned short *>(W),
-                                                               static_cast<unsigned short *>(out), q.S, F, q.R, Rp,
-                                                               with_a ? F : 1, with_a ? 1 : q.R);
+                                                               static_cast<unsigned short *>(out), q.S, F, q.R, Rp);
+    return cudaGetLastError();
+}
+
+// A transpose of prepare_kernel: out[q][c][r] = in[q][r][c], rows of out ld long.
+Transpose transpose(const void *in, void *out, long long blocks, long long rows, long long cols, long long ld) {
+    Transpose t{in, out, blocks, (int)rows, (int)cols, (int)ld, (int)((ld + 31) / 32), (int)((cols + 31) / 32), 0};
+    t.tiles = blocks * t.tr * t.tc;
+    return t;
+}
+
+cudaError_t prepare(const Adapters &q, PrepareArgs &p, long long N) {
+    long long tiles = 0;
+    for (const Transpose &t : p.job) tiles += t.tiles;
+    const long long blocks = p.sorted + std::min<long long>(tiles, 2LL * sm_count() * 4);
+    if (blocks == 0) return cudaSuccess;
+    p.ids = q.ids, p.N = (int)N, p.S = q.S;
+    if (q.bf16)
+        prepare_kernel<unsigned short><<<(unsigned)blocks, 1024, 0, q.st>>>(p);
+    else
+        prepare_kernel<float><<<(unsigned)blocks, 1024, 0, q.st>>>(p);
     return cudaGetLastError();
 }
 
@@ -1088,7 +1198,8 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         }
         if ((s = alloc(&w, (size_t)batch * row_ldh * 4, q.st)) != KS_OK) return s;
         float *H = reinterpret_cast<float *>(w);
-        e = launch_shrink_rows(X, A, scales, ids, H, false, batch, in_f, q.R, row_ldh, q.S, q.bf16, q.st);
+        const ShrinkArgs h{{{X, A, H, nullptr, in_f}}, scales, ids, batch, q.R, row_ldh, q.S, 0, device_status_ptr()};
+        e = launch_shrink_rows(h, 1, q.bf16, false, q.st);
         if (e == cudaSuccess) e = launch_adapter_rows(p, A, B, scales, ids, q.S, q.R, H, row_ldh);
     } else if (fuses(q, p, A, in_f, bias)) {
         // the adapters as K steps of the tensor-core product, with its bias and activation
@@ -1099,10 +1210,9 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         const size_t b_at = packed ? m.add((size_t)q.S * out_f * ldh * 2) : 0;
         if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
         const TcAdapters tc{packed ? w + b_at : B, w + h, reinterpret_cast<int *>(w + l), q.S, ldh, list_stride(q.S)};
-        e = packed ? pack(q, B, w + b_at, out_f, ldh, false) : cudaSuccess;
-        if (e == cudaSuccess)
-            e = shrink_bf16<__nv_bfloat16>(q, X, A, batch, in_f, nullptr, 0, reinterpret_cast<int *>(w + l),
-                                           reinterpret_cast<unsigned short *>(w + h));
+        e = packed ? pack(q, B, w + b_at, out_f, ldh) : cudaSuccess;
+        const ShrinkJob job{X, A, nullptr, reinterpret_cast<unsigned short *>(w + h), in_f};
+        if (e == cudaSuccess) e = shrink(q, &job, 1, true, batch, ldh, reinterpret_cast<int *>(w + l), false);
         if (e == cudaSuccess) {
             p.bias = bias;
             p.act = activation;
@@ -1116,7 +1226,8 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         if ((s = alloc(&w, (size_t)batch * ldh * 4, q.st)) != KS_OK) return s;
         float *H = reinterpret_cast<float *>(w);
         s = run(p, KS_VARIANT_AUTO);
-        e = s == KS_OK ? shrink_fp32_out(q, X, A, batch, in_f, H, ldh) : cudaSuccess;
+        const ShrinkJob job{X, A, H, nullptr, in_f};
+        e = s == KS_OK ? shrink(q, &job, 1, false, batch, ldh, nullptr, by_rows(q, batch, in_f)) : cudaSuccess;
         if (s == KS_OK && e == cudaSuccess)
             e = q.bf16 ? expand<__nv_bfloat16>(q, Y, B, false, batch, out_f, H, ldh, bias, activation)
                        : expand<float>(q, Y, B, false, batch, out_f, H, ldh, bias, activation);
@@ -1163,79 +1274,63 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     if (!dX && !dA && !dB) return KS_OK;
     const int in_f = (int)o.in_f, out_f = (int)o.out_f;
     // Workspace: G and H, B transposed to rank x out (what G contracts over), the
-    // rows' order, the partial sums (dA's, then dB's), and for a fused dX the
-    // transposed values, A packed to in x rank and the lists.
+    // rows' order, the partial sums, for dX the transposed values and, fused, A
+    // packed to in x rank, the lists and G's planes.
     Layout m;
     const int ldh = round_up(q.R, 8);
-    const size_t bt = m.add((size_t)o.bbytes), vt = dX ? m.add((size_t)(o.nvals * o.elem)) : 0;
-    Problem p;  // dX = dY K: the product of pattern (a, c, b, d) with the transposed blocks
-    bool fused = false;
-    if (dX) {
-        p = Problem{dY, nullptr, dX, a, c, b, d, batch, dtype, q.st};
-        fused = fuses(q, p, nullptr, out_f, nullptr);
-    }
+    const bool want_g = dX || dA;
+    const size_t bt = want_g ? m.add((size_t)o.bbytes) : 0, vt = dX ? m.add((size_t)(o.nvals * o.elem)) : 0;
+    // dX = dY K: the product of pattern (a, c, b, d) with the transposed blocks.  What
+    // is wanted does not decide how G, H and the sums are computed: a gradient asked
+    // for alone has the bits it has beside the others.
+    static const char dummy[16] __attribute__((aligned(256))) = {};
+    Problem p{dY, nullptr, dX ? dX : const_cast<char *>(dummy), a, c, b, d, batch, dtype, q.st};
+    const bool fusable = fuses(q, p, nullptr, out_f, nullptr), fused = fusable && dX;
+    const bool rows_g = dA || !fused;  // G also as rows
     const size_t h_bytes = (size_t)batch * ldh * (fused ? 2 : 4);
-    const size_t g_at = dX || dA ? m.add(h_bytes) : 0, h_at = dB ? m.add(h_bytes) : 0;
+    const size_t g_at = want_g && rows_g ? m.add(h_bytes) : 0, h_at = dB ? m.add(h_bytes) : 0;
     const size_t p_at = fused ? m.add(plane_bytes(batch, q.R)) : 0;
     const size_t l_at = fused ? m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4) : 0;
     const size_t ap = fused ? m.add((size_t)q.S * in_f * ldh * 2) : 0;
     const bool sorted = ids && (dA || dB);
     const size_t perm_at = sorted ? m.add((size_t)batch * 4) : 0, off_at = sorted ? m.add((size_t)(q.S + 1) * 4) : 0;
-    const GradPlan ga = grad_plan(q, X, batch, in_f), gb = grad_plan(q, dY, batch, out_f);
-    const size_t w_at = dA || dB ? m.add(std::max(dA ? ga.bytes : 0, dB ? gb.bytes : 0)) : 0;
+    GradJob grad[2] = {{X, nullptr, nullptr, dA, in_f, in_f, 1}, {dY, nullptr, nullptr, dB, out_f, 1, q.R}};
+    const GradPlan plan = grad_plan(q, grad, batch);
+    const size_t w_at = dA || dB ? m.add(plan.bytes) : 0;
     char *w = nullptr;
     if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
     int *perm = sorted ? reinterpret_cast<int *>(w + perm_at) : nullptr;
     int *offsets = sorted ? reinterpret_cast<int *>(w + off_at) : nullptr;
-    float *W = reinterpret_cast<float *>(w + w_at);
-    const auto f32 = [&](size_t at) { return reinterpret_cast<float *>(w + at); };
-    const auto b16 = [&](size_t at) { return reinterpret_cast<__nv_bfloat16 *>(w + at); };
-    cudaError_t e = cudaSuccess;
-    const auto then = [&](auto &&step) { if (e == cudaSuccess && s == KS_OK) e = step(); };
-    if (dX || dA) {
-        then([&] { return launch_transpose_blocks(B, w + bt, q.S, o.out_f, q.R, dtype, q.st); });
-        then([&] {
-            int *lists = fused ? reinterpret_cast<int *>(w + l_at) : nullptr;
-            return fused ? shrink_bf16(q, dY, w + bt, batch, out_f, dA ? b16(g_at) : nullptr, ldh, lists,
-                                       reinterpret_cast<unsigned short *>(w + p_at))
-                         : shrink_fp32_out(q, dY, w + bt, batch, out_f, f32(g_at), ldh);
-        });
-    }
-    if (dX) {
-        then([&] { return launch_transpose_blocks(values, w + vt, a * d, b, c, dtype, q.st); });
+    int *lists = fused ? reinterpret_cast<int *>(w + l_at) : nullptr;
+
+    PrepareArgs prep{};
+    prep.perm = perm, prep.offsets = offsets, prep.sorted = sorted ? q.S : 0;
+    if (want_g) prep.job[0] = transpose(B, w + bt, q.S, o.out_f, q.R, o.out_f);
+    if (dX) prep.job[1] = transpose(values, w + vt, a * d, b, c, b);
+    if (fused) prep.job[2] = transpose(A, w + ap, q.S, q.R, o.in_f, ldh);
+    cudaError_t e = prepare(q, prep, batch);
+    ShrinkJob job[2];
+    int n_jobs = 0;
+    if (want_g)
+        job[n_jobs++] = ShrinkJob{dY, w + bt, rows_g ? w + g_at : nullptr,
+                                  fused ? reinterpret_cast<unsigned short *>(w + p_at) : nullptr, out_f};
+    if (dB) job[n_jobs++] = ShrinkJob{X, A, w + h_at, nullptr, in_f};
+    if (e == cudaSuccess)
+        e = shrink(q, job, n_jobs, fused, batch, ldh, lists, !fusable && by_rows(q, batch, std::max(in_f, out_f)));
+    if (dX && e == cudaSuccess) {
         p.V = w + vt;
-        const TcAdapters tc{w + ap, w + p_at, reinterpret_cast<int *>(w + l_at), q.S, ldh, list_stride(q.S)};
-        if (fused) {
-            then([&] { return pack(q, A, w + ap, in_f, ldh, true); });
-            p.ad = &tc;
-        }
-        if (e == cudaSuccess) s = run(p, fused ? KS_VARIANT_TC : KS_VARIANT_AUTO);
-        if (!fused)
-            then([&] {
-                return q.bf16
-                           ? expand<__nv_bfloat16>(q, dX, A, true, batch, in_f, f32(g_at), ldh, nullptr, KS_ACT_NONE)
-                           : expand<float>(q, dX, A, true, batch, in_f, f32(g_at), ldh, nullptr, KS_ACT_NONE);
-            });
+        const TcAdapters tc{w + ap, w + p_at, lists, q.S, ldh, list_stride(q.S)};
+        if (fused) p.ad = &tc;
+        s = run(p, fused ? KS_VARIANT_TC : KS_VARIANT_AUTO);
+        const float *G = reinterpret_cast<const float *>(w + g_at);
+        if (!fused && s == KS_OK)
+            e = q.bf16 ? expand<__nv_bfloat16>(q, dX, A, true, batch, in_f, G, ldh, nullptr, KS_ACT_NONE)
+                       : expand<float>(q, dX, A, true, batch, in_f, G, ldh, nullptr, KS_ACT_NONE);
     }
-    if (sorted)
-        then([&] {
-            order_kernel<<<(unsigned)q.S, 1024, 0, q.st>>>(ids, perm, offsets, (int)batch, q.S);
-            return cudaGetLastError();
-        });
-    if (dA)
-        then([&] {
-            return fused ? grad(q, ga, X, b16(g_at), ldh, perm, offsets, dA, true, batch, in_f, W)
-                         : grad(q, ga, X, f32(g_at), ldh, perm, offsets, dA, true, batch, in_f, W);
-        });
-    if (dB) {
-        then([&] {
-            return fused ? shrink_bf16(q, X, A, batch, in_f, b16(h_at), ldh, nullptr, nullptr)
-                         : shrink_fp32_out(q, X, A, batch, in_f, f32(h_at), ldh);
-        });
-        then([&] {
-            return fused ? grad(q, gb, dY, b16(h_at), ldh, perm, offsets, dB, false, batch, out_f, W)
-                         : grad(q, gb, dY, f32(h_at), ldh, perm, offsets, dB, false, batch, out_f, W);
-        });
+    if ((dA || dB) && e == cudaSuccess && s == KS_OK) {
+        grad[0].V = w + g_at;
+        grad[1].V = w + h_at;
+        e = grads(q, plan, grad, fused, ldh, perm, offsets, batch, w + w_at);
     }
     if (e != cudaSuccess && s == KS_OK) s = cuda_fail(e, "adapter gradient launch");
     e = cudaFreeAsync(w, q.st);

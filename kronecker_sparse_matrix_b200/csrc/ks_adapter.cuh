@@ -41,6 +41,23 @@ __device__ __forceinline__ int row_adapter(const int *ids, long long n, long lon
     return s < 0 ? -1 : s;
 }
 
+// One or two products H = scale X W^T of the same rows (blockIdx.z picks one): W[s] is
+// R x F; H, batch x ldh, and planes (TcAdapters::planes, plane_r ranks) may each be null.
+struct ShrinkJob {
+    const void *X, *W;
+    void *H;
+    unsigned short *planes;
+    int F;
+};
+struct ShrinkArgs {
+    ShrinkJob job[2];
+    const float *scales;
+    const int *ids;
+    long long N;
+    int R, ldh, S, plane_r;
+    unsigned *status;
+};
+
 // Sums over F of x[f] w[r][f] for four ranks (w: F elements apart) by one warp;
 // every lane gets them.  F a multiple of the vector, rows past `ranks` not read.
 template <typename T>

@@ -30,16 +30,19 @@ constexpr int kMaxSmem = 96 * 1024;
 
 // H[n][r] = scale[s] sum_f X[n][f] W[s][r][f], r < ldh (zeros past R and for rows without an adapter).
 template <typename T, typename O>
-__global__ void __launch_bounds__(256)
-    shrink_rows_kernel(const T *__restrict__ X, const T *__restrict__ W, const float *__restrict__ scales,
-                       const int *__restrict__ ids, O *__restrict__ H, long long N, int F, int R, int ldh, int S,
-                       unsigned *status) {
+__global__ void __launch_bounds__(256) shrink_rows_kernel(const ShrinkArgs p) {
+    const ShrinkJob &job = p.job[blockIdx.z];
+    const T *__restrict__ const X = static_cast<const T *>(job.X);
+    const T *__restrict__ const W = static_cast<const T *>(job.W);
+    O *__restrict__ const H = static_cast<O *>(job.H);
+    const float *const scales = p.scales;
+    const int F = job.F, R = p.R, ldh = p.ldh;
     const int lane = threadIdx.x & 31, quads = (ldh + 3) / 4;
     const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const long long n = task / quads;
-    if (n >= N) return;
+    if (n >= p.N) return;
     const int r0 = (int)(task - n * quads) * 4;
-    const int s = row_adapter(ids, n, N, S, status);
+    const int s = row_adapter(p.ids, n, p.N, p.S, p.status);
     float h[4] = {0.f, 0.f, 0.f, 0.f};
     if (s >= 0 && r0 < R) {
         dot4(X + n * F, W + ((long long)s * R + r0) * F, F, R - r0, lane, h);
@@ -228,20 +231,15 @@ bool adapter_rows_supported(const Problem &p, const void *A, int ldh) {
     return al % 16 == 0 && rows_plan(p, ldh, &o);
 }
 
-template <typename T, typename O>
-static cudaError_t shrink_rows(const void *X, const void *W, const float *scales, const int *ids, O *H, long long N,
-                               int F, int R, int ldh, int S, cudaStream_t st) {
-    const long long tasks = N * ((ldh + 3) / 4);
-    shrink_rows_kernel<T, O><<<(unsigned)((tasks + 7) / 8), 256, 0, st>>>(
-        static_cast<const T *>(X), static_cast<const T *>(W), scales, ids, H, N, F, R, ldh, S, device_status_ptr());
+cudaError_t launch_shrink_rows(const ShrinkArgs &p, int jobs, bool bf16, bool h_bf16, cudaStream_t st) {
+    const dim3 grid((unsigned)((p.N * ((p.ldh + 3) / 4) + 7) / 8), 1, (unsigned)jobs);
+    if (!bf16)
+        shrink_rows_kernel<float, float><<<grid, 256, 0, st>>>(p);
+    else if (h_bf16)
+        shrink_rows_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, st>>>(p);
+    else
+        shrink_rows_kernel<__nv_bfloat16, float><<<grid, 256, 0, st>>>(p);
     return cudaGetLastError();
-}
-cudaError_t launch_shrink_rows(const void *X, const void *W, const float *scales, const int *ids, void *H, bool h_bf16,
-                               long long N, int F, int R, int ldh, int S, bool bf16, cudaStream_t st) {
-    if (!bf16) return shrink_rows<float>(X, W, scales, ids, static_cast<float *>(H), N, F, R, ldh, S, st);
-    if (h_bf16)
-        return shrink_rows<__nv_bfloat16>(X, W, scales, ids, static_cast<__nv_bfloat16 *>(H), N, F, R, ldh, S, st);
-    return shrink_rows<__nv_bfloat16>(X, W, scales, ids, static_cast<float *>(H), N, F, R, ldh, S, st);
 }
 
 cudaError_t launch_adapter_rows(const Problem &pr, const void *A, const void *B, const float *scales, const int *ids,

@@ -88,13 +88,13 @@ cudaError_t launch_fma(const Problem &p, const FmaConfig &cfg);
 cudaError_t launch_fma32(const Problem &p, const FmaConfig &cfg);  // fp32, cp.async ring (ks_fma32.cu)
 cudaError_t launch_tc(const Problem &p, const TcConfig &cfg);
 
-// Adapters beside a product of few rows (ks_adapter_rows.cu), and H = scale X W^T for few rows with W
-// S x R x F (F a multiple of a 16-byte vector, X and W aligned).
+// Adapters beside a product of few rows (ks_adapter_rows.cu), and H = scale X W^T for few rows (F a
+// multiple of a 16-byte vector, X and W aligned; ks_adapter.cuh).
+struct ShrinkArgs;
 bool adapter_rows_supported(const Problem &p, const void *A, int ldh);
 cudaError_t launch_adapter_rows(const Problem &p, const void *A, const void *B, const float *scales, const int *ids,
                                 int S, int R, const float *H, int ldh);
-cudaError_t launch_shrink_rows(const void *X, const void *W, const float *scales, const int *ids, void *H, bool h_bf16,
-                               long long N, int F, int R, int ldh, int S, bool bf16, cudaStream_t st);
+cudaError_t launch_shrink_rows(const ShrinkArgs &p, int jobs, bool bf16, bool h_bf16, cudaStream_t st);
 
 // Gradients (ks_backward.cu).  dV[i][l][k][j] = sum_n dY[n,(i,k,l)] X[n,(i,j,l)]
 // is computed over `splits` row ranges into fp32 partials W[split][a][d][b][c],

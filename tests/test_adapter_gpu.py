@@ -325,6 +325,16 @@ def test_backward_unaligned_and_many_adapters(dtype):
         assert_backward(make(p, 260, 200, 8, dtype, "rows", 6), p)
 
 
+def test_backward_with_some_buffers_unaligned():
+    """A fused dX beside an X and an A that take no vectors."""
+    p = (1, 64, 48, 8)
+    for names in (("A",), ("x",), ("x", "A"), ("B",), ("values",)):
+        q = make(p, 600, 3, 16, torch.bfloat16, "segments", 17)
+        odd = make(p, 600, 3, 16, torch.bfloat16, "segments", 17, shift=1)
+        assert_backward(dict(q, **{n: odd[n] for n in names}), p)
+        assert_forward(call(dict(q, **{n: odd[n] for n in names}), p), q, p)
+
+
 def test_backward_parts_and_determinism():
     p = (1, 256, 64, 16)
     q = make(p, 3000, 6, 16, torch.bfloat16, "segments", 8)
