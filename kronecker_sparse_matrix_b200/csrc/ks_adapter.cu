@@ -34,7 +34,7 @@ namespace {
 
 // Any size, type and alignment: one warp per row.
 template <typename T, typename O>
-__global__ void __launch_bounds__(256) shrink_any_kernel(const ShrinkArgs p) {
+__global__ void __launch_bounds__(256) shrink_any_kernel(const __grid_constant__ ShrinkArgs p) {
     const ShrinkJob &job = p.job[blockIdx.z];
     const T *const X = static_cast<const T *>(job.X), *const W = static_cast<const T *>(job.W);
     const float *const scales = p.scales;
@@ -75,9 +75,13 @@ __device__ __forceinline__ int next_id(int id, int last) {
 // fp32, F a multiple of 4 and 16-byte aligned: a warp takes eight rows and eight
 // ranks at a time, its lanes the features (four each), and adds the lanes up at
 // the end: 62 shuffles for the 64 sums, each exchange halving what a lane holds.
-// An adapter's pass runs over all eight rows and keeps those that take it.
-// Bound by X for few ranks (16 FMAs for each 16 bytes a lane loads).
-__global__ void __launch_bounds__(128) shrink_fp32_kernel(const ShrinkArgs p) {
+// An adapter's pass runs over all eight rows and keeps those that take it.  X runs
+// two steps ahead in shared memory (cp.async; a lane copies what it reads itself, so
+// nothing is synchronised): at 160 registers the loads of 12 warps an SM alone did
+// not cover X's latency.
+__global__ void __launch_bounds__(128) shrink_fp32_kernel(const __grid_constant__ ShrinkArgs p) {
+    constexpr int STAGES = 3;
+    __shared__ float4 xs[4][STAGES][8][32];
     const ShrinkJob &job = p.job[blockIdx.z];
     const float *__restrict__ const X = static_cast<const float *>(job.X);
     const float *__restrict__ const W = static_cast<const float *>(job.W);
@@ -85,13 +89,14 @@ __global__ void __launch_bounds__(128) shrink_fp32_kernel(const ShrinkArgs p) {
     const float *const scales = p.scales;
     const long long N = p.N;
     const int F = job.F, R = p.R, ldh = p.ldh;
-    const int lane = threadIdx.x & 31;
-    const long long n0 = ((long long)blockIdx.x * 4 + (threadIdx.x >> 5)) * 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long n0 = ((long long)blockIdx.x * 4 + warp) * 8;
     if (n0 >= N) return;
     const int id = lane < 8 ? row_adapter(p.ids, n0 + lane, N, p.S, p.status) : -1;
     const int row = lane >> 2;  // the row and ranks (2 q, 2 q + 1) whose sums end in this lane
     const long long n = n0 + row;
-    if (__shfl_sync(0xFFFFFFFFu, id, row) < 0 && n < N)
+    const int row_id = __shfl_sync(0xFFFFFFFFu, id, row);
+    if (row_id < 0 && n < N)
         for (int r = 2 * (lane & 3); r < ldh; r += 8) {
             H[n * ldh + r] = 0.f;
             if (r + 1 < ldh) H[n * ldh + r + 1] = 0.f;
@@ -112,21 +117,38 @@ __global__ void __launch_bounds__(128) shrink_fp32_kernel(const ShrinkArgs p) {
         }
         return;
     }
+    const auto issue = [&](int f, int stage) {  // (rows past the last are read as the last one)
+        if (f < F) {
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+                const float *src = X + (n0 + m < N ? n0 + m : N - 1) * F + f;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 (unsigned)__cvta_generic_to_shared(&xs[warp][stage][m][lane])),
+                             "l"(src)
+                             : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
-        const bool mine = __shfl_sync(0xFFFFFFFFu, id, row) == s;
+        const bool mine = row_id == s;
         const float sc = scales ? scales[s] : 1.f;
-        for (int r0 = 0; r0 < R; r0 += 8) {
+        for (int r0 = 0; r0 < ldh; r0 += 8) {
             const float *w = W + ((long long)s * R + r0) * F;
             float acc[64];
 #pragma unroll
             for (int q = 0; q < 64; ++q) acc[q] = 0.f;
-            for (int f = lane * 4; f < F; f += 128) {
+            issue(lane * 4, 0);
+            issue(lane * 4 + 128, 1);
+            int stage = 0;
+            for (int f = lane * 4; f - lane * 4 < F; f += 128) {
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
                 float4 x[8];
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {  // rows past the last are read as the last one
-                    const long long nn = n0 + m < N ? n0 + m : N - 1;
-                    x[m] = *reinterpret_cast<const float4 *>(X + nn * F + f);
-                }
+                for (int m = 0; m < 8; ++m) x[m] = xs[warp][stage][m][lane];
+                issue(f + 256, stage == 0 ? 2 : stage - 1);
+                stage = stage == 2 ? 0 : stage + 1;
+                if (f >= F) continue;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     const int rr = r0 + r < R ? r : 0;
@@ -141,7 +163,8 @@ __global__ void __launch_bounds__(128) shrink_fp32_kernel(const ShrinkArgs p) {
                     }
                 }
             }
-            // sums over the lanes: lane keeps the half of its values that its bit picks
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            // sums over the lanes: a lane keeps the half of its values that its bit picks
 #pragma unroll
             for (int half = 32; half >= 2; half >>= 1) {
                 const int bit = half >> 1;  // lane bits 16, 8, 4, 2, 1
@@ -222,7 +245,7 @@ constexpr int kMixed = 6;
 
 template <int MT, int NT, typename O>
 __global__ void __launch_bounds__(256)
-    shrink_mma_kernel(const ShrinkArgs p, int row_blocks, int *__restrict__ lists, int list_stride) {
+    shrink_mma_kernel(const __grid_constant__ ShrinkArgs p, int row_blocks, int *__restrict__ lists, int list_stride) {
     const ShrinkJob &job = p.job[blockIdx.z];
     const __nv_bfloat16 *__restrict__ const X = static_cast<const __nv_bfloat16 *>(job.X);
     const __nv_bfloat16 *__restrict__ const W = static_cast<const __nv_bfloat16 *>(job.W);
@@ -544,7 +567,7 @@ struct PrepareArgs {
     int sorted;  // blocks that order rows (S or 0), before the tiles
 };
 template <typename T>
-__global__ void __launch_bounds__(1024) prepare_kernel(const PrepareArgs p) {
+__global__ void __launch_bounds__(1024) prepare_kernel(const __grid_constant__ PrepareArgs p) {
     if ((int)blockIdx.x < p.sorted) {
         order_rows(p.ids, p.perm, p.offsets, p.N, p.S, (int)blockIdx.x);
         return;
@@ -614,9 +637,11 @@ struct GradArgs {
 
 // fp32: a warp takes 128 features (four a lane) and every fourth row of the chunk,
 // RC ranks of each; Q's row is the same address in a warp.  64 FMAs (RC = 16) for
-// each 16 bytes of P a lane loads.  Types and alignment: any (VEC: vectors of four).
+// each 16 bytes of P a lane loads.  Bound by P's latency: what costs warps an SM (rows
+// of P a step ahead in registers, Q's rows in shared memory and eight rows in
+// flight: 106 and 98 us where this takes 59, 25216 x (1536 + 384) rank 8) loses more than it hides.  Types and alignment: any (VEC: vectors of four).
 template <typename T, typename Q, int RC, bool VEC>
-__global__ void __launch_bounds__(128) grad_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(128) grad_kernel(const __grid_constant__ GradArgs a) {
     const GradJob &job = a.job[(int)blockIdx.x >= a.first];
     const int bx = (int)blockIdx.x >= a.first ? (int)blockIdx.x - a.first : (int)blockIdx.x;
     const T *__restrict__ const P = static_cast<const T *>(job.P);
@@ -718,7 +743,7 @@ __device__ __forceinline__ uint4 load8_bf16(const float *p) {
 // or so, is staged transposed in shared memory, 128 positions at a time.  Bound by
 // P's bytes.  Q is rounded to bf16 where it is fp32.
 template <int MT, typename Q>
-__global__ void __launch_bounds__(256) grad_mma_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(256) grad_mma_kernel(const __grid_constant__ GradArgs a) {
     const GradJob &job = a.job[(int)blockIdx.x >= a.first];
     const int bx = (int)blockIdx.x >= a.first ? (int)blockIdx.x - a.first : (int)blockIdx.x;
     const __nv_bfloat16 *__restrict__ const P = static_cast<const __nv_bfloat16 *>(job.P);
@@ -813,7 +838,7 @@ __global__ void __launch_bounds__(256) grad_mma_kernel(const GradArgs a) {
 // ranks of one adapter; its eight warps every eighth chunk, and their sums are
 // added in order.  r * rs + f * fs is an entry's place in out[s].
 template <typename T>
-__global__ void __launch_bounds__(256) reduce_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(256) reduce_kernel(const __grid_constant__ GradArgs a) {
     __shared__ float part[8][8][33];
     const GradJob &job = a.job[(int)blockIdx.x >= a.first];
     const float *__restrict__ const W = job.W;
@@ -827,7 +852,7 @@ __global__ void __launch_bounds__(256) reduce_kernel(const GradArgs a) {
     if (lo < hi && f0 + lane < F) {
         const float *w = W + ((long long)s * R + r0) * F + f0 + lane;
         const int last = (hi - 1) / chunk;
-#pragma unroll 2
+#pragma unroll 4
         for (int z = lo / chunk + warp; z <= last; z += 8)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -928,7 +953,7 @@ cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf1
         return cudaGetLastError();
     }
     const int cols = lists ? std::max(ldh, p.plane_r) : ldh;
-    const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
+    const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
     // 16 rows a block for few ranks (more warps for X's latency), 32 for many (W is read half as often)
     const int rows = nt <= 2 ? 16 : 32;
     const int row_blocks = (int)((N + rows - 1) / rows), list_blocks = lists ? (int)((list_tiles(N) + 7) / 8) : 0;
@@ -977,8 +1002,8 @@ cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long 
 }
 
 // How the gradients (dA, dB; out null: not wanted) are cut: feature blocks of each,
-// `bz` blocks of ranks, chunks of `chunk` of the N rows, for about two blocks of
-// eight warps an SM.
+// `bz` blocks of ranks, chunks of `chunk` of the N rows, for about 16 warps an SM
+// (tensor cores) or 32.
 struct GradPlan {
     bool mma, vec;
     int warps, bx[2], bz, rc, chunk, chunks;
@@ -998,7 +1023,7 @@ GradPlan grad_plan(const Adapters &q, const GradJob (&job)[2], long long N) {
     g.bz = (q.R + g.rc - 1) / g.rc;
     long long blocks = 0;
     for (int j = 0; j < 2; ++j) blocks += g.bx[j] = (job[j].F + features - 1) / features;
-    const long long wanted = std::max<long long>(1, 2LL * sm_count() * 8 / g.warps / (blocks * g.bz));
+    const long long wanted = std::max<long long>(1, (g.mma ? 16LL : 32LL) * sm_count() / g.warps / (blocks * g.bz));
     long long chunk = std::max<long long>(64, (N + wanted - 1) / wanted);
     chunk = std::min<long long>((chunk + 15) / 16 * 16, (N + 15) / 16 * 16);
     chunk = std::max<long long>(chunk, (N + 65534) / 65535);  // grid limit

@@ -30,7 +30,7 @@ constexpr int kMaxSmem = 96 * 1024;
 
 // H[n][r] = scale[s] sum_f X[n][f] W[s][r][f], r < ldh (zeros past R and for rows without an adapter).
 template <typename T, typename O>
-__global__ void __launch_bounds__(256) shrink_rows_kernel(const ShrinkArgs p) {
+__global__ void __launch_bounds__(256) shrink_rows_kernel(const __grid_constant__ ShrinkArgs p) {
     const ShrinkJob &job = p.job[blockIdx.z];
     const T *__restrict__ const X = static_cast<const T *>(job.X);
     const T *__restrict__ const W = static_cast<const T *>(job.W);
@@ -73,7 +73,7 @@ struct RowsParams {
 
 // RB rows of a block; blockIdx.x: columns, blockIdx.y: rows.
 template <typename T, int RB>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowsParams p) {
     constexpr int V = kVec<T>;
     extern __shared__ __align__(16) uint8_t smem[];
     T *const xs = reinterpret_cast<T *>(smem);  // [RB][x_rows][pitch]
