@@ -333,7 +333,7 @@ cudaError_t launch_table(const ks_adamw_tensor *ts, int count, int iters, const 
 
 // Launches of at most kMany tensors and 2^31 - 1 blocks.  The parameter block of
 // a launch is copied with it, so few tensors take a small one.
-constexpr int kFew = 16, kMany = 400;
+constexpr int kFew = 16, kSome = 96, kMany = 400;
 constexpr long long kMaxBlocks = 0x7FFFFFFFll;
 
 template <typename T, typename S, bool MASTER>
@@ -353,8 +353,9 @@ cudaError_t launch_all(const std::vector<ks_adamw_tensor> &ts, const Hyper &h, c
         // finding the tensor and the step's numbers are then paid once for them
         constexpr int many = sizeof(S) == 1 ? kIters8 : kIters32;
         const int iters = blocks >= 8LL * many * sm_count() ? many : 1;
-        const cudaError_t err = count <= kFew ? launch_table<T, S, MASTER, kFew>(&ts[k], count, iters, h, st)
-                                              : launch_table<T, S, MASTER, kMany>(&ts[k], count, iters, h, st);
+        const cudaError_t err = count <= kFew    ? launch_table<T, S, MASTER, kFew>(&ts[k], count, iters, h, st)
+                                : count <= kSome ? launch_table<T, S, MASTER, kSome>(&ts[k], count, iters, h, st)
+                                                 : launch_table<T, S, MASTER, kMany>(&ts[k], count, iters, h, st);
         if (err != cudaSuccess) return err;
         k = e;
     }
@@ -366,15 +367,29 @@ struct Range {
     bool written;
 };
 
-// Whether a written buffer shares bytes with any other of the step's buffers.
-bool any_overlap(std::vector<Range> &r) {
-    std::sort(r.begin(), r.end(), [](const Range &x, const Range &y) { return x.begin < y.begin; });
+// Whether a written buffer shares bytes with any other of the step's buffers.  The
+// buffers come in columns (all params, all grads, ..), which are mostly in the order
+// of their addresses already: each is sorted if need be, and they are merged.
+constexpr int kColumns = 8;
+bool any_overlap(std::vector<Range> (&col)[kColumns]) {
+    const auto before = [](const Range &x, const Range &y) { return x.begin < y.begin; };
+    size_t at[kColumns] = {};
+    for (auto &c : col)
+        if (!std::is_sorted(c.begin(), c.end(), before)) std::sort(c.begin(), c.end(), before);
     uintptr_t end_read = 0, end_written = 0;
-    for (const Range &q : r) {
+    while (true) {
+        int k = -1;
+        uintptr_t least = UINTPTR_MAX;
+        for (int j = 0; j < kColumns; ++j)
+            if (at[j] < col[j].size() && col[j][at[j]].begin < least) {
+                least = col[j][at[j]].begin;
+                k = j;
+            }
+        if (k < 0) return false;
+        const Range &q = col[k][at[k]++];
         if (q.begin < end_written || (q.written && q.begin < end_read)) return true;
         (q.written ? end_written : end_read) = std::max(q.written ? end_written : end_read, q.end);
     }
-    return false;
 }
 
 ks_status adamw_step(const ks_adamw_tensor *tensors, int64_t n_tensors, int dtype, int state_bits,
@@ -400,9 +415,9 @@ ks_status adamw_step(const ks_adamw_tensor *tensors, int64_t n_tensors, int dtyp
         return record_error(KS_ERR_MISALIGNED, "lr_ptr, grad_scale or step_ptr is not aligned to its element");
     const uintptr_t elem = dtype == KS_BF16 ? 2 : 4, selem = state_bits == 8 ? 1 : 4;
     std::vector<ks_adamw_tensor> ts;
-    std::vector<Range> ranges;
+    std::vector<Range> ranges[kColumns];
     ts.reserve((size_t)n_tensors);
-    ranges.reserve((size_t)n_tensors * 7 + 3);
+    for (auto &c : ranges) c.reserve((size_t)n_tensors + 3);
     bool masters = false;
     for (int64_t k = 0; k < n_tensors; ++k) {
         const ks_adamw_tensor &q = tensors[k];
@@ -427,24 +442,24 @@ ks_status adamw_step(const ks_adamw_tensor *tensors, int64_t n_tensors, int dtyp
             !is_aligned(q.exp_avg_sq_scale, 4))
             return record_error(KS_ERR_MISALIGNED, "tensor %lld: a buffer is not aligned to its element",
                                 (long long)k);
-        const auto add = [&](const void *p, uintptr_t bytes, bool written) {
-            if (p) ranges.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written});
+        const auto add = [&](int column, const void *p, uintptr_t bytes, bool written) {
+            if (p) ranges[column].push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written});
         };
         const uintptr_t n = (uintptr_t)q.n, blocks = (n + kBlock - 1) / kBlock;
-        add(q.param, n * elem, true);
-        add(q.grad, n * elem, false);
-        add(q.exp_avg, n * selem, true);
-        add(q.exp_avg_sq, n * selem, true);
-        add(q.master, n * 4, true);
+        add(0, q.param, n * elem, true);
+        add(1, q.grad, n * elem, false);
+        add(2, q.exp_avg, n * selem, true);
+        add(3, q.exp_avg_sq, n * selem, true);
+        add(4, q.master, n * 4, true);
         if (state_bits == 8) {
-            add(q.exp_avg_scale, blocks * 4, true);
-            add(q.exp_avg_sq_scale, blocks * 4, true);
+            add(5, q.exp_avg_scale, blocks * 4, true);
+            add(6, q.exp_avg_sq_scale, blocks * 4, true);
         }
         ts.push_back(q);
     }
     if (ts.empty()) return KS_OK;
     const auto scalar = [&](const void *p, uintptr_t bytes) {
-        if (p) ranges.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, false});
+        if (p) ranges[7].push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, false});
     };
     scalar(opt->lr_ptr, 4);
     scalar(opt->grad_scale, 4);
