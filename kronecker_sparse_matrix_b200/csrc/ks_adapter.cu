@@ -225,6 +225,23 @@ __device__ void tile_list(const int *__restrict__ ids, int *__restrict__ lists, 
     if (lane == 0) list[0] = count;
 }
 
+// The bias as the tensor-core product takes it (TcAdapters): a thread for each
+// output, and the plane of ones by the first block.
+struct BiasPack {
+    const unsigned short *bias;
+    uint4 *packed, *ones;
+    int n, blocks;
+};
+__device__ __forceinline__ void pack_bias(const BiasPack &b, int block) {
+    const int at = block * 256 + (int)threadIdx.x;
+    if (at < b.n) b.packed[at] = make_uint4(b.bias[at], 0u, 0u, 0u);
+    // 16-byte lines (rank octet, row group, rank): rank 0 is ones, eight rows of 1.0 in bf16
+    if (block == 0) {
+        const unsigned one = threadIdx.x < 128 && threadIdx.x % 8 == 0 ? 0x3F803F80u : 0u;
+        b.ones[threadIdx.x] = make_uint4(one, one, one, one);
+    }
+}
+
 // bf16, F a multiple of 8 and 16-byte aligned, on the tensor cores (mma.sync: the
 // operands of so narrow a product are read once each, straight into registers,
 // and a tcgen05 tile would first have to pass through shared memory).  A block
@@ -245,7 +262,8 @@ constexpr int kMixed = 6;
 
 template <int MT, int NT, typename O>
 __global__ void __launch_bounds__(256)
-    shrink_mma_kernel(const __grid_constant__ ShrinkArgs p, int row_blocks, int *__restrict__ lists, int list_stride) {
+    shrink_mma_kernel(const __grid_constant__ ShrinkArgs p, int row_blocks, int *__restrict__ lists, int list_stride,
+                      const __grid_constant__ BiasPack bias) {
     const ShrinkJob &job = p.job[blockIdx.z];
     const __nv_bfloat16 *__restrict__ const X = static_cast<const __nv_bfloat16 *>(job.X);
     const __nv_bfloat16 *__restrict__ const W = static_cast<const __nv_bfloat16 *>(job.W);
@@ -259,7 +277,11 @@ __global__ void __launch_bounds__(256)
     __shared__ int row_id[ROWS], found[ROWS], n_found;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((int)blockIdx.x >= row_blocks) {
-        const long long tile = (long long)(blockIdx.x - row_blocks) * 8 + warp;
+        if (bias.packed && (int)blockIdx.x - row_blocks < bias.blocks) {
+            pack_bias(bias, (int)blockIdx.x - row_blocks);
+            return;
+        }
+        const long long tile = (long long)(blockIdx.x - row_blocks - bias.blocks) * 8 + warp;
         if (blockIdx.y == 0 && blockIdx.z == 0 && tile * 128 < N)
             tile_list(p.ids, lists, list_stride, N, p.S, tile, lane);
         return;
@@ -920,9 +942,9 @@ bool by_rows(const Adapters &q, long long N, int F) {
 
 // H = scale X W^T of one or two jobs.  h_bf16: their H are bf16; lists: null, or the
 // lists of the tensor-core product to be built (its planes are job[0]'s; the caller
-// has made sure of vectors); few: row by row (by_rows).
+// has made sure of vectors), and its bias to be packed; few: row by row (by_rows).
 cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf16, long long N, int ldh, int *lists,
-                   bool few) {
+                   bool few, const BiasPack &bias = BiasPack{}) {
     ShrinkArgs p{};
     bool vec = true;
     for (int j = 0; j < jobs; ++j) {
@@ -957,9 +979,9 @@ cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf1
     // 16 rows a block for few ranks (more warps for X's latency), 32 for many (W is read half as often)
     const int rows = nt <= 2 ? 16 : 32;
     const int row_blocks = (int)((N + rows - 1) / rows), list_blocks = lists ? (int)((list_tiles(N) + 7) / 8) : 0;
-    const dim3 grid((unsigned)(row_blocks + list_blocks), (unsigned)((cols + 8 * nt - 1) / (8 * nt)), z);
+    const dim3 grid((unsigned)(row_blocks + bias.blocks + list_blocks), (unsigned)((cols + 8 * nt - 1) / (8 * nt)), z);
     const auto go = [&](auto kernel) {
-        kernel<<<grid, 256, 0, q.st>>>(p, row_blocks, lists, list_stride(q.S));
+        kernel<<<grid, 256, 0, q.st>>>(p, row_blocks, lists, list_stride(q.S), bias);
         return cudaGetLastError();
     };
     const auto ranks = [&](auto h) {
@@ -1134,11 +1156,10 @@ struct Layout {
 // Whether the tensor-core kernel can take the product with adapters beside it:
 // bf16, a pattern that AUTO gives to it, and A's vectors aligned (null: a
 // workspace's).  The product's V may be null: a workspace's.
-bool fuses(const Adapters &q, Problem p, const void *A, int F, const void *bias) {
+bool fuses(const Adapters &q, Problem p, const void *A, int F) {
     if (!q.bf16) return false;
     static const char dummy[16] __attribute__((aligned(256))) = {};
     if (!p.V) p.V = dummy;
-    p.bias = bias;
     Plan plan;
     const char *why = "";
     const int ldh = round_up(q.R, 8);
@@ -1226,20 +1247,26 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         const ShrinkArgs h{{{X, A, H, nullptr, in_f}}, scales, ids, batch, q.R, row_ldh, q.S, 0, device_status_ptr()};
         e = launch_shrink_rows(h, 1, q.bf16, false, q.st);
         if (e == cudaSuccess) e = launch_adapter_rows(p, A, B, scales, ids, q.S, q.R, H, row_ldh);
-    } else if (fuses(q, p, A, in_f, bias)) {
+    } else if (fuses(q, p, A, in_f)) {
         // the adapters as K steps of the tensor-core product, with its bias and activation
         Layout m;
         const int ldh = round_up(q.R, 8);
         const size_t h = m.add(plane_bytes(batch, q.R)), l = m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4);
         const bool packed = q.R != ldh || !aligned(B, 16);
         const size_t b_at = packed ? m.add((size_t)q.S * out_f * ldh * 2) : 0;
+        const size_t bias_at = bias ? m.add((size_t)out_f * 16) : 0, ones_at = bias ? m.add(4096) : 0;
         if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
-        const TcAdapters tc{packed ? w + b_at : B, w + h, reinterpret_cast<int *>(w + l), q.S, ldh, list_stride(q.S)};
+        TcAdapters tc{packed ? w + b_at : B, w + h, reinterpret_cast<int *>(w + l), q.S, ldh, list_stride(q.S)};
+        BiasPack pack_b{};
+        if (bias) {
+            tc.bias = w + bias_at, tc.ones = w + ones_at;
+            pack_b = BiasPack{static_cast<const unsigned short *>(bias), reinterpret_cast<uint4 *>(w + bias_at),
+                              reinterpret_cast<uint4 *>(w + ones_at), out_f, (out_f + 255) / 256};
+        }
         e = packed ? pack(q, B, w + b_at, out_f, ldh) : cudaSuccess;
         const ShrinkJob job{X, A, nullptr, reinterpret_cast<unsigned short *>(w + h), in_f};
-        if (e == cudaSuccess) e = shrink(q, &job, 1, true, batch, ldh, reinterpret_cast<int *>(w + l), false);
+        if (e == cudaSuccess) e = shrink(q, &job, 1, true, batch, ldh, reinterpret_cast<int *>(w + l), false, pack_b);
         if (e == cudaSuccess) {
-            p.bias = bias;
             p.act = activation;
             p.ad = &tc;
             s = run(p, KS_VARIANT_TC);
@@ -1310,7 +1337,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     // for alone has the bits it has beside the others.
     static const char dummy[16] __attribute__((aligned(256))) = {};
     Problem p{dY, nullptr, dX ? dX : const_cast<char *>(dummy), a, c, b, d, batch, dtype, q.st};
-    const bool fusable = fuses(q, p, nullptr, out_f, nullptr), fused = fusable && dX;
+    const bool fusable = fuses(q, p, nullptr, out_f), fused = fusable && dX;
     const bool rows_g = dA || !fused;  // G also as rows
     const size_t h_bytes = (size_t)batch * ldh * (fused ? 2 : 4);
     const size_t g_at = want_g && rows_g ? m.add(h_bytes) : 0, h_at = dB ? m.add(h_bytes) : 0;

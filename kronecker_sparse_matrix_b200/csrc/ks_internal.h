@@ -23,6 +23,9 @@ struct TcAdapters {
     const void *planes;  // 16-byte aligned
     const int *lists;    // list_stride words for each 128 rows, 16-byte aligned
     int S, R, list_stride;
+    // A bias of all rows (instead of Problem::bias): out_features x 8 bf16, the bias
+    // first and seven zeros, and a plane of 16 ranks whose first is one; or null.
+    const void *bias = nullptr, *ones = nullptr;
 };
 
 // One KS product, after validation: Y = X K^T with K of pattern (a,b,c,d).

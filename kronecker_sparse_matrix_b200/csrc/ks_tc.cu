@@ -164,6 +164,9 @@ struct TcParams {
 // so that the transposer warps and the X ring know nothing of it.  The MMAs leave
 // out the lanes of the rows of other adapters, so that nothing an adapter holds
 // (infinities, NaN) reaches a row that does not take it.  Y is still written once.
+// A bias is one more such stage, for all rows: a plane whose first rank is one, and
+// the bias as the first of its ranks.  In the epilogue it would cost the four
+// warps' serial chains 12 us of 72 (GPT-2-shaped, 8192 rows); as a stage it is 3.
 constexpr int kRankStep = 16;                        // ranks of a stage: one K step
 constexpr int kPlaneBytes = kRows * kRankStep * 2;   // H of a stage
 template <bool AD>
@@ -171,6 +174,8 @@ struct TcAd {};
 template <>
 struct TcAd<true> {
     CUtensorMap wmap;       // W viewed as (rank, k, l, i + a * s)
+    CUtensorMap bmap;       // the packed bias likewise, (8, k, l, i)
+    const uint8_t *ones;    // the bias's plane, or null: no bias
     const uint8_t *planes;  // H as operand planes: plane_stride bytes for each 128 rows
     const int *lists;       // per 128 rows: see TcAdapters
     int R, list_stride;
@@ -305,6 +310,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if constexpr (AD) {
                     constexpr uint32_t wb = DLS * 32;  // bytes of W for one k
+                    if (ad.ones) {
+                        const int vs = vq % VS;
+                        ok = mbar_wait(&v_empty[vs], ((vq / VS) & 1) ^ 1, abort_flag, p.status, wait_ns);
+                        if (!ok) break;
+                        uint8_t *dst = sV + vs * p.v_stride;
+                        mbar_expect_tx(&v_full[vs], wb * p.bp + kPlaneBytes);
+                        tma_load_4d(dst, &ad.bmap, &v_full[vs], 0, ps * p.bp, l0, i);
+                        bulk_load(dst + p.v_stage_bytes, ad.ones, kPlaneBytes, &v_full[vs]);
+                        ++vq;
+                    }
                     for (int r0 = 0; r0 < ad.R && ok; r0 += kRankStep)
                         for (int q = 0; q < head.x && ok; ++q) {
                             const int s = q == 0 ? head.y : ad.lists[rb * ad.list_stride + 8 + 8 * q];
@@ -393,25 +408,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(&x_empty[xs]);
                 }
                 if constexpr (AD) {
-                    for (int r0 = 0; r0 < ad.R && ok; r0 += kRankStep)
-                        for (int q = 0; q < count && ok; ++q) {
-                            const int4 m = q == 0 ? off0 : *reinterpret_cast<const int4 *>(list + 8 + 8 * q + 4);
-                            const uint32_t off[4] = {(uint32_t)m.x, (uint32_t)m.y, (uint32_t)m.z, (uint32_t)m.w};
-                            const int vs = vq % VS;
-                            ok = mbar_wait(&v_full[vs], (vq / VS) & 1, abort_flag, p.status, wait_ns);
-                            ++vq;
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t vstage = su32(sV) + vs * p.v_stride;
-                            // H: core matrices of 8 ranks x 8 rows, row groups 128 bytes apart, rank octets 2048
-                            const uint64_t adsc = smem_desc(vstage + p.v_stage_bytes, 2048, 128);
+                    const auto rank_step = [&](const int4 &m) {
+                        const uint32_t off[4] = {(uint32_t)m.x, (uint32_t)m.y, (uint32_t)m.z, (uint32_t)m.w};
+                        const int vs = vq % VS;
+                        if (!mbar_wait(&v_full[vs], (vq / VS) & 1, abort_flag, p.status, wait_ns)) return false;
+                        ++vq;
+                        tc_fence_after();
+                        const uint32_t vstage = su32(sV) + vs * p.v_stride;
+                        // H: core matrices of 8 ranks x 8 rows, row groups 128 bytes apart, rank octets 2048
+                        const uint64_t adsc = smem_desc(vstage + p.v_stage_bytes, 2048, 128);
 #pragma unroll
-                            for (int l = 0; l < DLS; ++l) {
-                                const uint64_t bd = smem_desc_sw(vstage + l * (p.bp * 32), 8 * 32, 6u);
-                                mma_bf16_lanes(d_base + l * p.bp, adsc, bd, idesc | (1u << 15), off);
-                            }
-                            mma_commit(&v_empty[vs]);
+                        for (int l = 0; l < DLS; ++l) {
+                            const uint64_t bd = smem_desc_sw(vstage + l * (p.bp * 32), 8 * 32, 6u);
+                            mma_bf16_lanes(d_base + l * p.bp, adsc, bd, idesc | (1u << 15), off);
                         }
+                        mma_commit(&v_empty[vs]);
+                        return true;
+                    };
+                    if (ok && ad.ones) ok = rank_step(make_int4(0, 0, 0, 0));
+                    for (int r0 = 0; r0 < ad.R && ok; r0 += kRankStep)
+                        for (int q = 0; q < count && ok; ++q)
+                            ok = rank_step(q == 0 ? off0 : *reinterpret_cast<const int4 *>(list + 8 + 8 * q + 4));
                 }
                 if (ok) mma_commit(&acc_full[buf]);
             }
@@ -1119,6 +1136,16 @@ static cudaError_t launch_dls(const Problem &pr, const TcConfig &cfg) {
                        CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
             if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+            ad.ones = static_cast<const uint8_t *>(q.ones);
+            memset(&ad.bmap, 0, sizeof(ad.bmap));
+            if (q.ones) {
+                cuuint64_t bdims[4] = {8, (cuuint64_t)pr.b, (cuuint64_t)pr.d, (cuuint64_t)pr.a};
+                cuuint64_t bstrides[3] = {(cuuint64_t)pr.d * 16, 16, (cuuint64_t)pr.b * pr.d * 16};
+                r = encode(&ad.bmap, kType, 4, const_cast<void *>(q.bias), bdims, bstrides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+            }
             ad.planes = static_cast<const uint8_t *>(q.planes);
             ad.plane_stride = (long long)((q.R + kRankStep - 1) / kRankStep) * kPlaneBytes;
             ad.lists = q.lists;
