@@ -72,6 +72,39 @@ __device__ __forceinline__ int next_id(int id, int last) {
     return (int)__reduce_min_sync(0xFFFFFFFFu, (unsigned)(id > last ? id : INT_MAX));
 }
 
+// The adapters among each 128 rows and their rows, for the products that take them
+// as further stages (TcAdapters::lists): one warp per 128 rows.
+__device__ void tile_list(const int *__restrict__ ids, int *__restrict__ lists, int list_stride, long long N, int S,
+                          long long tile, int lane) {
+    int id[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const long long n = tile * 128 + 32 * q + lane;
+        id[q] = n < N ? (ids ? ids[n] : 0) : -1;
+        if (id[q] >= S) id[q] = -1;
+    }
+    int *list = lists + tile * list_stride;
+    int count = 0, last = -1;
+    while (true) {
+        int best = INT_MAX;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) best = id[q] > last ? min(best, id[q]) : best;
+        last = (int)__reduce_min_sync(0xFFFFFFFFu, (unsigned)best);
+        if (last == INT_MAX) break;
+        unsigned off[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) off[q] = ~__ballot_sync(0xFFFFFFFFu, id[q] == last);
+        if (lane == 0) {
+            int *e = list + 8 + 8 * count;
+            e[0] = last;
+            if (count == 0) list[1] = last;
+            *reinterpret_cast<uint4 *>(e + 4) = make_uint4(off[0], off[1], off[2], off[3]);
+        }
+        ++count;
+    }
+    if (lane == 0) list[0] = count;
+}
+
 // fp32, F a multiple of 4 and 16-byte aligned: a warp takes eight rows and eight
 // ranks at a time, its lanes the features (four each), and adds the lanes up at
 // the end: 62 shuffles for the 64 sums, each exchange halving what a lane holds.
@@ -79,7 +112,9 @@ __device__ __forceinline__ int next_id(int id, int last) {
 // two steps ahead in shared memory (cp.async; a lane copies what it reads itself, so
 // nothing is synchronised): at 160 registers the loads of 12 warps an SM alone did
 // not cover X's latency.
-__global__ void __launch_bounds__(128) shrink_fp32_kernel(const __grid_constant__ ShrinkArgs p) {
+// Blocks past the rows' build the lists of the product that follows.
+__global__ void __launch_bounds__(128)
+    shrink_fp32_kernel(const __grid_constant__ ShrinkArgs p, int row_blocks, int *__restrict__ lists, int list_stride) {
     constexpr int STAGES = 3;
     __shared__ float4 xs[4][STAGES][8][32];
     const ShrinkJob &job = p.job[blockIdx.z];
@@ -90,6 +125,11 @@ __global__ void __launch_bounds__(128) shrink_fp32_kernel(const __grid_constant_
     const long long N = p.N;
     const int F = job.F, R = p.R, ldh = p.ldh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if ((int)blockIdx.x >= row_blocks) {
+        const long long tile = (long long)(blockIdx.x - row_blocks) * 4 + warp;
+        if (blockIdx.z == 0 && tile * 128 < N) tile_list(p.ids, lists, list_stride, N, p.S, tile, lane);
+        return;
+    }
     const long long n0 = ((long long)blockIdx.x * 4 + warp) * 8;
     if (n0 >= N) return;
     const int id = lane < 8 ? row_adapter(p.ids, n0 + lane, N, p.S, p.status) : -1;
@@ -190,39 +230,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], unsigned a0, unsigned a1
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The adapters among each 128 rows and their rows, for the tensor-core product
-// (TcAdapters::lists): one warp per 128 rows.
-__device__ void tile_list(const int *__restrict__ ids, int *__restrict__ lists, int list_stride, long long N, int S,
-                          long long tile, int lane) {
-    int id[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const long long n = tile * 128 + 32 * q + lane;
-        id[q] = n < N ? (ids ? ids[n] : 0) : -1;
-        if (id[q] >= S) id[q] = -1;
-    }
-    int *list = lists + tile * list_stride;
-    int count = 0, last = -1;
-    while (true) {
-        int best = INT_MAX;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) best = id[q] > last ? min(best, id[q]) : best;
-        last = (int)__reduce_min_sync(0xFFFFFFFFu, (unsigned)best);
-        if (last == INT_MAX) break;
-        unsigned off[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) off[q] = ~__ballot_sync(0xFFFFFFFFu, id[q] == last);
-        if (lane == 0) {
-            int *e = list + 8 + 8 * count;
-            e[0] = last;
-            if (count == 0) list[1] = last;
-            *reinterpret_cast<uint4 *>(e + 4) = make_uint4(off[0], off[1], off[2], off[3]);
-        }
-        ++count;
-    }
-    if (lane == 0) list[0] = count;
 }
 
 // The bias as the tensor-core product takes it (TcAdapters): a thread for each
@@ -507,7 +514,10 @@ __global__ void __launch_bounds__(128, 6)
     for (int m = 0; m < ROWS; ++m) {
         if (m < rows) {
             float4 v = acc[m];
-            if constexpr (ACT != KS_ACT_NONE) {
+            if constexpr (ACT == KS_ACT_GELU_ERF) {
+                const float2 a = gelu_erf_f2(make_float2(v.x, v.y)), b = gelu_erf_f2(make_float2(v.z, v.w));
+                v = make_float4(a.x, a.y, b.x, b.y);
+            } else if constexpr (ACT != KS_ACT_NONE) {
                 v.x = ep_act_fn(v.x, ACT);
                 v.y = ep_act_fn(v.y, ACT);
                 v.z = ep_act_fn(v.z, ACT);
@@ -941,8 +951,9 @@ bool by_rows(const Adapters &q, long long N, int F) {
 }
 
 // H = scale X W^T of one or two jobs.  h_bf16: their H are bf16; lists: null, or the
-// lists of the tensor-core product to be built (its planes are job[0]'s; the caller
-// has made sure of vectors), and its bias to be packed; few: row by row (by_rows).
+// lists of the product that takes the adapters as stages, to be built (a tensor-core
+// product's planes are job[0]'s; the caller has made sure of vectors); its bias to
+// be packed; few: row by row (by_rows).
 cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf16, long long N, int ldh, int *lists,
                    bool few, const BiasPack &bias = BiasPack{}) {
     ShrinkArgs p{};
@@ -971,7 +982,9 @@ cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf1
     }
     if (few) return launch_shrink_rows(p, jobs, q.bf16, h_bf16, q.st);
     if (!q.bf16) {
-        shrink_fp32_kernel<<<dim3((unsigned)((N + 31) / 32), 1, z), 128, 0, q.st>>>(p);
+        const int row_blocks = (int)((N + 31) / 32), list_blocks = lists ? (int)((list_tiles(N) + 3) / 4) : 0;
+        shrink_fp32_kernel<<<dim3((unsigned)(row_blocks + list_blocks), 1, z), 128, 0, q.st>>>(p, row_blocks, lists,
+                                                                                               list_stride(q.S));
         return cudaGetLastError();
     }
     const int cols = lists ? std::max(ldh, p.plane_r) : ldh;
@@ -1169,6 +1182,13 @@ bool fuses(const Adapters &q, Problem p, const void *A, int F) {
            tc_adapters_supported(p, tc) && shrink_vec(q, p.X, A, F);
 }
 
+// The same for the fp32 kernel.
+bool fuses_fp32(const Adapters &q, Problem p, const void *A, int F) {
+    static const char dummy[16] __attribute__((aligned(256))) = {};
+    if (!p.V) p.V = dummy;
+    return !q.bf16 && p.dtype == KS_F32 && shrink_vec(q, p.X, A, F) && fma32_adapters_supported(p);
+}
+
 cudaError_t pack(const Adapters &q, const void *W, void *out, int F, int Rp) {
     const long long n = (long long)q.S * F * (Rp / 8);
     if ((n + 255) / 256 > INT_MAX) return cudaErrorInvalidConfiguration;
@@ -1271,6 +1291,22 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
             p.ad = &tc;
             s = run(p, KS_VARIANT_TC);
         }
+    } else if (fuses_fp32(q, p, A, in_f)) {
+        // the adapters as stages of the fp32 product, with its bias and activation
+        Layout m;
+        const int ldh = round_up(q.R, 4);
+        const size_t h = m.add((size_t)batch * ldh * 4), l = m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4);
+        const size_t v = m.add((size_t)o.nvals * 4);
+        if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
+        const auto *vt = reinterpret_cast<const float *>(w + v);
+        const ShrinkJob job{X, A, w + h, nullptr, in_f};
+        e = launch_transpose_blocks(values, w + v, a * d, b, c, dtype, q.st);
+        if (e == cudaSuccess) e = shrink(q, &job, 1, false, batch, ldh, reinterpret_cast<int *>(w + l), false);
+        p.bias = bias;
+        p.act = activation;
+        const Fma32Adapters ad{reinterpret_cast<const float *>(w + h), static_cast<const float *>(B),
+                               reinterpret_cast<const int *>(w + l), q.R, ldh, q.R, list_stride(q.S)};
+        if (e == cudaSuccess) e = launch_fma32_adapters(p, vt, ad);
     } else {
         // The product, then one pass that adds the adapters, the bias and the
         // activation.  In bf16 the product is rounded before they are added.
@@ -1331,19 +1367,22 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     Layout m;
     const int ldh = round_up(q.R, 8);
     const bool want_g = dX || dA;
-    const size_t bt = want_g ? m.add((size_t)o.bbytes) : 0, vt = dX ? m.add((size_t)(o.nvals * o.elem)) : 0;
+    const size_t bt = want_g ? m.add((size_t)o.bbytes) : 0;
     // dX = dY K: the product of pattern (a, c, b, d) with the transposed blocks.  What
     // is wanted does not decide how G, H and the sums are computed: a gradient asked
     // for alone has the bits it has beside the others.
     static const char dummy[16] __attribute__((aligned(256))) = {};
     Problem p{dY, nullptr, dX ? dX : const_cast<char *>(dummy), a, c, b, d, batch, dtype, q.st};
     const bool fusable = fuses(q, p, nullptr, out_f), fused = fusable && dX;
+    // fp32: the transposed blocks, transposed for the kernel, are the values as they are
+    const bool fusable32 = fuses_fp32(q, p, nullptr, out_f) && aligned(values, 16), fused32 = fusable32 && dX;
+    const size_t vt = dX && !fused32 ? m.add((size_t)(o.nvals * o.elem)) : 0;
     const bool rows_g = dA || !fused;  // G also as rows
     const size_t h_bytes = (size_t)batch * ldh * (fused ? 2 : 4);
     const size_t g_at = want_g && rows_g ? m.add(h_bytes) : 0, h_at = dB ? m.add(h_bytes) : 0;
     const size_t p_at = fused ? m.add(plane_bytes(batch, q.R)) : 0;
-    const size_t l_at = fused ? m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4) : 0;
-    const size_t ap = fused ? m.add((size_t)q.S * in_f * ldh * 2) : 0;
+    const size_t l_at = fused || fused32 ? m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4) : 0;
+    const size_t ap = fused || fused32 ? m.add((size_t)q.S * in_f * ldh * o.elem) : 0;
     const bool sorted = ids && (dA || dB);
     const size_t perm_at = sorted ? m.add((size_t)batch * 4) : 0, off_at = sorted ? m.add((size_t)(q.S + 1) * 4) : 0;
     GradJob grad[2] = {{X, nullptr, nullptr, dA, in_f, in_f, 1}, {dY, nullptr, nullptr, dB, out_f, 1, q.R}};
@@ -1353,13 +1392,13 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
     int *perm = sorted ? reinterpret_cast<int *>(w + perm_at) : nullptr;
     int *offsets = sorted ? reinterpret_cast<int *>(w + off_at) : nullptr;
-    int *lists = fused ? reinterpret_cast<int *>(w + l_at) : nullptr;
+    int *lists = fused || fused32 ? reinterpret_cast<int *>(w + l_at) : nullptr;
 
     PrepareArgs prep{};
     prep.perm = perm, prep.offsets = offsets, prep.sorted = sorted ? q.S : 0;
     if (want_g) prep.job[0] = transpose(B, w + bt, q.S, o.out_f, q.R, o.out_f);
-    if (dX) prep.job[1] = transpose(values, w + vt, a * d, b, c, b);
-    if (fused) prep.job[2] = transpose(A, w + ap, q.S, q.R, o.in_f, ldh);
+    if (dX && !fused32) prep.job[1] = transpose(values, w + vt, a * d, b, c, b);
+    if (fused || fused32) prep.job[2] = transpose(A, w + ap, q.S, q.R, o.in_f, ldh);
     cudaError_t e = prepare(q, prep, batch);
     ShrinkJob job[2];
     int n_jobs = 0;
@@ -1368,8 +1407,12 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
                                   fused ? reinterpret_cast<unsigned short *>(w + p_at) : nullptr, out_f};
     if (dB) job[n_jobs++] = ShrinkJob{X, A, w + h_at, nullptr, in_f};
     if (e == cudaSuccess)
-        e = shrink(q, job, n_jobs, fused, batch, ldh, lists, !fusable && by_rows(q, batch, std::max(in_f, out_f)));
-    if (dX && e == cudaSuccess) {
+        e = shrink(q, job, n_jobs, fused, batch, ldh, lists, !fusable && !fusable32 && by_rows(q, batch, std::max(in_f, out_f)));
+    if (fused32 && e == cudaSuccess) {
+        const Fma32Adapters ad{reinterpret_cast<const float *>(w + g_at), reinterpret_cast<const float *>(w + ap), lists,
+                               q.R, ldh, ldh, list_stride(q.S)};
+        e = launch_fma32_adapters(p, static_cast<const float *>(values), ad);
+    } else if (dX && e == cudaSuccess) {
         p.V = w + vt;
         const TcAdapters tc{w + ap, w + p_at, lists, q.S, ldh, list_stride(q.S)};
         if (fused) p.ad = &tc;

@@ -98,13 +98,19 @@ struct Tile32 {
     static constexpr int NXC = (BM * CA + kCopyRoles - 1) / kCopyRoles;  // A copies per role
 };
 
-// Activation ACT (0 none, 1 ReLU, 2 GELU tanh form, 3 GELU erf form) of four
-// outputs, chosen at compile time.
+// Activation ACT (0 none, 1 ReLU, 2 GELU tanh form, 3 GELU erf form, 4 the same by
+// gelu_erf_f2) of four outputs, chosen at compile time.
 template <int ACT>
 __device__ __forceinline__ void ep_act4(float (&v)[4]) {
     if constexpr (ACT == 2) {  // in pairs (ViT bias + GELU: 1.23x against the earlier scalar tanh form)
         const float2 a = gelu_tanh_f2(make_float2(v[0], v[1]));
         const float2 b = gelu_tanh_f2(make_float2(v[2], v[3]));
+        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+        return;
+    }
+    if constexpr (ACT == 4) {
+        const float2 a = gelu_erf_f2(make_float2(v[0], v[1]));
+        const float2 b = gelu_erf_f2(make_float2(v[2], v[3]));
         v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
         return;
     }
@@ -137,7 +143,43 @@ __device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t *bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// VT: p.V holds the values transposed per block, vt[i][l][j][k] (k
+// Calls stage(adapter, entry, its rows' words, group, first rank) for each stage of
+// the adapters among a tile's rows (n0 .. n0 + BM), in the order that the copying
+// and the computing warps share.
+template <int BM, typename F>
+__device__ __forceinline__ void for_adapter_stages(const Fma32Adapters &ad, long long n0, long long N, bool &ok,
+                                                   F &&stage) {
+    constexpr int kGroups = BM < 128 ? 1 : BM / 128;
+    for (int li = 0; li < kGroups && ok; ++li) {
+        const long long group = n0 / 128 + li;
+        if (group * 128 >= N) break;
+        const int *list = ad.lists + group * ad.list_stride;
+        const int count = __ldg(list);
+        for (int q = 0; q < count && ok; ++q) {
+            const int *entry = list + 8 + 8 * q;
+            if (BM < 128) {  // only the words of the tile's rows
+                unsigned off = 0xFFFFFFFFu;
+                for (int w = 0; w < (BM + 31) / 32; ++w) off &= (unsigned)__ldg(entry + 4 + (int)(n0 % 128) / 32 + w);
+                if (off == 0xFFFFFFFFu) continue;
+            }
+            const int s = __ldg(entry);
+            for (int r0 = 0; r0 < ad.R && ok; r0 += kJT) stage(s, q, entry + 4, li, r0);
+        }
+    }
+}
+
+// Low-rank adapters beside the product (Fma32Adapters): Y[n] += H[n] W[s]^T for the
+// rows n of adapter s, as further stages of a tile, eight ranks each: the rows' H
+// (compact, the same for every l) in place of X, W[s] of the tile's outputs in place
+// of the values.  A stage is one adapter's, for the rows of one 128-row group that
+// take it; in a warp that holds other rows too the products of those are left out
+// row by row, so that nothing an adapter holds (infinities, NaN) reaches them.
+template <bool AD>
+struct Fma32Ad {};
+template <>
+struct Fma32Ad<true> : Fma32Adapters {};
+
+// AD: adapters beside the product.  VT: p.V holds the values transposed per block, vt[i][l][j][k] (k
 // contiguous), and goes to shared memory with 16-byte copies; otherwise the
 // values keep their [i][l][k][j] layout and move as 4-byte transposing copies.
 //
@@ -151,8 +193,8 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // (setmaxnreg: 128 x 40 + 256 x 232 = the 384 x 168 of the launch).  Every
 // wait is bounded; a wait that runs out sets the device status word and the
 // CTA's abort flag, which ends every role's loop.
-template <int DL, int WM, int WK, int TN, bool VT>
-__global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p) {
+template <int DL, int WM, int WK, int TN, bool VT, bool AD = false>
+__global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p, const Fma32Ad<AD> ad) {
     using TL = Tile32<DL, WM, WK, TN>;
     constexpr int BM = TL::BM, BKL = TL::BKL;
     using LN = typename TL::LN;
@@ -277,6 +319,43 @@ __global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p)
                 }
                 cp_async_mbar_arrive_noinc(&full_bar[buf]);  // fires when this lane's copies have landed
             }
+            if constexpr (AD) {
+                for_adapter_stages<BM>(ad, n0, p.N, ok, [&](int s, int, const int *, int li, int r0) {
+                    const int buf = (int)(fill % kNS);
+                    ok = sm100::mbar_wait(&empty_bar[buf], ((fill / kNS) & 1) ^ 1, abort_flag, p.status);
+                    if (!ok) return;
+                    ++fill;
+                    const uint32_t st = s_base + (uint32_t)(buf * TL::STAGE) * 4u;
+#pragma unroll 1
+                    for (int v = 0; v < kT / (kThreads - 256); ++v) {
+                        const int vt = pt + 128 * v;
+                        // H: two 16-byte units of each of the group's rows
+                        constexpr int GR = BM < 128 ? BM : 128;
+                        if (vt < 2 * GR) {
+                            const int row = li * 128 + (vt >> 1), r = r0 + 4 * (vt & 1);
+                            const bool in = n0 + row < p.N && r < ad.ldh;
+                            cp_async16(st + (uint32_t)(row * TL::RA + 4 * (vt & 1)) * 4u,
+                                       in ? ad.H + (n0 + row) * ad.ldh + r : p.X, in);
+                        }
+                        const int vj = vt & 7, kq = vt >> 3;
+                        const float *ws = ad.W + ((long long)s * p.out_f + ((long long)i * p.b + k0 + kq) * p.d + l0) * ad.ldw +
+                                          r0 + vj;
+                        const uint32_t sv = st + (uint32_t)(TL::A_WORDS + vj * TL::BKP + kq) * 4u;
+                        const int k_left = p.b - k0 - kq;
+                        const bool rv = r0 + vj < ad.R;
+#pragma unroll
+                        for (int t = 0; t < NV; ++t) {
+                            const int e8 = kq + 32 * t, l = e8 / BKL, kc = e8 % BKL - kq;
+                            if (e8 < DL * BKL) {
+                                const bool in = rv && kc < k_left;
+                                cp_async4(sv + (uint32_t)(l * TL::PSB + kc) * 4u,
+                                          in ? ws + ((long long)kc * p.d + l) * ad.ldw : p.V, in);
+                            }
+                        }
+                    }
+                    cp_async_mbar_arrive_noinc(&full_bar[buf]);
+                });
+            }
         }
         cp_async_wait_all();  // no copy may still be landing when the CTA exits
         return;
@@ -329,6 +408,56 @@ __global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p)
             }
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(&empty_bar[buf]);  // this warp is done with the stage
+        }
+        if constexpr (AD) {
+            const long long n0 = (long long)(tile / p.n_kb / p.n_g) * BM;
+            if (ok)
+                for_adapter_stages<BM>(ad, n0, p.N, ok, [&](int, int, const int *off, int li, int) {
+                    const int buf = (int)(fill % kNS);
+                    ok = __all_sync(0xffffffffu, sm100::mbar_wait(&full_bar[buf], (fill / kNS) & 1, abort_flag, p.status));
+                    if (!ok) return;
+                    ++fill;
+                    const float *stage = smem + buf * TL::STAGE;
+                    const float *Ah = stage + a_row * TL::RA;
+                    const float *Bs = stage + TL::A_WORDS + c_l * TL::PSB + b_col;
+                    // which of the thread's rows take the adapter
+                    unsigned take = 0;
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        const int at = (int)(n0 & 127) * (BM < 128) + a_row + LN::RG * m - 128 * li;  // row of the group
+                        if (at >= 0 && at < 128 && !(__ldg(off + (at >> 5)) >> (at & 31) & 1)) take |= 1u << m;
+                    }
+                    const bool all = __all_sync(0xffffffffu, take == 0xFFu);
+                    const auto products = [&](auto every) {
+#pragma unroll(decltype(every)::value ? kJT : 1)
+                        for (int jj = 0; jj < kJT; ++jj) {
+                            float am[8];
+#pragma unroll
+                            for (int m = 0; m < 8; ++m) am[m] = Ah[m * LN::RG * TL::RA + jj];
+                            float4 bq[TN / 4];
+#pragma unroll
+                            for (int q = 0; q < TN / 4; ++q)
+                                bq[q] = *reinterpret_cast<const float4 *>(Bs + jj * TL::BKP + 4 * LN::KQ * q);
+#pragma unroll
+                            for (int m = 0; m < 8; ++m) {
+                                if (!decltype(every)::value && !(take >> m & 1)) continue;
+                                const float2 a2 = make_float2(am[m], am[m]);
+#pragma unroll
+                                for (int q = 0; q < TN / 4; ++q) {
+                                    acc[m][2 * q] = __ffma2_rn(a2, make_float2(bq[q].x, bq[q].y), acc[m][2 * q]);
+                                    acc[m][2 * q + 1] =
+                                        __ffma2_rn(a2, make_float2(bq[q].z, bq[q].w), acc[m][2 * q + 1]);
+                                }
+                            }
+                        }
+                    };
+                    if (all)
+                        products(std::true_type{});
+                    else if (__any_sync(0xffffffffu, take != 0u))
+                        products(std::false_type{});
+                    __syncwarp();
+                    if (lane == 0) sm100::mbar_arrive(&empty_bar[buf]);
+                });
         }
         if (!ok) break;
         // Epilogue straight from registers.  A thread holds, per row m and k group q,
@@ -417,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p)
             switch (p.act) {
                 case 1: store_tile(std::integral_constant<int, 1>(), bp); break;
                 case 2: store_tile(std::integral_constant<int, 2>(), bp); break;
-                case 3: store_tile(std::integral_constant<int, 3>(), bp); break;
+                case 3: store_tile(std::integral_constant<int, AD ? 4 : 3>(), bp); break;  // (ViT: 230 us with erff)
                 default: store_tile(std::integral_constant<int, 0>(), bp); break;
             }
         }
@@ -425,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p)
 }
 
 template <int DL, int WM, int WK, int TN>
-cudaError_t launch_cfg32(const Problem &pr, const float *vt) {
+cudaError_t launch_cfg32(const Problem &pr, const float *vt, const Fma32Adapters *adapters) {
     using TL = Tile32<DL, WM, WK, TN>;
     Fma32Params p;
     p.X = static_cast<const float *>(pr.X);
@@ -450,12 +579,23 @@ cudaError_t launch_cfg32(const Problem &pr, const float *vt) {
     if (smem > 232448) return cudaErrorInvalidConfiguration;
     p.status = device_status_ptr();
     if (!p.status) return cudaErrorUnknown;
-    auto kern = vt ? fma32_kernel<DL, WM, WK, TN, true> : fma32_kernel<DL, WM, WK, TN, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     const long long grid = std::min<long long>(p.n_tiles, (long long)sm_count());
-    kern<<<(int)grid, kThreads, smem, pr.stream>>>(p);
-    return cudaGetLastError();
+    const auto go = [&](auto kern, const auto &ad) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        kern<<<(int)grid, kThreads, smem, pr.stream>>>(p, ad);
+        return cudaGetLastError();
+    };
+    if (adapters) {
+        if constexpr (DL == 8) {
+            Fma32Ad<true> ad;
+            static_cast<Fma32Adapters &>(ad) = *adapters;
+            return vt ? go(fma32_kernel<DL, WM, WK, TN, true, true>, ad) : cudaErrorInvalidConfiguration;
+        }
+        return cudaErrorInvalidConfiguration;
+    }
+    return vt ? go(fma32_kernel<DL, WM, WK, TN, true>, Fma32Ad<false>{})
+              : go(fma32_kernel<DL, WM, WK, TN, false>, Fma32Ad<false>{});
 }
 
 }  // namespace
@@ -499,9 +639,10 @@ FmaConfig fma32_choose(const Problem &p, int dl) {
     return best;
 }
 
-cudaError_t launch_cfg_any(const Problem &p, const FmaConfig &c, const float *vt) {
+cudaError_t launch_cfg_any(const Problem &p, const FmaConfig &c, const float *vt,
+                           const Fma32Adapters *ad = nullptr) {
 #define KS_FMA32_CASE(DL_, WM_, WK_, TN_) \
-    if (c.dl == DL_ && c.wm == WM_ && c.wk == WK_ && c.tn == TN_) return launch_cfg32<DL_, WM_, WK_, TN_>(p, vt);
+    if (c.dl == DL_ && c.wm == WM_ && c.wk == WK_ && c.tn == TN_) return launch_cfg32<DL_, WM_, WK_, TN_>(p, vt, ad);
     KS_FMA32_CASE(8, 2, 4, 16)
     KS_FMA32_CASE(8, 4, 2, 16)
     KS_FMA32_CASE(8, 2, 4, 12)
@@ -553,6 +694,25 @@ cudaError_t launch_fma32(const Problem &p, const FmaConfig &c_in) {
         (void)cudaGetLastError();
     }
     return launch_cfg_any(p, c, nullptr);
+}
+
+// Adapters beside a product that the transposed copy of the values pays for (as in
+// launch_fma32, 8 l a tile); the caller has the values transposed per block in vt,
+// 16-byte aligned.  Measured against a second pass over Y: see fma32_kernel.
+bool fma32_adapters_supported(const Problem &p) {
+    if (p.dtype != KS_F32 || p.b % 4 || 2.0 * (double)p.batch * (double)(p.a * p.b * p.c * p.d) < 1073741824.0)
+        return false;
+    Plan plan;
+    const char *why = "";
+    if (!make_plan(p, KS_VARIANT_AUTO, &plan, &why) || plan.variant != KS_VARIANT_FMA || plan.fma.dl != 8) return false;
+    const FmaConfig c = fma32_choose(p, 8);
+    if (c.dl != 8) return false;
+    const double tiles = (double)((p.batch + cfg_bm(c) - 1) / cfg_bm(c)) * (double)(p.a * (p.d / 8)) *
+                         (double)((p.b + cfg_bk(c) - 1) / cfg_bk(c));
+    return tiles < (double)(INT32_MAX - 4096);
+}
+cudaError_t launch_fma32_adapters(const Problem &p, const float *vt, const Fma32Adapters &ad) {
+    return launch_cfg_any(p, fma32_choose(p, 8), vt, &ad);
 }
 
 }  // namespace ks

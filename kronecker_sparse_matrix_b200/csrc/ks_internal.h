@@ -28,6 +28,14 @@ struct TcAdapters {
     const void *bias = nullptr, *ones = nullptr;
 };
 
+// Low-rank adapters that the fp32 kernel adds to a product: Y[n] += H[n] W[s]^T.
+struct Fma32Adapters {
+    const float *H;    // batch x ldh, ldh a multiple of 4, zeros past R, 16-byte aligned
+    const float *W;    // S x out_features x ldw, ranks contiguous
+    const int *lists;  // as in TcAdapters
+    int R, ldh, ldw, list_stride;
+};
+
 // One KS product, after validation: Y = X K^T with K of pattern (a,b,c,d).
 struct Problem {
     const void *X;
@@ -90,6 +98,8 @@ cudaError_t launch_stream(const Problem &p);
 cudaError_t launch_fma(const Problem &p, const FmaConfig &cfg);
 cudaError_t launch_fma32(const Problem &p, const FmaConfig &cfg);  // fp32, cp.async ring (ks_fma32.cu)
 cudaError_t launch_tc(const Problem &p, const TcConfig &cfg);
+bool fma32_adapters_supported(const Problem &p);
+cudaError_t launch_fma32_adapters(const Problem &p, const float *vt, const Fma32Adapters &ad);
 
 // Adapters beside a product of few rows (ks_adapter_rows.cu), and H = scale X W^T for few rows (F a
 // multiple of a 16-byte vector, X and W aligned; ks_adapter.cuh).

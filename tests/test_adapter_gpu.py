@@ -325,6 +325,35 @@ def test_backward_unaligned_and_many_adapters(dtype):
         assert_backward(make(p, 260, 200, 8, dtype, "rows", 6), p)
 
 
+@pytest.mark.parametrize("p,n", [((1, 192, 48, 8), 7300), ((2, 100, 48, 8), 7000), ((1, 64, 200, 16), 2700),
+                                 ((1, 32, 256, 24), 2800)])
+@pytest.mark.parametrize("kind", ["segments", "rows", "one"])
+def test_fp32_products_large_enough_to_take_the_adapters_along(p, n, kind):
+    """At least 2^30 flop: the adapters are stages of the fp32 product (64- and 128-row tiles, ragged rows and k)."""
+    a, b, c, d = p
+    assert 2 * n * a * b * c * d >= 1 << 30
+    for r in (8, 5, 20):
+        q = make(p, n, 1 if kind == "one" else 4, r, torch.float32, kind, n + r, bias=True)
+        if kind == "rows":  # runs of a few rows, so that warps hold several adapters
+            q["ids"] = q["ids"][:n // 3 + 1].repeat_interleave(3)[:n].contiguous()
+        assert_forward(call(q, p, act="gelu_erf"), q, p, "gelu_erf")
+        assert_backward(q, p)
+
+
+def test_a_broken_adapter_in_a_large_fp32_product():
+    p, n = (1, 192, 48, 8), 7300
+    q = make(p, n, 3, 8, torch.float32, "segments", 3)
+    q["ids"][5] = 1
+    q["ids"][6] = 0
+    clean, dx = call(q, p), ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"])[0]
+    other = q["ids"] != 1
+    q["B"][1] = float("inf")
+    q["A"][1] = float("nan")
+    assert torch.equal(call(q, p)[other], clean[other])
+    dx2 = ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"])[0]
+    assert torch.equal(dx2[other], dx[other]) and not torch.isfinite(dx2[5]).any()
+
+
 def test_backward_with_some_buffers_unaligned():
     """A fused dX beside an X and an A that take no vectors."""
     p = (1, 64, 48, 8)
