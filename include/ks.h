@@ -306,10 +306,10 @@ ks_status ks_butterfly_factorize(const void *A, int log2n, void *const *factors,
  * more takes none either, and the next ks_sync_status reports
  * KS_ERR_INVALID_ARG: no such id is ever used as an index.  Any order of the ids is
  * allowed; rows of one adapter next to each other run fastest, since a tile of
- * rows passes once over the weights of each adapter that it holds.
+ * rows (64 to 128) passes once over the weights of each adapter that it holds.
  * X, values, bias, activation and dtype are as for ks_matmul_ep (KS_TF32: the
  * KS product uses TF32 as there, the adapters' products are fp32).  Y must not
- * overlap any input.  1 <= n_adapters <= 65535, 1 <= rank <= 1024, batch <=
+ * overlap any input.  1 <= n_adapters <= 4096, 1 <= rank <= 1024, batch <=
  * 2^30.  H = scales[s] * X A[s]^T lives in a stream-ordered workspace from the
  * library's pool (KS_ERR_ALLOC if it cannot be had). */
 ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_t b, int64_t c, int64_t d,

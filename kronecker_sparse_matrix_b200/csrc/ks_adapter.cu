@@ -903,6 +903,42 @@ __global__ void __launch_bounds__(256) reduce_kernel(const __grid_constant__ Gra
     }
 }
 
+// The same where an adapter has few chunks: one thread for a feature and eight ranks
+// (256 adapters of 32 rows, rank 16: blocks of reduce_kernel spend their time in
+// starting and meeting).
+template <typename T>
+__global__ void __launch_bounds__(256) reduce_few_kernel(const __grid_constant__ GradArgs a) {
+    const GradJob &job = a.job[(int)blockIdx.x >= a.first];
+    const int *__restrict__ const offsets = a.offsets;
+    const int F = job.F, R = a.R, rs = job.rs, fs = job.fs, chunk = a.chunk;
+    const int s = blockIdx.y, r0 = blockIdx.z * 8;
+    const int f = ((int)blockIdx.x >= a.first ? (int)blockIdx.x - a.first : (int)blockIdx.x) * 256 + (int)threadIdx.x;
+    if (f >= F) return;
+    const int lo = offsets ? offsets[s] : 0, hi = offsets ? offsets[s + 1] : s == 0 ? a.N : 0;
+    float sum[8] = {};
+    if (lo < hi) {
+        const float *__restrict__ const w = job.W + ((long long)s * R + r0) * F + f;
+        for (int z = lo / chunk; z <= (hi - 1) / chunk; ++z)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (r0 + e < R) sum[e] += w[((long long)z * R + e) * F];
+    }
+    T *o = static_cast<T *>(job.out) + (long long)s * R * F + (long long)r0 * rs + (long long)f * fs;
+    if (sizeof(T) == 2 && rs == 1 && R % 8 == 0 && reinterpret_cast<uintptr_t>(job.out) % 16 == 0) {
+        unsigned v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(sum[2 * e], sum[2 * e + 1]);
+            v[e] = *reinterpret_cast<const unsigned *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(o) = make_uint4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (r0 + e < R) put(o + (long long)e * rs, sum[e]);
+    }
+}
+
 // B as the tensor-core product reads it: out[s][f][r], r < Rp (a multiple of 8), zeros past R.
 __global__ void __launch_bounds__(256)
     pack_kernel(const unsigned short *__restrict__ W, unsigned short *__restrict__ out, int S, int F, int R, int Rp) {
@@ -1078,11 +1114,12 @@ GradPlan grad_plan(const Adapters &q, const GradJob (&job)[2], long long N) {
 cudaError_t grads(const Adapters &q, const GradPlan &g, const GradJob (&job)[2], bool v_bf16, int ldh,
                   const int *perm, const int *offsets, long long N, char *W) {
     GradArgs p{};
+    const bool few = g.chunks <= 3 * q.S;  // chunks of an adapter, were the rows spread evenly
     int reduce_blocks[2] = {};
     for (int j = 0; j < 2; ++j) {
         p.job[j] = job[j];
         p.job[j].W = reinterpret_cast<float *>(W + g.at[j]);
-        if (job[j].out) reduce_blocks[j] = (job[j].F + 31) / 32;
+        if (job[j].out) reduce_blocks[j] = few ? (job[j].F + 255) / 256 : (job[j].F + 31) / 32;
     }
     p.perm = perm, p.offsets = offsets, p.N = (int)N, p.R = q.R, p.ldh = ldh, p.S = q.S, p.chunk = g.chunk;
     p.first = g.bx[0];
@@ -1109,14 +1146,16 @@ cudaError_t grads(const Adapters &q, const GradPlan &g, const GradJob (&job)[2],
     if (e != cudaSuccess) return e;
     p.first = reduce_blocks[0];
     const dim3 rgrid((unsigned)(reduce_blocks[0] + reduce_blocks[1]), (unsigned)q.S, (unsigned)((q.R + 7) / 8));
-    if (q.bf16)
-        reduce_kernel<__nv_bfloat16><<<rgrid, 256, 0, q.st>>>(p);
-    else
-        reduce_kernel<float><<<rgrid, 256, 0, q.st>>>(p);
-    return cudaGetLastError();
+    const auto sum = [&](auto kernel) {
+        kernel<<<rgrid, 256, 0, q.st>>>(p);
+        return cudaGetLastError();
+    };
+    if (q.bf16) return few ? sum(reduce_few_kernel<__nv_bfloat16>) : sum(reduce_kernel<__nv_bfloat16>);
+    return few ? sum(reduce_few_kernel<float>) : sum(reduce_kernel<float>);
 }
 
-constexpr int kMaxAdapters = 65535, kMaxRank = 1024;
+// (each adapter's rows are found by a scan of all ids: prepare_kernel)
+constexpr int kMaxAdapters = 4096, kMaxRank = 1024;
 
 struct Checked {
     int64_t in_f, out_f, nvals, abytes, bbytes;

@@ -257,8 +257,10 @@ cudaError_t launch_adapter_rows(const Problem &pr, const void *A, const void *B,
     p.status = device_status_ptr();
     const dim3 grid((unsigned)o.tiles, (unsigned)((pr.batch + o.rb - 1) / o.rb));
     const auto go = [&](auto kernel) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)o.smem);
-        if (e != cudaSuccess) return e;
+        if (o.smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)o.smem);
+            if (e != cudaSuccess) return e;
+        }
         kernel<<<grid, kThreads, o.smem, pr.stream>>>(p);
         return cudaGetLastError();
     };

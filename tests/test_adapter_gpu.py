@@ -354,6 +354,15 @@ def test_a_broken_adapter_in_a_large_fp32_product():
     assert torch.equal(dx2[other], dx[other]) and not torch.isfinite(dx2[5]).any()
 
 
+def test_many_adapters_with_few_rows_each():
+    for dtype in (torch.float32, torch.bfloat16):
+        for p in ((1, 64, 48, 8), (1, 10, 6, 3)):
+            q = make(p, 2000, 150, 16, dtype, "rows", 31)
+            q["ids"] = q["ids"].sort().values
+            assert_backward(q, p)
+            assert_forward(call(q, p), q, p)
+
+
 def test_backward_with_some_buffers_unaligned():
     """A fused dX beside an X and an A that take no vectors."""
     p = (1, 64, 48, 8)

@@ -26,7 +26,7 @@ def backward(lib, dY=P, X=P + FAR, V=P + 2 * FAR, pat=(1, 16, 8, 4), batch=4, dt
     return lib.ks_adapter_backward(dY, X, V, *pat, batch, dtype, A, B, scales, ids, s, r, dX, dA, dB, None)
 
 
-@pytest.mark.parametrize("kw", [dict(s=0), dict(s=65536), dict(r=0), dict(r=1025), dict(A=None), dict(B=None),
+@pytest.mark.parametrize("kw", [dict(s=0), dict(s=4097), dict(s=65536), dict(r=0), dict(r=1025), dict(A=None), dict(B=None),
                                 dict(X=None), dict(Y=None), dict(V=None), dict(dtype=5), dict(act=4), dict(batch=-1),
                                 dict(batch=(1 << 30) + 1), dict(pat=(1, 0, 8, 4)), dict(Y=P + 3 * FAR),
                                 dict(Y=P + 4 * FAR), dict(Y=P), dict(Y=P + FAR), dict(ids=P + 2 * FAR + 4),
