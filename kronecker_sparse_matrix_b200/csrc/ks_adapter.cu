@@ -343,21 +343,29 @@ __global__ void __launch_bounds__(256)
             w[j] = reinterpret_cast<const uint4 *>(W + ((long long)s * R + r) * F);
         }
         float acc[MT][NT][4] = {};
-#pragma unroll NT <= 2 ? 4 : 2
-        for (int f = warp * 32 + 8 * t; f - 8 * t < F; f += 256) {
-            const bool in = f < F;
-            uint4 xv[2 * MT], wv[NT];
+        // U steps' loads in flight together
+        constexpr int U = NT <= 2 ? 4 : 1;
+        for (int f0 = warp * 32 + 8 * t; f0 - 8 * t < F; f0 += 256 * U) {
+            uint4 xv[U][2 * MT], wv[U][NT];
 #pragma unroll
-            for (int m = 0; m < 2 * MT; ++m) xv[m] = in ? __ldg(x[m] + (f >> 3)) : make_uint4(0u, 0u, 0u, 0u);
+            for (int u = 0; u < U; ++u) {
+                const int f = f0 + 256 * u;
+                const bool in = f < F;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) wv[j] = in ? __ldg(w[j] + (f >> 3)) : make_uint4(0u, 0u, 0u, 0u);
+                for (int m = 0; m < 2 * MT; ++m) xv[u][m] = in ? __ldg(x[m] + (f >> 3)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int j = 0; j < NT; ++j) wv[u][j] = in ? __ldg(w[j] + (f >> 3)) : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    mma16816(acc[m][j], xv[2 * m].x, xv[2 * m + 1].x, xv[2 * m].y, xv[2 * m + 1].y, wv[j].x, wv[j].y);
-                    mma16816(acc[m][j], xv[2 * m].z, xv[2 * m + 1].z, xv[2 * m].w, xv[2 * m + 1].w, wv[j].z, wv[j].w);
-                }
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const uint4 &p0 = xv[u][2 * m], &p1 = xv[u][2 * m + 1], &v = wv[u][j];
+                        mma16816(acc[m][j], p0.x, p1.x, p0.y, p1.y, v.x, v.y);
+                        mma16816(acc[m][j], p0.z, p1.z, p0.w, p1.w, v.z, v.w);
+                    }
         }
         // warps 4..7 hand their sums to warps 0..3, which add theirs
         if (warp >= 4) {
@@ -530,58 +538,61 @@ __global__ void __launch_bounds__(128, 6)
 
 // ---------------------------------------------------------------- dA and dB
 
+constexpr int kPrepareThreads = 256;
+
 // The rows of each adapter in order: perm[offsets[s] .. offsets[s + 1]) holds the
-// rows with id s.  The block counts the rows of smaller ids and of its own, then
-// writes its own in row order.
+// rows with id s.  The block counts the rows of smaller ids, then writes the rows of
+// its own, 1024 ids at a time, four neighbouring ones a thread.
 __device__ void order_rows(const int *__restrict__ ids, int *__restrict__ perm, int *__restrict__ offsets, int N, int S,
                            int s) {
-    __shared__ int warp_n[32];
-    __shared__ int base_sh, total_sh;
+    constexpr int WARPS = kPrepareThreads / 32, STEP = 4 * kPrepareThreads;
+    __shared__ int warp_n[2][WARPS];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     int less = 0;
-    for (int n = t; n < N; n += 1024) {
+#pragma unroll 4
+    for (int n = t; n < N; n += kPrepareThreads) {
         const int id = ids[n];
         less += id >= 0 && id < s;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) less += __shfl_xor_sync(0xFFFFFFFFu, less, o);
-    if (lane == 0) warp_n[warp] = less;
+    less = __reduce_add_sync(0xFFFFFFFFu, less);
+    if (lane == 0) warp_n[0][warp] = less;
     __syncthreads();
-    if (t == 0) {
-        int b = 0;
-        for (int w = 0; w < 32; ++w) b += warp_n[w];
-        offsets[s] = b;
-        base_sh = b;
-    }
-    __syncthreads();
-    int base = base_sh;
-    for (int n0 = 0; n0 < N; n0 += 1024) {
-        const int n = n0 + t;
-        const bool mine = n < N && ids[n] == s;
-        const unsigned b = __ballot_sync(0xFFFFFFFFu, mine);
-        if (lane == 0) warp_n[warp] = __popc(b);
-        __syncthreads();
-        if (warp == 0) {
-            const int v = warp_n[lane];
-            int sum = v;
+    int base = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                if (lane >= o) sum += u;
-            }
-            warp_n[lane] = sum - v;
-            if (lane == 31) total_sh = sum;
+    for (int w = 0; w < WARPS; ++w) base += warp_n[0][w];
+    if (t == 0) offsets[s] = base;
+    int buf = 1;
+    for (int n0 = 0; n0 < N; n0 += STEP, buf ^= 1) {
+        unsigned mine = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = n0 + 4 * t + e;
+            if (n < N && ids[n] == s) mine |= 1u << e;
         }
-        __syncthreads();
-        if (mine) perm[base + warp_n[warp] + __popc(b & ((1u << lane) - 1))] = n;
-        base += total_sh;
-        __syncthreads();
+        const int c = __popc(mine);
+        int sum = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += u;
+        }
+        if (lane == 31) warp_n[buf][warp] = sum;
+        __syncthreads();  // (the next step writes the other buffer, the one after that is past a barrier)
+        int at = base + sum - c;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const int u = warp_n[buf][w];
+            if (w < warp) at += u;
+            base += u;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (mine >> e & 1) perm[at++] = n0 + 4 * t + e;
     }
     if (s == S - 1 && t == 0) offsets[S] = base;
 }
 
-
-// What a backward pass has to lay out first, in one launch of blocks of 1024 threads:
+// What a backward pass has to lay out first, in one launch:
 // transposed copies out[q][c][r] = in[q][r][c] of `blocks` blocks of rows x cols (32 x
 // 32 tiles; out's rows are ld long, zeros past `rows`), and the rows of each adapter.
 struct Transpose {
@@ -599,7 +610,7 @@ struct PrepareArgs {
     int sorted;  // blocks that order rows (S or 0), before the tiles
 };
 template <typename T>
-__global__ void __launch_bounds__(1024) prepare_kernel(const __grid_constant__ PrepareArgs p) {
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ PrepareArgs p) {
     if ((int)blockIdx.x < p.sorted) {
         order_rows(p.ids, p.perm, p.offsets, p.N, p.S, (int)blockIdx.x);
         return;
@@ -612,15 +623,21 @@ __global__ void __launch_bounds__(1024) prepare_kernel(const __grid_constant__ P
     for (int j = 0; j < 3; ++j) {
         const Transpose &q = p.job[j];
         for (; at < q.tiles; at += step) {
-            const long long blk = at / (q.tr * q.tc);
-            const int rest = (int)(at - blk * (q.tr * q.tc)), r0 = rest / q.tc * 32, c0 = rest % q.tc * 32;
+            const unsigned per = (unsigned)(q.tr * q.tc);
+            const long long blk = q.tiles >> 32 ? at / per : (unsigned)at / per;
+            const int rest = (int)(at - blk * per), r0 = rest / q.tc * 32, c0 = rest % q.tc * 32;
             const T *in = static_cast<const T *>(q.in) + blk * q.rows * q.cols;
-            T v{};
-            if (r0 + y < q.rows && c0 + x < q.cols) v = in[(long long)(r0 + y) * q.cols + c0 + x];
-            tile[y][x] = v;
+#pragma unroll
+            for (int e = 0; e < 32; e += kPrepareThreads / 32) {
+                T v{};
+                if (r0 + y + e < q.rows && c0 + x < q.cols) v = in[(long long)(r0 + y + e) * q.cols + c0 + x];
+                tile[y + e][x] = v;
+            }
             __syncthreads();
-            if (c0 + y < q.cols && r0 + x < q.ld)
-                static_cast<T *>(q.out)[(blk * q.cols + c0 + y) * q.ld + r0 + x] = tile[x][y];
+#pragma unroll
+            for (int e = 0; e < 32; e += kPrepareThreads / 32)
+                if (c0 + y + e < q.cols && r0 + x < q.ld)
+                    static_cast<T *>(q.out)[(blk * q.cols + c0 + y + e) * q.ld + r0 + x] = tile[x][y + e];
             __syncthreads();
         }
         at -= q.tiles;
@@ -1246,13 +1263,13 @@ Transpose transpose(const void *in, void *out, long long blocks, long long rows,
 cudaError_t prepare(const Adapters &q, PrepareArgs &p, long long N) {
     long long tiles = 0;
     for (const Transpose &t : p.job) tiles += t.tiles;
-    const long long blocks = p.sorted + std::min<long long>(tiles, 2LL * sm_count() * 4);
+    const long long blocks = p.sorted + std::min<long long>(tiles, 16LL * sm_count());
     if (blocks == 0) return cudaSuccess;
     p.ids = q.ids, p.N = (int)N, p.S = q.S;
     if (q.bf16)
-        prepare_kernel<unsigned short><<<(unsigned)blocks, 1024, 0, q.st>>>(p);
+        prepare_kernel<unsigned short><<<(unsigned)blocks, kPrepareThreads, 0, q.st>>>(p);
     else
-        prepare_kernel<float><<<(unsigned)blocks, 1024, 0, q.st>>>(p);
+        prepare_kernel<float><<<(unsigned)blocks, kPrepareThreads, 0, q.st>>>(p);
     return cudaGetLastError();
 }
 
