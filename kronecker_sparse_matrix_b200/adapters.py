@@ -9,7 +9,7 @@ from typing import Optional
 
 import torch
 
-from . import KS_BF16, KS_F32, KS_TF32, KSLinear, Pattern, _act, _lib, _stream_ptr, bias_grad, matmul_dv
+from . import KS_BF16, KS_F32, KS_TF32, KSLinear, Pattern, _act, _lib, bias_grad, matmul_dv
 
 
 def _empty(shape, like: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
@@ -31,15 +31,15 @@ def _dtype_of(kind: int, tf32: bool) -> int:
     return KS_BF16 if kind == 1 else KS_TF32 if tf32 else KS_F32
 
 
-def _call(device: int, stream: Optional[torch.cuda.Stream], function: str, *args) -> None:
-    """The entry point on the given device, its current stream if none is given."""
-    dev = torch.device("cuda", device)
+def _call(device: int, function, *args) -> None:
+    """The entry point with the given device current."""
     if torch.cuda.current_device() == device:
-        st = getattr(_lib.load(), function)(*args, _stream_ptr(stream, dev))
+        st = function(*args)
     else:
-        with torch.cuda.device(dev):
-            st = getattr(_lib.load(), function)(*args, _stream_ptr(stream, dev))
-    _lib.check(st)
+        with torch.cuda.device(device):
+            st = function(*args)
+    if st:
+        _lib.check(st)
 
 
 def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: torch.Tensor, B: torch.Tensor,
@@ -59,14 +59,14 @@ def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: t
     fin, fout = a * c * d, a * b * d
     if values is None:
         raise ValueError("values must be a tensor")
-    batch, s, r, kind, dev, px, pv, pa, pb, pids, pscales, pbias = adapter_args(
+    batch, s, r, kind, dev, st, px, pv, pa, pb, pids, pscales, pbias = adapter_args(
         x, values, A, B, ids, scales, bias, fin, fin, fout, a * b * c * d, "x")
     if out is None:
         out = _empty((batch, fout), x, stream)
     elif not out.is_contiguous() or out.dtype != x.dtype or out.device != x.device or out.shape != (batch, fout):
         raise ValueError(f"out must be a contiguous ({batch}, {fout}) tensor with x's dtype and device")
-    _call(dev, stream, "ks_adapter_matmul", px, pv, a, b, c, d, batch, out.data_ptr(), _dtype_of(kind, tf32), pbias,
-          _act(act), pa, pb, pscales, pids, s, r)
+    _call(dev, _lib.load().ks_adapter_matmul, px, pv, a, b, c, d, batch, out.data_ptr(), _dtype_of(kind, tf32), pbias,
+          _act(act), pa, pb, pscales, pids, s, r, st if stream is None else stream.cuda_stream)
     return out
 
 
@@ -81,7 +81,7 @@ def adapter_backward(dy: torch.Tensor, x: Optional[torch.Tensor], values: Option
     from ._ks_marshal import adapter_args  # built with the library
     a, b, c, d = (int(v) for v in pattern)
     fin, fout = a * c * d, a * b * d
-    batch, s, r, kind, dev, pdy, pv, pa, pb, pids, pscales, _ = adapter_args(
+    batch, s, r, kind, dev, st, pdy, pv, pa, pb, pids, pscales, _ = adapter_args(
         dy, values, A, B, ids, scales, None, fout, fin, fout, a * b * c * d, "dy")
     if need_dx and values is None:
         raise ValueError("dX needs the values")
@@ -92,8 +92,8 @@ def adapter_backward(dy: torch.Tensor, x: Optional[torch.Tensor], values: Option
     dx = _empty((batch, fin), dy, stream) if need_dx else None
     da = _empty(A.shape, A, stream) if need_da else None
     db = _empty(B.shape, B, stream) if need_db else None
-    _call(dev, stream, "ks_adapter_backward", pdy, _ptr(x), pv, a, b, c, d, batch, _dtype_of(kind, tf32), pa, pb,
-          pscales, pids, s, r, _ptr(dx), _ptr(da), _ptr(db))
+    _call(dev, _lib.load().ks_adapter_backward, pdy, _ptr(x), pv, a, b, c, d, batch, _dtype_of(kind, tf32), pa, pb,
+          pscales, pids, s, r, _ptr(dx), _ptr(da), _ptr(db), st if stream is None else stream.cuda_stream)
     return dx, da, db
 
 

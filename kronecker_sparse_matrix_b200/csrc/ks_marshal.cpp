@@ -66,12 +66,20 @@ bool read(PyObject *o, Info *out) {
     return true;
 }
 
+// The current stream of a CUDA device, as torch has it; false with an error set.
+bool current_stream(int device, unsigned long long *out) {
+    void *st = nullptr;
+    if (g_api->current_work_stream(kDLCUDA, device, &st) != 0) return false;
+    *out = (unsigned long long)(uintptr_t)st;
+    return true;
+}
+
 const char *const kNames[7] = {"params", "grads", "exp_avgs", "exp_avg_sqs", "masters", "exp_avg_scales",
                                "exp_avg_sq_scales"};
 constexpr int64_t kBlock = 256;  // elements that share a scale in an 8-bit state
 
 // adamw_table(params, grads, exp_avgs, exp_avg_sqs, masters, exp_avg_scales, exp_avg_sq_scales)
-//   -> (table, tensors, dtype kind, state kind, device index)
+//   -> (table, tensors, dtype kind, state kind, device index, its current stream)
 // Lists of equal lengths; the last three may be None.
 PyObject *adamw_table(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     if (nargs != 7) return PyErr_Format(PyExc_TypeError, "adamw_table takes 7 lists");
@@ -79,6 +87,7 @@ PyObject *adamw_table(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     Py_ssize_t count = 0;
     int dtype = kNone, state = kNone, device = -1;
     uint64_t *words = nullptr;
+    unsigned long long stream = 0;
     for (int c = 0; c < 7; ++c) {
         if (args[c] == Py_None && c >= 4) continue;
         list[c] = PySequence_Fast(args[c], "expected lists of tensors");
@@ -141,7 +150,7 @@ PyObject *adamw_table(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
             words[8 * k + c] = t.ptr;
         }
     }
-    result = Py_BuildValue("Oniii", table, count, dtype, state, device);
+    if (current_stream(device, &stream)) result = Py_BuildValue("OniiiK", table, count, dtype, state, device, stream);
 done:
     Py_XDECREF(table);
     for (PyObject *l : list) Py_XDECREF(l);
@@ -149,7 +158,7 @@ done:
 }
 
 // adapter_args(x, values, A, B, ids, scales, bias, width, in_f, out_f, nvals, name)
-//   -> (rows, adapters, rank, dtype kind, device, x, values, A, B, ids, scales, bias)
+//   -> (rows, adapters, rank, dtype kind, device, its current stream, x, values, A, B, ids, scales, bias)
 // x: (rows, width), called `name` in messages; values, ids, scales and bias may be None (0).
 PyObject *adapter_args(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     if (nargs != 12) return PyErr_Format(PyExc_TypeError, "adapter_args takes 12 arguments");
@@ -191,7 +200,9 @@ PyObject *adapter_args(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     if (given(6) && (!like_x(t[6]) || t[6].numel != out_f))
         return PyErr_Format(PyExc_ValueError,
                             "bias must be a contiguous tensor of %lld elements with x's dtype and device", out_f);
-    return Py_BuildValue("LLLiiKKKKKKK", (long long)x.shape[0], s, r, x.kind, x.device, (unsigned long long)x.ptr,
+    unsigned long long stream = 0;
+    if (!current_stream(x.device, &stream)) return nullptr;
+    return Py_BuildValue("LLLiiKKKKKKKK", (long long)x.shape[0], s, r, x.kind, x.device, stream, (unsigned long long)x.ptr,
                          (unsigned long long)t[1].ptr, (unsigned long long)A.ptr, (unsigned long long)B.ptr,
                          (unsigned long long)t[4].ptr, (unsigned long long)t[5].ptr, (unsigned long long)t[6].ptr);
 }
@@ -220,7 +231,8 @@ PyMODINIT_FUNC PyInit__ks_marshal(void) {
     }
     const auto *api = static_cast<const DLPackExchangeAPI *>(PyCapsule_GetPointer(capsule, "dlpack_exchange_api"));
     Py_DECREF(capsule);
-    if (api && (api->header.version.major != DLPACK_MAJOR_VERSION || !api->dltensor_from_py_object_no_sync)) {
+    if (api && (api->header.version.major != DLPACK_MAJOR_VERSION || !api->dltensor_from_py_object_no_sync ||
+                !api->current_work_stream)) {
         PyErr_SetString(PyExc_ImportError, "torch's DLPack exchange functions have another version than this build");
         api = nullptr;
     }

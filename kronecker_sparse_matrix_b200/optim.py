@@ -8,7 +8,7 @@ from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
-from . import KS_BF16, KS_F32, _lib, _stream_ptr
+from . import KS_BF16, KS_F32, _lib
 
 ADAMW_BLOCK = 256  # elements that share a scale in an 8-bit state
 
@@ -17,10 +17,6 @@ def _scalar(name: str, t: torch.Tensor, dtype: torch.dtype, device: int) -> int:
     if t.dtype != dtype or t.get_device() != device or t.numel() != 1:
         raise ValueError(f"{name} as a tensor must hold one {dtype} on cuda:{device}")
     return t.data_ptr()
-
-
-def _run(device: int, opt, args, stream: Optional[torch.cuda.Stream]) -> int:
-    return _lib.load().ks_adamw_step(*args, ctypes.byref(opt), _stream_ptr(stream, torch.device("cuda", device)))
 
 
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor],
@@ -45,8 +41,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
         raise ValueError("exp_avg_scales and exp_avg_sq_scales come together")
     from ._ks_marshal import adamw_table  # built with the library
-    table, count, dtype, state, dev = adamw_table(params, grads, exp_avgs, exp_avg_sqs, masters, exp_avg_scales,
-                                                  exp_avg_sq_scales)
+    table, count, dtype, state, dev, st = adamw_table(params, grads, exp_avgs, exp_avg_sqs, masters,
+                                                      exp_avg_scales, exp_avg_sq_scales)
     bits = 8 if state == 2 else 32  # kinds: 0 float32, 1 bfloat16, 2 float8_e4m3fn
     if (bits == 8) != (exp_avg_scales is not None):
         raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales, 32-bit states take none")
@@ -61,13 +57,16 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
         opt.step = step
     if grad_scale is not None:
         opt.grad_scale = _scalar("grad_scale", grad_scale, torch.float32, dev)
-    args = (table, count, KS_BF16 if dtype == 1 else KS_F32, bits)
+    step_fn = _lib.load().ks_adamw_step
+    args = (table, count, KS_BF16 if dtype == 1 else KS_F32, bits, ctypes.byref(opt),
+            st if stream is None else stream.cuda_stream)
     if torch.cuda.current_device() == dev:
-        st = _run(dev, opt, args, stream)
+        status = step_fn(*args)
     else:
         with torch.cuda.device(dev):
-            st = _run(dev, opt, args, stream)
-    _lib.check(st)
+            status = step_fn(*args)
+    if status:
+        _lib.check(status)
 
 
 class AdamW(torch.optim.Optimizer):
