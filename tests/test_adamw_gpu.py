@@ -181,6 +181,20 @@ def test_small_second_state_never_becomes_zero():
     assert (q["v"][0].float() > 0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_second_state_below_the_normal_range_of_fp32_is_kept(dtype):
+    """v is subnormal in fp32 here, about 4e-39; its root, 6e-20, is held."""
+    q = make([512], dtype, 8)
+    q["m"][0].zero_(), q["v"][0].zero_()
+    q["g"][0].fill_(6e-19)
+    step(q, 8, step=1)
+    g = q["g"][0].double()
+    root = spread(q["vs"][0], 512) * q["v"][0].double()
+    want = ((1 - HYPER["betas"][1]) * g * g).sqrt()
+    # half a step of e4m3; v to half a spacing (2^-149) of the subnormal numbers, 2e-7 of 4e-39
+    assert ((root - want).abs() <= (2.0 ** -4 + 1e-5) * want).all()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_nan_and_infinite_gradients_stay_where_they_are(bits):
     q = make([1024], torch.float32, bits)
