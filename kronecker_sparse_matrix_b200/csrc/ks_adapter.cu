@@ -559,17 +559,23 @@ constexpr int kPrepareThreads = 256;
 
 // The rows of each adapter in order: perm[offsets[s] .. offsets[s + 1]) holds the
 // rows with id s.  The block counts the rows of smaller ids, then writes the rows of
-// its own, 1024 ids at a time, four neighbouring ones a thread.
+// its own, 4096 ids at a time, 16 neighbouring ones a thread: the loads of a step are in
+// flight together, and their latency is what this costs.
 __device__ void order_rows(const int *__restrict__ ids, int *__restrict__ perm, int *__restrict__ offsets, int N, int S,
                            int s) {
-    constexpr int WARPS = kPrepareThreads / 32, STEP = 4 * kPrepareThreads;
+    constexpr int WARPS = kPrepareThreads / 32, EACH = 16, STEP = EACH * kPrepareThreads;
     __shared__ int warp_n[2][WARPS];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     int less = 0;
-#pragma unroll 4
-    for (int n = t; n < N; n += kPrepareThreads) {
-        const int id = ids[n];
-        less += id >= 0 && id < s;
+    for (int n0 = 0; n0 < N; n0 += STEP) {
+        int id[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const int n = n0 + e * kPrepareThreads + t;
+            id[e] = n < N ? ids[n] : -1;
+        }
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) less += id[e] >= 0 && id[e] < s;
     }
     less = __reduce_add_sync(0xFFFFFFFFu, less);
     if (lane == 0) warp_n[0][warp] = less;
@@ -580,12 +586,11 @@ __device__ void order_rows(const int *__restrict__ ids, int *__restrict__ perm, 
     if (t == 0) offsets[s] = base;
     int buf = 1;
     for (int n0 = 0; n0 < N; n0 += STEP, buf ^= 1) {
+        const int first = n0 + EACH * t;
         unsigned mine = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int n = n0 + 4 * t + e;
-            if (n < N && ids[n] == s) mine |= 1u << e;
-        }
+        for (int e = 0; e < EACH; ++e)
+            if (first + e < N && ids[first + e] == s) mine |= 1u << e;
         const int c = __popc(mine);
         int sum = c;
 #pragma unroll
@@ -602,9 +607,7 @@ __device__ void order_rows(const int *__restrict__ ids, int *__restrict__ perm, 
             if (w < warp) at += u;
             base += u;
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (mine >> e & 1) perm[at++] = n0 + 4 * t + e;
+        for (; mine; mine &= mine - 1) perm[at++] = first + __ffs(mine) - 1;
     }
     if (s == S - 1 && t == 0) offsets[S] = base;
 }
@@ -1068,8 +1071,7 @@ cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf1
         using O = decltype(h);
         return nt == 1   ? go(shrink_mma_kernel<1, 1, O>)
                : nt == 2 ? go(shrink_mma_kernel<1, 2, O>)
-               : nt == 4 ? go(shrink_mma_kernel<2, 4, O>)
-                         : go(shrink_mma_kernel<2, 8, O>);
+                         : go(shrink_mma_kernel<2, 4, O>);
     };
     return h_bf16 ? ranks(__nv_bfloat16{}) : ranks(float{});
 }
