@@ -99,6 +99,17 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+_addresses: dict = {}
+
+
+def address(name: str) -> int:
+    """The address of an entry point, for the native callers of the binding."""
+    found = _addresses.get(name)
+    if found is None:
+        found = _addresses[name] = ctypes.cast(getattr(load(), name), _vp).value
+    return found
+
+
 def check(status: int) -> None:
     if status != 0:
         msg = load().ks_last_error().decode(errors="replace")

@@ -5,6 +5,7 @@ marshals torch tensors into the C ABI (ks_adapter_matmul, ks_adapter_backward).
 """
 from __future__ import annotations
 
+import weakref
 from typing import Optional
 
 import torch
@@ -54,19 +55,22 @@ def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: t
     scales: float32, one per adapter (None: ones).  An id that is too large
     takes no adapter, and the next ``sync_status`` raises.  Rows of one adapter
     next to each other run fastest.  Asynchronous on ``stream``."""
-    from ._ks_marshal import adapter_args  # built with the library
-    a, b, c, d = (int(v) for v in pattern)
-    fin, fout = a * c * d, a * b * d
+    from ._ks_marshal import adapter_matmul as run  # built with the library
+    a, b, c, d = pattern
+    args = (_lib.address("ks_adapter_matmul"), x, values, A, B, ids, scales, bias, out, int(a), int(b), int(c), int(d),
+            _act(act), (KS_TF32, -1) if tf32 else (KS_F32, KS_BF16))
     if values is None:
         raise ValueError("values must be a tensor")
-    batch, s, r, kind, dev, st, px, pv, pa, pb, pids, pscales, pbias = adapter_args(
-        x, values, A, B, ids, scales, bias, fin, fin, fout, a * b * c * d, "x")
-    if out is None:
-        out = _empty((batch, fout), x, stream)
-    elif not out.is_contiguous() or out.dtype != x.dtype or out.device != x.device or out.shape != (batch, fout):
-        raise ValueError(f"out must be a contiguous ({batch}, {fout}) tensor with x's dtype and device")
-    _call(dev, _lib.load().ks_adapter_matmul, px, pv, a, b, c, d, batch, out.data_ptr(), _dtype_of(kind, tf32), pbias,
-          _act(act), pa, pb, pscales, pids, s, r, st if stream is None else stream.cuda_stream)
+    if stream is not None:  # a new output's memory belongs to the stream that writes it
+        with torch.cuda.stream(stream):
+            status, out = run(*args, stream.cuda_stream)
+    elif not isinstance(x, torch.Tensor) or not x.is_cuda or x.get_device() == torch.cuda.current_device():
+        status, out = run(*args, None)
+    else:
+        with torch.cuda.device(x.get_device()):
+            status, out = run(*args, None)
+    if status:
+        _lib.check(status)
     return out
 
 
@@ -97,11 +101,30 @@ def adapter_backward(dy: torch.Tensor, x: Optional[torch.Tensor], values: Option
     return dx, da, db
 
 
+class _EagerGraph:
+    """The leaves of an autograd graph recorded on the default stream, while that graph lives.
+
+    A leaf's gradient is accumulated on the stream where the first living graph of it was
+    recorded.  Were that the default stream, a captured backward pass would have to
+    wait there, which no capture allows: the engine's error can end the process.  So a
+    backward pass refuses it before it starts."""
+    __slots__ = ("leaves", "__weakref__")
+
+
+_eager_graphs = weakref.WeakSet()
+
+
 class _KSAdapterFn(torch.autograd.Function):
     """y = x K^T + bias + the adapters' products; every gradient on the GPU."""
 
     @staticmethod
     def forward(ctx, x, values, bias, A, B, scales, ids, pattern):
+        ctx.leaves = [weakref.ref(t) for t, need in zip((x, values, bias, A, B), ctx.needs_input_grad)
+                      if need and t.is_leaf]
+        if ctx.leaves and torch.cuda.current_stream(x.device).cuda_stream == 0:
+            ctx.graph = _EagerGraph()
+            ctx.graph.leaves = ctx.leaves
+            _eager_graphs.add(ctx.graph)
         values, A, B = values.contiguous(), A.contiguous(), B.contiguous()
         ctx.pattern = pattern
         ctx.save_for_backward(x, values, A, B, scales, ids)
@@ -112,6 +135,11 @@ class _KSAdapterFn(torch.autograd.Function):
     def backward(ctx, dy):
         x, values, A, B, scales, ids = ctx.saved_tensors
         need = ctx.needs_input_grad
+        if torch.cuda.is_current_stream_capturing():
+            mine = {id(leaf()) for leaf in ctx.leaves} - {id(None)}
+            if any(id(leaf()) in mine for graph in _eager_graphs for leaf in graph.leaves):
+                raise RuntimeError("an autograd graph of the same tensors, recorded on the default stream, still lives: "
+                                   "release its results before a backward pass is captured")
         dy = dy.contiguous()
         dx = da = db = None
         if need[0] or need[3] or need[4]:
@@ -129,7 +157,9 @@ class KSAdapterLinear(KSLinear):
     A (n_adapters, rank, in_features) is drawn N(0, 1/in_features), B
     (n_adapters, out_features, rank) starts at zero, so a fresh layer is its
     KSLinear.  ``scales`` is a buffer of alpha/rank per adapter (alpha defaults
-    to rank).  ``freeze_base()`` leaves the adapters alone to be trained."""
+    to rank).  ``freeze_base()`` leaves the adapters alone to be trained.  A
+    training step can be captured into a CUDA graph once the results of earlier steps
+    on the default stream are released (warm up on another stream)."""
 
     def __init__(self, pattern: Pattern, n_adapters: int, rank: int, alpha: Optional[float] = None, bias: bool = False,
                  dtype=torch.float32, device=None):

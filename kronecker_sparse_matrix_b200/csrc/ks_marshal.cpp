@@ -157,59 +157,143 @@ done:
     return result;
 }
 
-// adapter_args(x, values, A, B, ids, scales, bias, width, in_f, out_f, nvals, name)
-//   -> (rows, adapters, rank, dtype kind, device, its current stream, x, values, A, B, ids, scales, bias)
-// x: (rows, width), called `name` in messages; values, ids, scales and bias may be None (0).
-PyObject *adapter_args(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
-    if (nargs != 12) return PyErr_Format(PyExc_TypeError, "adapter_args takes 12 arguments");
-    long long size[4];
-    for (int k = 0; k < 4; ++k) {
-        size[k] = PyLong_AsLongLong(args[7 + k]);
-        if (size[k] == -1 && PyErr_Occurred()) return nullptr;
-    }
-    const long long width = size[0], in_f = size[1], out_f = size[2], nvals = size[3];
-    Info t[7];
+// Reads and checks the tensors of an adapter call, args: x, values, A, B, ids, scales, bias.
+// x: (rows, width), called `name` in messages; values, ids, scales and bias may be None.
+bool check_adapters(PyObject *const *args, long long width, long long in_f, long long out_f, long long nvals,
+                    const char *name, Info (&t)[7]) {
     for (int k = 0; k < 7; ++k) {
         t[k] = Info{};
         if (args[k] == Py_None && k != 0 && k != 2 && k != 3) continue;
-        if (!read(args[k], &t[k])) return nullptr;
+        if (!read(args[k], &t[k])) return false;
     }
     const Info &x = t[0], &A = t[2], &B = t[3];
     const auto given = [&](int k) { return args[k] != Py_None; };
     const auto like_x = [&](const Info &o) { return o.kind == x.kind && o.device == x.device && o.contiguous; };
-    if (x.kind != kF32 && x.kind != kBF16)
-        return PyErr_Format(PyExc_TypeError, "unsupported dtype of %U: use float32 or bfloat16", args[11]);
-    if (x.ndim != 2 || x.device < 0 || !x.contiguous || x.shape[1] != width)
-        return PyErr_Format(PyExc_ValueError, "%U must be a contiguous CUDA tensor of shape (batch, %lld)", args[11], width);
-    if (A.ndim != 3 || A.shape[2] != in_f || A.shape[0] == 0 || A.shape[1] == 0)
-        return PyErr_Format(PyExc_ValueError, "A must have shape (adapters, rank, %lld)", in_f);
     const long long s = A.shape[0], r = A.shape[1];
-    if (B.ndim != 3 || B.shape[0] != s || B.shape[1] != out_f || B.shape[2] != r)
-        return PyErr_Format(PyExc_ValueError, "B must have shape (%lld, %lld, %lld)", s, out_f, r);
-    if (!like_x(A) || !like_x(B) || (given(1) && !like_x(t[1])))
-        return PyErr_Format(PyExc_ValueError, "values, A and B must be contiguous, with %U's dtype and device", args[11]);
-    if (given(1) && t[1].numel != nvals) return PyErr_Format(PyExc_ValueError, "values must have %lld elements", nvals);
-    if (given(4) && (t[4].kind != kI32 || t[4].device != x.device || t[4].ndim != 1 || t[4].shape[0] != x.shape[0] ||
-                     !t[4].contiguous))
-        return PyErr_Format(PyExc_ValueError,
-                            "ids must be a contiguous int32 tensor with one entry per row, on the same device");
-    if (given(5) && (t[5].kind != kF32 || t[5].device != x.device || t[5].ndim != 1 || t[5].shape[0] != s ||
-                     !t[5].contiguous))
-        return PyErr_Format(PyExc_ValueError,
-                            "scales must be a contiguous float32 tensor with one entry per adapter, on the same device");
-    if (given(6) && (!like_x(t[6]) || t[6].numel != out_f))
-        return PyErr_Format(PyExc_ValueError,
-                            "bias must be a contiguous tensor of %lld elements with x's dtype and device", out_f);
+    if (x.kind != kF32 && x.kind != kBF16)
+        PyErr_Format(PyExc_TypeError, "unsupported dtype of %s: use float32 or bfloat16", name);
+    else if (x.ndim != 2 || x.device < 0 || !x.contiguous || x.shape[1] != width)
+        PyErr_Format(PyExc_ValueError, "%s must be a contiguous CUDA tensor of shape (batch, %lld)", name, width);
+    else if (A.ndim != 3 || A.shape[2] != in_f || s == 0 || r == 0)
+        PyErr_Format(PyExc_ValueError, "A must have shape (adapters, rank, %lld)", in_f);
+    else if (B.ndim != 3 || B.shape[0] != s || B.shape[1] != out_f || B.shape[2] != r)
+        PyErr_Format(PyExc_ValueError, "B must have shape (%lld, %lld, %lld)", s, out_f, r);
+    else if (!like_x(A) || !like_x(B) || (given(1) && !like_x(t[1])))
+        PyErr_Format(PyExc_ValueError, "values, A and B must be contiguous, with %s's dtype and device", name);
+    else if (given(1) && t[1].numel != nvals)
+        PyErr_Format(PyExc_ValueError, "values must have %lld elements", nvals);
+    else if (given(4) && (t[4].kind != kI32 || t[4].device != x.device || t[4].ndim != 1 ||
+                          t[4].shape[0] != x.shape[0] || !t[4].contiguous))
+        PyErr_SetString(PyExc_ValueError,
+                        "ids must be a contiguous int32 tensor with one entry per row, on the same device");
+    else if (given(5) && (t[5].kind != kF32 || t[5].device != x.device || t[5].ndim != 1 || t[5].shape[0] != s ||
+                          !t[5].contiguous))
+        PyErr_SetString(PyExc_ValueError,
+                        "scales must be a contiguous float32 tensor with one entry per adapter, on the same device");
+    else if (given(6) && (!like_x(t[6]) || t[6].numel != out_f))
+        PyErr_Format(PyExc_ValueError, "bias must be a contiguous tensor of %lld elements with x's dtype and device",
+                     out_f);
+    else
+        return true;
+    return false;
+}
+
+// The integers of args[0 .. n); false with an error set.
+bool integers(PyObject *const *args, int n, long long *out) {
+    for (int k = 0; k < n; ++k) {
+        out[k] = PyLong_AsLongLong(args[k]);
+        if (out[k] == -1 && PyErr_Occurred()) return false;
+    }
+    return true;
+}
+
+// adapter_args(x, values, A, B, ids, scales, bias, width, in_f, out_f, nvals, name)
+//   -> (rows, adapters, rank, dtype kind, device, its current stream, x, values, A, B, ids, scales, bias)
+// The addresses of tensors that are None are 0.
+PyObject *adapter_args(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    if (nargs != 12) return PyErr_Format(PyExc_TypeError, "adapter_args takes 12 arguments");
+    long long size[4];
+    Info t[7];
+    const char *name = PyUnicode_AsUTF8(args[11]);
+    if (!name || !integers(args + 7, 4, size) || !check_adapters(args, size[0], size[1], size[2], size[3], name, t))
+        return nullptr;
     unsigned long long stream = 0;
-    if (!current_stream(x.device, &stream)) return nullptr;
-    return Py_BuildValue("LLLiiKKKKKKKK", (long long)x.shape[0], s, r, x.kind, x.device, stream, (unsigned long long)x.ptr,
-                         (unsigned long long)t[1].ptr, (unsigned long long)A.ptr, (unsigned long long)B.ptr,
-                         (unsigned long long)t[4].ptr, (unsigned long long)t[5].ptr, (unsigned long long)t[6].ptr);
+    if (!current_stream(t[0].device, &stream)) return nullptr;
+    return Py_BuildValue("LLLiiKKKKKKKK", (long long)t[0].shape[0], (long long)t[2].shape[0], (long long)t[2].shape[1],
+                         t[0].kind, t[0].device, stream, (unsigned long long)t[0].ptr, (unsigned long long)t[1].ptr,
+                         (unsigned long long)t[2].ptr, (unsigned long long)t[3].ptr, (unsigned long long)t[4].ptr,
+                         (unsigned long long)t[5].ptr, (unsigned long long)t[6].ptr);
+}
+
+// adapter_matmul(function, x, values, A, B, ids, scales, bias, out, a, b, c, d, activation, dtypes, stream)
+//   -> (status, out)
+// Checks the tensors, makes out (None: a new tensor) and calls ks_adapter_matmul
+// (function: its address).  dtypes: (ks_dtype of float32 tensors, of bfloat16 ones or
+// -1); stream: None for the current one.  Through ctypes the call alone takes 2 us more.
+using AdapterMatmul = int (*)(const void *, const void *, int64_t, int64_t, int64_t, int64_t, int64_t, void *, int,
+                              const void *, int, const void *, const void *, const float *, const int32_t *, int64_t,
+                              int64_t, void *);
+PyObject *adapter_matmul(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    if (nargs != 16) return PyErr_Format(PyExc_TypeError, "adapter_matmul takes 16 arguments");
+    const auto function = reinterpret_cast<AdapterMatmul>(PyLong_AsVoidPtr(args[0]));
+    if (!function) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "no function");
+    long long n[5];  // a, b, c, d, activation
+    int dtypes[2];
+    if (!integers(args + 9, 5, n) || !PyArg_ParseTuple(args[14], "ii", &dtypes[0], &dtypes[1])) return nullptr;
+    long long in_f, out_f, nvals;
+    if (__builtin_mul_overflow(n[0], n[3], &out_f) || __builtin_mul_overflow(out_f, n[2], &in_f) ||
+        __builtin_mul_overflow(out_f, n[1], &out_f) || __builtin_mul_overflow(in_f, n[1], &nvals))
+        return PyErr_Format(PyExc_ValueError, "the pattern's sizes overflow");
+    Info t[7];
+    if (!check_adapters(args + 1, in_f, in_f, out_f, nvals, "x", t)) return nullptr;
+    const Info &x = t[0];
+    const int dtype = dtypes[x.kind == kBF16];
+    if (dtype < 0) return PyErr_Format(PyExc_ValueError, "tf32 applies to fp32 tensors only");
+    unsigned long long stream = 0;
+    if (args[15] == Py_None) {
+        if (!current_stream(x.device, &stream)) return nullptr;
+    } else {
+        stream = PyLong_AsUnsignedLongLong(args[15]);
+        if (PyErr_Occurred()) return nullptr;
+    }
+    PyObject *out = nullptr;
+    if (args[8] == Py_None) {
+        PyObject *shape = Py_BuildValue("((LL))", (long long)x.shape[0], out_f);
+        PyObject *make = shape ? PyObject_GetAttrString(args[1], "new_empty") : nullptr;
+        if (make) out = PyObject_CallObject(make, shape);
+        Py_XDECREF(make);
+        Py_XDECREF(shape);
+    } else {
+        out = args[8];
+        Py_INCREF(out);
+    }
+    if (!out) return nullptr;
+    Info y;
+    if (!read(out, &y)) {
+        Py_DECREF(out);
+        return nullptr;
+    }
+    if (y.kind != x.kind || y.device != x.device || !y.contiguous || y.ndim != 2 || y.shape[0] != x.shape[0] ||
+        y.shape[1] != out_f) {
+        Py_DECREF(out);
+        return PyErr_Format(PyExc_ValueError, "out must be a contiguous (%lld, %lld) tensor with x's dtype and device",
+                            (long long)x.shape[0], out_f);
+    }
+    const auto ptr = [](const Info &o) { return reinterpret_cast<void *>((uintptr_t)o.ptr); };
+    int status = 0;
+    Py_BEGIN_ALLOW_THREADS
+    status = function(ptr(x), ptr(t[1]), n[0], n[1], n[2], n[3], x.shape[0], ptr(y), dtype, ptr(t[6]), (int)n[4],
+                      ptr(t[2]), ptr(t[3]), static_cast<const float *>(ptr(t[5])), static_cast<const int32_t *>(ptr(t[4])),
+                      t[2].shape[0], t[2].shape[1], reinterpret_cast<void *>((uintptr_t)stream));
+    Py_END_ALLOW_THREADS
+    return Py_BuildValue("iN", status, out);
 }
 
 PyMethodDef kMethods[] = {
     {"adapter_args", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adapter_args)), METH_FASTCALL,
-     "Checked arguments of the adapter calls."},
+     "Checked arguments of an adapter call."},
+    {"adapter_matmul", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adapter_matmul)), METH_FASTCALL,
+     "ks_adapter_matmul on torch tensors."},
     {"adamw_table", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adamw_table)), METH_FASTCALL,
      "The table of ks_adamw_step from lists of tensors."},
     {nullptr, nullptr, 0, nullptr}};

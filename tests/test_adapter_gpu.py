@@ -502,3 +502,62 @@ def test_binding_refusals():
         ks.adapter_backward(q["dy"], None, q["values"], p, **good)
     with pytest.raises(ks.KsError, match="overlaps"):
         ks.adapter_matmul(q["x"], q["values"], p, **good, out=q["B"].view(-1)[:6 * 512].view(6, 512))
+
+
+def layer_of(dtype):
+    torch.manual_seed(5)
+    layer = ks.KSAdapterLinear((1, 256, 64, 16), 3, 16, bias=True, dtype=dtype, device=DEV)
+    with torch.no_grad():
+        layer.B.normal_(std=0.1)
+    ids = (torch.arange(300, device=DEV) // 70 - 1).clamp(max=2).to(torch.int32)
+    return layer, ids, torch.randn(2, 300, 1024, device=DEV, dtype=dtype), torch.randn(2, 300, 4096, device=DEV, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_captured_training_step_follows_its_inputs(dtype):
+    layer, ids, xs, dys = layer_of(dtype)
+    x, dy = xs[0].clone(), dys[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            layer.zero_grad(set_to_none=True)
+            layer(x, ids).backward(dy)
+    torch.cuda.current_stream().wait_stream(side)
+    layer.zero_grad(set_to_none=True)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = layer(x, ids)
+        y.backward(dy)
+    for k in (1, 0):
+        x.copy_(xs[k]), dy.copy_(dys[k])
+        for p in layer.parameters():
+            p.grad.zero_()
+        g.replay()
+        p = layer.pattern
+        with torch.no_grad():
+            assert torch.equal(y, ks.adapter_matmul(x, layer.values, p, layer.A, layer.B, ids, layer.scales,
+                                                    bias=layer.bias))
+            _, da, db = ks.adapter_backward(dy, x, layer.values, p, layer.A, layer.B, ids, layer.scales)
+        # (a captured gradient is written where it was first made: zeroed or not, it holds this replay's alone)
+        assert torch.equal(layer.A.grad, da) and torch.equal(layer.B.grad, db)
+        assert torch.equal(layer.bias.grad, ks.bias_grad(dy))
+        assert torch.equal(layer.values.grad, ks.matmul_dv(dy, x, p))
+
+
+def test_capture_is_refused_while_an_eager_graph_of_the_leaves_lives():
+    layer, ids, xs, dys = layer_of(torch.bfloat16)
+    eager = layer(xs[0], ids)  # on the default stream, never differentiated
+    with pytest.raises(RuntimeError, match="still lives"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            layer(xs[0], ids).backward(dys[0])
+    with torch.cuda.graph(torch.cuda.CUDAGraph()), torch.no_grad():  # a forward pass has nothing to wait for
+        layer(xs[0], ids)
+    del eager
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer(xs[0], ids).backward(dys[0])
+    g.replay()
+    _, da, _ = ks.adapter_backward(dys[0], xs[0], layer.values.detach(), layer.pattern, layer.A.detach(),
+                                   layer.B.detach(), ids, layer.scales)
+    assert torch.equal(layer.A.grad, da)
