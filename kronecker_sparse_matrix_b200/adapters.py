@@ -12,35 +12,18 @@ import torch
 
 from . import KS_BF16, KS_F32, KS_TF32, KSLinear, Pattern, _act, _lib, bias_grad, matmul_dv
 
-
-def _empty(shape, like: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """An uninitialised tensor whose memory belongs to the stream that writes it."""
-    if stream is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+_DTYPES, _DTYPES_TF32 = (KS_F32, KS_BF16), (KS_TF32, -1)
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _dtype_of(kind: int, tf32: bool) -> int:
-    """ks_dtype of a kind of _ks_marshal (0 float32, 1 bfloat16)."""
-    if kind == 1 and tf32:
-        raise ValueError("tf32 applies to fp32 tensors only")
-    return KS_BF16 if kind == 1 else KS_TF32 if tf32 else KS_F32
-
-
-def _call(device: int, function, *args) -> None:
-    """The entry point with the given device current."""
-    if torch.cuda.current_device() == device:
-        st = function(*args)
-    else:
-        with torch.cuda.device(device):
-            st = function(*args)
-    if st:
-        _lib.check(st)
+def _on_device(run, args, x, stream):
+    """run(*args, stream) with x's device current; on a stream given, new tensors' memory belongs to it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return run(*args, stream.cuda_stream)
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.get_device() == torch.cuda.current_device():
+        return run(*args, None)
+    with torch.cuda.device(x.get_device()):
+        return run(*args, None)
 
 
 def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: torch.Tensor, B: torch.Tensor,
@@ -58,17 +41,10 @@ def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: t
     from ._ks_marshal import adapter_matmul as run  # built with the library
     a, b, c, d = pattern
     args = (_lib.address("ks_adapter_matmul"), x, values, A, B, ids, scales, bias, out, int(a), int(b), int(c), int(d),
-            _act(act), (KS_TF32, -1) if tf32 else (KS_F32, KS_BF16))
+            _act(act), _DTYPES_TF32 if tf32 else _DTYPES)
     if values is None:
         raise ValueError("values must be a tensor")
-    if stream is not None:  # a new output's memory belongs to the stream that writes it
-        with torch.cuda.stream(stream):
-            status, out = run(*args, stream.cuda_stream)
-    elif not isinstance(x, torch.Tensor) or not x.is_cuda or x.get_device() == torch.cuda.current_device():
-        status, out = run(*args, None)
-    else:
-        with torch.cuda.device(x.get_device()):
-            status, out = run(*args, None)
+    status, out = _on_device(run, args, x, stream)
     if status:
         _lib.check(status)
     return out
@@ -82,22 +58,13 @@ def adapter_backward(dy: torch.Tensor, x: Optional[torch.Tensor], values: Option
     dY (batch, a*b*d); None in the place of one that is not needed (values may
     be None without dX, x without dA and dB).  An adapter without rows gets
     zeros.  Deterministic; fp32 sums, bf16 gradients rounded once."""
-    from ._ks_marshal import adapter_args  # built with the library
-    a, b, c, d = (int(v) for v in pattern)
-    fin, fout = a * c * d, a * b * d
-    batch, s, r, kind, dev, st, pdy, pv, pa, pb, pids, pscales, _ = adapter_args(
-        dy, values, A, B, ids, scales, None, fout, fin, fout, a * b * c * d, "dy")
-    if need_dx and values is None:
-        raise ValueError("dX needs the values")
-    if need_da or need_db:
-        if x is None or x.shape != (batch, fin) or x.dtype != dy.dtype or x.device != dy.device or \
-                not x.is_contiguous():
-            raise ValueError(f"x must be a contiguous ({batch}, {fin}) tensor with dy's dtype and device")
-    dx = _empty((batch, fin), dy, stream) if need_dx else None
-    da = _empty(A.shape, A, stream) if need_da else None
-    db = _empty(B.shape, B, stream) if need_db else None
-    _call(dev, _lib.load().ks_adapter_backward, pdy, _ptr(x), pv, a, b, c, d, batch, _dtype_of(kind, tf32), pa, pb,
-          pscales, pids, s, r, _ptr(dx), _ptr(da), _ptr(db), st if stream is None else stream.cuda_stream)
+    from ._ks_marshal import adapter_backward as run  # built with the library
+    a, b, c, d = pattern
+    args = (_lib.address("ks_adapter_backward"), dy, values, A, B, ids, scales, x, int(a), int(b), int(c), int(d),
+            need_dx, need_da, need_db, _DTYPES_TF32 if tf32 else _DTYPES)
+    status, dx, da, db = _on_device(run, args, dy, stream)
+    if status:
+        _lib.check(status)
     return dx, da, db
 
 

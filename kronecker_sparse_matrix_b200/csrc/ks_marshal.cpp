@@ -1,10 +1,10 @@
-// Checks and reads torch tensors for the Python binding (the table of
-// ks_adamw_step, the arguments of the adapter calls): type, device, contiguity,
-// shape and address of each tensor through the DLPack exchange functions that
-// torch.Tensor publishes (__dlpack_c_exchange_api__), so that no torch type is
-// needed here.  The same checks as attribute reads from Python take 18 us for a
-// list of 60 tensors, an order of magnitude more than here, and a step has up to
-// seven lists; for one adapter call they take half of a single token's time.
+// The calls of the Python binding whose own time counts (adapters, AdamW): checks and
+// reads torch tensors and calls the library.  Type, device, contiguity, shape and
+// address of each tensor come through the DLPack exchange functions that torch.Tensor
+// publishes (__dlpack_c_exchange_api__), so that no torch type is needed here.  The same
+// checks as attribute reads from Python take 18 us for a list of 60 tensors, an order of
+// magnitude more than here, and a step has up to seven lists; for one adapter call they
+// take half of a single token's time.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -74,16 +74,122 @@ bool current_stream(int device, unsigned long long *out) {
     return true;
 }
 
+// The integers of args[0 .. n); false with an error set.
+bool integers(PyObject *const *args, int n, long long *out) {
+    for (int k = 0; k < n; ++k) {
+        out[k] = PyLong_AsLongLong(args[k]);
+        if (out[k] == -1 && PyErr_Occurred()) return false;
+    }
+    return true;
+}
+
+// The sizes of a pattern's product.
+struct Sizes {
+    long long in_f, out_f, nvals;
+};
+bool sizes_of(const long long *p, Sizes *o) {
+    if (__builtin_mul_overflow(p[0], p[3], &o->out_f) || __builtin_mul_overflow(o->out_f, p[2], &o->in_f) ||
+        __builtin_mul_overflow(o->out_f, p[1], &o->out_f) || __builtin_mul_overflow(o->in_f, p[1], &o->nvals)) {
+        PyErr_SetString(PyExc_ValueError, "the pattern's sizes overflow");
+        return false;
+    }
+    return true;
+}
+
+// The ks_dtype of tensors of kind k from a pair (of float32 tensors, of bfloat16 ones or -1).
+bool dtype_of(PyObject *pair, int k, int *out) {
+    int d[2];
+    if (!PyArg_ParseTuple(pair, "ii", &d[0], &d[1])) return false;
+    *out = d[k == kBF16];
+    if (*out < 0) PyErr_SetString(PyExc_ValueError, "tf32 applies to fp32 tensors only");
+    return *out >= 0;
+}
+
+// The stream of a call: the handle given, or for None the device's current one.
+bool stream_of(PyObject *given, int device, unsigned long long *out) {
+    if (given == Py_None) return current_stream(device, out);
+    *out = PyLong_AsUnsignedLongLong(given);
+    return !PyErr_Occurred();
+}
+
+// A new tensor of the given shape with the dtype and device of `like`.
+PyObject *new_empty(PyObject *like, const int64_t *shape, int ndim, Info *info) {
+    PyObject *args = ndim == 2 ? Py_BuildValue("((LL))", (long long)shape[0], (long long)shape[1])
+                               : Py_BuildValue("((LLL))", (long long)shape[0], (long long)shape[1], (long long)shape[2]);
+    PyObject *make = args ? PyObject_GetAttrString(like, "new_empty") : nullptr;
+    PyObject *out = make ? PyObject_CallObject(make, args) : nullptr;
+    Py_XDECREF(make);
+    Py_XDECREF(args);
+    if (out && !read(out, info)) Py_CLEAR(out);
+    return out;
+}
+
+void *address(const Info &o) { return reinterpret_cast<void *>((uintptr_t)o.ptr); }
+
 const char *const kNames[7] = {"params", "grads", "exp_avgs", "exp_avg_sqs", "masters", "exp_avg_scales",
                                "exp_avg_sq_scales"};
 constexpr int64_t kBlock = 256;  // elements that share a scale in an 8-bit state
 
-// adamw_table(params, grads, exp_avgs, exp_avg_sqs, masters, exp_avg_scales, exp_avg_sq_scales)
-//   -> (table, tensors, dtype kind, state kind, device index, its current stream)
-// Lists of equal lengths; the last three may be None.
-PyObject *adamw_table(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
-    if (nargs != 7) return PyErr_Format(PyExc_TypeError, "adamw_table takes 7 lists");
+// ks_adamw_options
+struct Options {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    const void *step_ptr, *lr_ptr, *grad_scale;
+};
+using AdamwStep = int (*)(const void *, int64_t, int, int, const Options *, void *);
+
+// A tensor of one element of the given type (kind kNone: int64) on the device, or false with an error set.
+bool scalar_of(PyObject *o, const char *name, int kind, int device, const void **out) {
+    Info t;
+    DLTensor d;
+    if (!read(o, &t) || g_api->dltensor_from_py_object_no_sync(o, &d) != 0) return false;
+    const bool type = kind == kNone ? d.dtype.code == kDLInt && d.dtype.bits == 64 && d.dtype.lanes == 1 : t.kind == kind;
+    if (!type || t.device != device || t.numel != 1) {
+        PyErr_Format(PyExc_ValueError, "%s as a tensor must hold one %s on cuda:%d", name,
+                     kind == kNone ? "torch.int64" : kind_name(kind), device);
+        return false;
+    }
+    *out = reinterpret_cast<const void *>((uintptr_t)t.ptr);
+    return true;
+}
+
+// A step's numbers, args: lr, step, grad_scale (each a number or a tensor; grad_scale may be
+// None), beta1, beta2, eps, weight_decay.
+bool options_of(PyObject *const *args, int device, Options *o) {
+    *o = Options{};
+    double *const number[4] = {&o->beta1, &o->beta2, &o->eps, &o->weight_decay};
+    for (int k = 0; k < 4; ++k) {
+        *number[k] = PyFloat_AsDouble(args[3 + k]);
+        if (PyErr_Occurred()) return false;
+    }
+    if (PyObject_TypeCheck(args[0], g_tensor)) {
+        if (!scalar_of(args[0], "lr", kF32, device, &o->lr_ptr)) return false;
+    } else {
+        o->lr = PyFloat_AsDouble(args[0]);
+    }
+    if (PyErr_Occurred()) return false;
+    if (PyObject_TypeCheck(args[1], g_tensor)) {
+        if (!scalar_of(args[1], "step", kNone, device, &o->step_ptr)) return false;
+    } else {
+        o->step = PyLong_AsLongLong(args[1]);
+    }
+    if (PyErr_Occurred()) return false;
+    return args[2] == Py_None || scalar_of(args[2], "grad_scale", kF32, device, &o->grad_scale);
+}
+
+// adamw_step(function, params, grads, exp_avgs, exp_avg_sqs, masters, exp_avg_scales, exp_avg_sq_scales,
+//            lr, step, grad_scale, beta1, beta2, eps, weight_decay, dtypes, stream) -> status
+// Checks the tensors and numbers and calls ks_adamw_step (function: its address;
+// dtypes and stream: dtype_of, stream_of).  Lists of equal lengths; masters and scales may be None.
+PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    if (nargs != 17) return PyErr_Format(PyExc_TypeError, "adamw_step takes 17 arguments");
+    const auto function = reinterpret_cast<AdamwStep>(PyLong_AsVoidPtr(args[0]));
+    if (!function) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "no function");
+    PyObject *const *const options = args + 8;
+    ++args;
     PyObject *list[7] = {}, *table = nullptr, *result = nullptr;
+    Options opt;
+    int ks_dtype = 0, status = 0;
     Py_ssize_t count = 0;
     int dtype = kNone, state = kNone, device = -1;
     uint64_t *words = nullptr;
@@ -150,7 +256,22 @@ PyObject *adamw_table(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
             words[8 * k + c] = t.ptr;
         }
     }
-    if (current_stream(device, &stream)) result = Py_BuildValue("OniiiK", table, count, dtype, state, device, stream);
+    if (count == 0) {
+        result = PyLong_FromLong(0);
+        goto done;
+    }
+    if ((state == kE4M3) != (list[5] != nullptr) || (list[5] != nullptr) != (list[6] != nullptr)) {
+        PyErr_SetString(PyExc_ValueError,
+                        "8-bit states need exp_avg_scales and exp_avg_sq_scales, 32-bit states take none");
+        goto done;
+    }
+    if (!options_of(options, device, &opt) || !dtype_of(options[7], dtype, &ks_dtype) ||
+        !stream_of(options[8], device, &stream))
+        goto done;
+    Py_BEGIN_ALLOW_THREADS
+    status = function(words, count, ks_dtype, state == kE4M3 ? 8 : 32, &opt, reinterpret_cast<void *>((uintptr_t)stream));
+    Py_END_ALLOW_THREADS
+    result = PyLong_FromLong(status);
 done:
     Py_XDECREF(table);
     for (PyObject *l : list) Py_XDECREF(l);
@@ -198,38 +319,11 @@ bool check_adapters(PyObject *const *args, long long width, long long in_f, long
     return false;
 }
 
-// The integers of args[0 .. n); false with an error set.
-bool integers(PyObject *const *args, int n, long long *out) {
-    for (int k = 0; k < n; ++k) {
-        out[k] = PyLong_AsLongLong(args[k]);
-        if (out[k] == -1 && PyErr_Occurred()) return false;
-    }
-    return true;
-}
-
-// adapter_args(x, values, A, B, ids, scales, bias, width, in_f, out_f, nvals, name)
-//   -> (rows, adapters, rank, dtype kind, device, its current stream, x, values, A, B, ids, scales, bias)
-// The addresses of tensors that are None are 0.
-PyObject *adapter_args(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
-    if (nargs != 12) return PyErr_Format(PyExc_TypeError, "adapter_args takes 12 arguments");
-    long long size[4];
-    Info t[7];
-    const char *name = PyUnicode_AsUTF8(args[11]);
-    if (!name || !integers(args + 7, 4, size) || !check_adapters(args, size[0], size[1], size[2], size[3], name, t))
-        return nullptr;
-    unsigned long long stream = 0;
-    if (!current_stream(t[0].device, &stream)) return nullptr;
-    return Py_BuildValue("LLLiiKKKKKKKK", (long long)t[0].shape[0], (long long)t[2].shape[0], (long long)t[2].shape[1],
-                         t[0].kind, t[0].device, stream, (unsigned long long)t[0].ptr, (unsigned long long)t[1].ptr,
-                         (unsigned long long)t[2].ptr, (unsigned long long)t[3].ptr, (unsigned long long)t[4].ptr,
-                         (unsigned long long)t[5].ptr, (unsigned long long)t[6].ptr);
-}
-
 // adapter_matmul(function, x, values, A, B, ids, scales, bias, out, a, b, c, d, activation, dtypes, stream)
 //   -> (status, out)
 // Checks the tensors, makes out (None: a new tensor) and calls ks_adapter_matmul
-// (function: its address).  dtypes: (ks_dtype of float32 tensors, of bfloat16 ones or
-// -1); stream: None for the current one.  Through ctypes the call alone takes 2 us more.
+// (function: its address; dtypes and stream: dtype_of, stream_of).  Through ctypes the
+// call alone takes 2 us more.
 using AdapterMatmul = int (*)(const void *, const void *, int64_t, int64_t, int64_t, int64_t, int64_t, void *, int,
                               const void *, int, const void *, const void *, const float *, const int32_t *, int64_t,
                               int64_t, void *);
@@ -238,64 +332,97 @@ PyObject *adapter_matmul(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     const auto function = reinterpret_cast<AdapterMatmul>(PyLong_AsVoidPtr(args[0]));
     if (!function) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "no function");
     long long n[5];  // a, b, c, d, activation
-    int dtypes[2];
-    if (!integers(args + 9, 5, n) || !PyArg_ParseTuple(args[14], "ii", &dtypes[0], &dtypes[1])) return nullptr;
-    long long in_f, out_f, nvals;
-    if (__builtin_mul_overflow(n[0], n[3], &out_f) || __builtin_mul_overflow(out_f, n[2], &in_f) ||
-        __builtin_mul_overflow(out_f, n[1], &out_f) || __builtin_mul_overflow(in_f, n[1], &nvals))
-        return PyErr_Format(PyExc_ValueError, "the pattern's sizes overflow");
-    Info t[7];
-    if (!check_adapters(args + 1, in_f, in_f, out_f, nvals, "x", t)) return nullptr;
-    const Info &x = t[0];
-    const int dtype = dtypes[x.kind == kBF16];
-    if (dtype < 0) return PyErr_Format(PyExc_ValueError, "tf32 applies to fp32 tensors only");
+    Sizes z;
+    Info t[7], y;
+    int dtype = 0;
     unsigned long long stream = 0;
-    if (args[15] == Py_None) {
-        if (!current_stream(x.device, &stream)) return nullptr;
+    if (!integers(args + 9, 5, n) || !sizes_of(n, &z) ||
+        !check_adapters(args + 1, z.in_f, z.in_f, z.out_f, z.nvals, "x", t) || !dtype_of(args[14], t[0].kind, &dtype) ||
+        !stream_of(args[15], t[0].device, &stream))
+        return nullptr;
+    const Info &x = t[0];
+    const int64_t shape[2] = {x.shape[0], z.out_f};
+    PyObject *out = args[8];
+    if (out == Py_None) {
+        out = new_empty(args[1], shape, 2, &y);
+        if (!out) return nullptr;
     } else {
-        stream = PyLong_AsUnsignedLongLong(args[15]);
-        if (PyErr_Occurred()) return nullptr;
-    }
-    PyObject *out = nullptr;
-    if (args[8] == Py_None) {
-        PyObject *shape = Py_BuildValue("((LL))", (long long)x.shape[0], out_f);
-        PyObject *make = shape ? PyObject_GetAttrString(args[1], "new_empty") : nullptr;
-        if (make) out = PyObject_CallObject(make, shape);
-        Py_XDECREF(make);
-        Py_XDECREF(shape);
-    } else {
-        out = args[8];
+        if (!read(out, &y)) return nullptr;
+        if (y.kind != x.kind || y.device != x.device || !y.contiguous || y.ndim != 2 || y.shape[0] != shape[0] ||
+            y.shape[1] != shape[1])
+            return PyErr_Format(PyExc_ValueError, "out must be a contiguous (%lld, %lld) tensor with x's dtype and device",
+                                (long long)shape[0], (long long)shape[1]);
         Py_INCREF(out);
     }
-    if (!out) return nullptr;
-    Info y;
-    if (!read(out, &y)) {
-        Py_DECREF(out);
-        return nullptr;
-    }
-    if (y.kind != x.kind || y.device != x.device || !y.contiguous || y.ndim != 2 || y.shape[0] != x.shape[0] ||
-        y.shape[1] != out_f) {
-        Py_DECREF(out);
-        return PyErr_Format(PyExc_ValueError, "out must be a contiguous (%lld, %lld) tensor with x's dtype and device",
-                            (long long)x.shape[0], out_f);
-    }
-    const auto ptr = [](const Info &o) { return reinterpret_cast<void *>((uintptr_t)o.ptr); };
     int status = 0;
     Py_BEGIN_ALLOW_THREADS
-    status = function(ptr(x), ptr(t[1]), n[0], n[1], n[2], n[3], x.shape[0], ptr(y), dtype, ptr(t[6]), (int)n[4],
-                      ptr(t[2]), ptr(t[3]), static_cast<const float *>(ptr(t[5])), static_cast<const int32_t *>(ptr(t[4])),
-                      t[2].shape[0], t[2].shape[1], reinterpret_cast<void *>((uintptr_t)stream));
+    status = function(address(x), address(t[1]), n[0], n[1], n[2], n[3], x.shape[0], address(y), dtype, address(t[6]),
+                      (int)n[4], address(t[2]), address(t[3]), static_cast<const float *>(address(t[5])),
+                      static_cast<const int32_t *>(address(t[4])), t[2].shape[0], t[2].shape[1],
+                      reinterpret_cast<void *>((uintptr_t)stream));
     Py_END_ALLOW_THREADS
     return Py_BuildValue("iN", status, out);
 }
 
+// adapter_backward(function, dy, values, A, B, ids, scales, x, a, b, c, d, need_dx, need_da, need_db, dtypes, stream)
+//   -> (status, dx, da, db)
+// The same for ks_adapter_backward; gradients that are not needed are None.
+using AdapterBackward = int (*)(const void *, const void *, const void *, int64_t, int64_t, int64_t, int64_t, int64_t,
+                                int, const void *, const void *, const float *, const int32_t *, int64_t, int64_t,
+                                void *, void *, void *, void *);
+PyObject *adapter_backward(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    if (nargs != 17) return PyErr_Format(PyExc_TypeError, "adapter_backward takes 17 arguments");
+    const auto function = reinterpret_cast<AdapterBackward>(PyLong_AsVoidPtr(args[0]));
+    if (!function) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "no function");
+    long long n[4];
+    Sizes z;
+    Info t[7], x{}, g[3] = {};
+    int dtype = 0, need[3];
+    unsigned long long stream = 0;
+    for (int k = 0; k < 3; ++k)
+        if ((need[k] = PyObject_IsTrue(args[12 + k])) < 0) return nullptr;
+    PyObject *const in[7] = {args[1], args[2], args[3], args[4], args[5], args[6], Py_None};
+    if (!integers(args + 8, 4, n) || !sizes_of(n, &z) ||
+        !check_adapters(in, z.out_f, z.in_f, z.out_f, z.nvals, "dy", t) || !dtype_of(args[15], t[0].kind, &dtype) ||
+        !stream_of(args[16], t[0].device, &stream))
+        return nullptr;
+    const Info &dy = t[0];
+    if (need[0] && args[2] == Py_None) return PyErr_Format(PyExc_ValueError, "dX needs the values");
+    if (need[1] || need[2]) {
+        if (args[7] != Py_None && !read(args[7], &x)) return nullptr;
+        if (args[7] == Py_None || x.ndim != 2 || x.shape[0] != dy.shape[0] || x.shape[1] != z.in_f ||
+            x.kind != dy.kind || x.device != dy.device || !x.contiguous)
+            return PyErr_Format(PyExc_ValueError, "x must be a contiguous (%lld, %lld) tensor with dy's dtype and device",
+                                (long long)dy.shape[0], z.in_f);
+    }
+    const int64_t shape[3][3] = {{dy.shape[0], z.in_f, 0},
+                                 {t[2].shape[0], t[2].shape[1], t[2].shape[2]},
+                                 {t[3].shape[0], t[3].shape[1], t[3].shape[2]}};
+    PyObject *grad[3] = {};
+    for (int k = 0; k < 3; ++k) {
+        grad[k] = need[k] ? new_empty(args[1], shape[k], k ? 3 : 2, &g[k]) : Py_NewRef(Py_None);
+        if (!grad[k]) {
+            for (int j = 0; j < k; ++j) Py_DECREF(grad[j]);
+            return nullptr;
+        }
+    }
+    int status = 0;
+    Py_BEGIN_ALLOW_THREADS
+    status = function(address(dy), address(x), address(t[1]), n[0], n[1], n[2], n[3], dy.shape[0], dtype, address(t[2]),
+                      address(t[3]), static_cast<const float *>(address(t[5])),
+                      static_cast<const int32_t *>(address(t[4])), t[2].shape[0], t[2].shape[1], address(g[0]),
+                      address(g[1]), address(g[2]), reinterpret_cast<void *>((uintptr_t)stream));
+    Py_END_ALLOW_THREADS
+    return Py_BuildValue("iNNN", status, grad[0], grad[1], grad[2]);
+}
+
 PyMethodDef kMethods[] = {
-    {"adapter_args", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adapter_args)), METH_FASTCALL,
-     "Checked arguments of an adapter call."},
     {"adapter_matmul", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adapter_matmul)), METH_FASTCALL,
      "ks_adapter_matmul on torch tensors."},
-    {"adamw_table", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adamw_table)), METH_FASTCALL,
-     "The table of ks_adamw_step from lists of tensors."},
+    {"adapter_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adapter_backward)), METH_FASTCALL,
+     "ks_adapter_backward on torch tensors."},
+    {"adamw_step", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(adamw_step)), METH_FASTCALL,
+     "ks_adamw_step on lists of torch tensors."},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ks_marshal", nullptr, -1, kMethods};

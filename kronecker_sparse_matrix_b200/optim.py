@@ -2,7 +2,6 @@
 optimizer class ``AdamW`` built on it, with states in 32 bits or in 8 bits."""
 from __future__ import annotations
 
-import ctypes
 from itertools import chain
 from typing import Optional, Sequence, Tuple, Union
 
@@ -11,12 +10,6 @@ import torch
 from . import KS_BF16, KS_F32, _lib
 
 ADAMW_BLOCK = 256  # elements that share a scale in an 8-bit state
-
-
-def _scalar(name: str, t: torch.Tensor, dtype: torch.dtype, device: int) -> int:
-    if t.dtype != dtype or t.get_device() != device or t.numel() != 1:
-        raise ValueError(f"{name} as a tensor must hold one {dtype} on cuda:{device}")
-    return t.data_ptr()
 
 
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor],
@@ -38,33 +31,16 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     runs: a captured step follows them.  Asynchronous on ``stream``."""
     if len(params) == 0:
         return
-    if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
-        raise ValueError("exp_avg_scales and exp_avg_sq_scales come together")
-    from ._ks_marshal import adamw_table  # built with the library
-    table, count, dtype, state, dev, st = adamw_table(params, grads, exp_avgs, exp_avg_sqs, masters,
-                                                      exp_avg_scales, exp_avg_sq_scales)
-    bits = 8 if state == 2 else 32  # kinds: 0 float32, 1 bfloat16, 2 float8_e4m3fn
-    if (bits == 8) != (exp_avg_scales is not None):
-        raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales, 32-bit states take none")
-    opt = _lib.KsAdamwOptions(0.0, betas[0], betas[1], eps, weight_decay, 1)
-    if isinstance(lr, torch.Tensor):
-        opt.lr_ptr = _scalar("lr", lr, torch.float32, dev)
-    else:
-        opt.lr = lr
-    if isinstance(step, torch.Tensor):
-        opt.step_ptr = _scalar("step", step, torch.int64, dev)
-    else:
-        opt.step = step
-    if grad_scale is not None:
-        opt.grad_scale = _scalar("grad_scale", grad_scale, torch.float32, dev)
-    step_fn = _lib.load().ks_adamw_step
-    args = (table, count, KS_BF16 if dtype == 1 else KS_F32, bits, ctypes.byref(opt),
-            st if stream is None else stream.cuda_stream)
-    if torch.cuda.current_device() == dev:
-        status = step_fn(*args)
+    from ._ks_marshal import adamw_step as run  # built with the library
+    args = (_lib.address("ks_adamw_step"), params, grads, exp_avgs, exp_avg_sqs, masters, exp_avg_scales,
+            exp_avg_sq_scales, lr, step, grad_scale, betas[0], betas[1], eps, weight_decay, (KS_F32, KS_BF16),
+            None if stream is None else stream.cuda_stream)
+    dev = params[0].get_device() if isinstance(params[0], torch.Tensor) else -1
+    if dev < 0 or dev == torch.cuda.current_device():
+        status = run(*args)
     else:
         with torch.cuda.device(dev):
-            status = step_fn(*args)
+            status = run(*args)
     if status:
         _lib.check(status)
 
