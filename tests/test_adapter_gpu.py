@@ -561,3 +561,29 @@ def test_capture_is_refused_while_an_eager_graph_of_the_leaves_lives():
     _, da, _ = ks.adapter_backward(dys[0], xs[0], layer.values.detach(), layer.pattern, layer.A.detach(),
                                    layer.B.detach(), ids, layer.scales)
     assert torch.equal(layer.A.grad, da)
+
+
+@pytest.mark.parametrize("p,r", [((1, 96, 80, 1), 17), ((1, 96, 80, 1), 40), ((1, 96, 80, 1), 100), ((2, 32, 48, 4), 64)])
+@pytest.mark.parametrize("kind", ["rows", "segments", "one", "none"])
+def test_many_rows_of_many_ranks(p, r, kind):
+    """More rows than the small tiles of H take at once, in features and rows that no tile divides."""
+    q = make(p, 9601, 1 if kind == "one" else 5, r, torch.bfloat16, kind, r, bias=True)
+    assert_forward(call(q, p, act="gelu_tanh"), q, p, "gelu_tanh")
+    assert_backward(q, p, ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"]))
+
+
+def test_a_broken_adapter_among_many_rows_of_many_ranks():
+    p = (1, 96, 80, 1)
+    q = make(p, 9601, 5, 40, torch.bfloat16, "rows", 2)
+    clean = call(q, p)
+    other = q["ids"] != 1
+    q["A"][1, 7] = float("inf")
+    q["x"][~other] = float("nan")
+    y = call(q, p)
+    assert torch.equal(y[other], clean[other]) and torch.isnan(y[~other]).any()
+    q["ids"][4000] = 5  # one past the last
+    y = ks.adapter_matmul(q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"])
+    with pytest.raises(ks.KsError, match="adapter id"):
+        ks.sync_status()
+    other[4000] = False
+    assert torch.equal(y[other], clean[other])
