@@ -45,44 +45,72 @@ namespace {
 // its rounding, 2^-9 of each term of the low-rank sum on average, stays below
 // the rounding of a bf16 result.
 
-// Any size, type and alignment: one warp per row.
-template <typename T, typename O>
-__global__ void __launch_bounds__(256) shrink_any_kernel(const __grid_constant__ ShrinkArgs p) {
-    const ShrinkJob &job = p.job[blockIdx.z];
-    const T *const X = static_cast<const T *>(job.X), *const W = static_cast<const T *>(job.W);
-    const float *const scales = p.scales;
-    const int F = job.F, R = p.R, ldh = p.ldh;
-    const int lane = threadIdx.x & 31;
-    const long long n = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (n >= p.N) return;
-    const int s = row_adapter(p.ids, n, p.N, p.S, p.status);
-    O *h = static_cast<O *>(job.H) + n * ldh;
-    if (s < 0) {
-        for (int r = lane; r < ldh; r += 32) put(h + r, 0.f);
-        return;
-    }
-    const T *x = X + n * F, *w = W + (long long)s * R * F;
-    const float sc = scales ? scales[s] : 1.f;
-    for (int r0 = 0; r0 < ldh; r0 += 8) {
-        float acc[8] = {};
-        for (int f = lane; f < F; f += 32) {
-            const float xv = to_f(x[f]);
+// The smallest id above `last` among the warp's (INT_MAX: none left).
+__device__ __forceinline__ int next_id(int id, int last) {
+    return (int)__reduce_min_sync(0xFFFFFFFFu, (unsigned)(id > last ? id : INT_MAX));
+}
+
+// Sums over the lanes of 64 values of a lane: a lane keeps the half of its values that
+// its bit picks, so 62 exchanges leave sums 2 lane and 2 lane + 1 in v[0] and v[1].
+__device__ __forceinline__ void sum_lanes(float (&v)[64], int lane) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (r0 + e < R) acc[e] = fmaf(xv, to_f(w[(long long)(r0 + e) * F + f]), acc[e]);
-        }
+    for (int half = 32; half >= 2; half >>= 1) {
+        const int bit = half >> 1;  // lane bits 16, 8, 4, 2, 1
+        const bool up = lane & bit;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-#pragma unroll
-            for (int o = 16; o; o >>= 1) acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], o);
-            if (lane == e && r0 + e < ldh) put(h + r0 + e, r0 + e < R ? sc * acc[e] : 0.f);
+        for (int q = 0; q < half; ++q) {
+            const float send = up ? v[q] : v[q + half], keep = up ? v[q + half] : v[q];
+            v[q] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, bit);
         }
     }
 }
 
-// The smallest id above `last` among the warp's (INT_MAX: none left).
-__device__ __forceinline__ int next_id(int id, int last) {
-    return (int)__reduce_min_sync(0xFFFFFFFFu, (unsigned)(id > last ? id : INT_MAX));
+// Any size, type and alignment: a warp takes eight rows and eight ranks, its lanes the
+// features, and loads the rows of one adapter in each pass.  12057 x 588 bf16, rank 64:
+// 98 us, where a warp for each row, reading all of W[s] for it, took 270.
+template <typename T, typename O>
+__global__ void __launch_bounds__(128) shrink_any_kernel(const __grid_constant__ ShrinkArgs p) {
+    const ShrinkJob &job = p.job[blockIdx.z];
+    const T *const X = static_cast<const T *>(job.X), *const W = static_cast<const T *>(job.W);
+    O *const H = static_cast<O *>(job.H);
+    const int F = job.F, R = p.R, ldh = p.ldh, r0 = blockIdx.y * 8;
+    const int lane = threadIdx.x & 31;
+    const long long n0 = ((long long)blockIdx.x * 4 + (threadIdx.x >> 5)) * 8;
+    if (n0 >= p.N) return;
+    const int id = lane < 8 ? row_adapter(p.ids, n0 + lane, p.N, p.S, p.status) : -1;
+    const int row = lane >> 2, r = r0 + 2 * (lane & 3);  // whose sums end in this lane (ranks r and r + 1)
+    const long long n = n0 + row;
+    const int row_id = __shfl_sync(0xFFFFFFFFu, id, row);
+    if (row_id < 0 && n < p.N) {
+        if (r < ldh) put(H + n * ldh + r, 0.f);
+        if (r + 1 < ldh) put(H + n * ldh + r + 1, 0.f);
+    }
+    for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
+        const unsigned take = __ballot_sync(0xFFFFFFFFu, id == s);
+        const T *w = W + ((long long)s * R + r0) * F, *x = X + n0 * F;
+        const int ranks = min(8, R - r0);  // (none of a padded octet)
+        float acc[64];
+#pragma unroll
+        for (int q = 0; q < 64; ++q) acc[q] = 0.f;
+#pragma unroll 2
+        for (int f = lane; f < F; f += 32) {
+            float xv[8], wv[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) xv[m] = take >> m & 1 ? to_f(x[(long long)m * F + f]) : 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wv[e] = e < ranks ? to_f(w[(long long)e * F + f]) : 0.f;
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[m * 8 + e] = fmaf(xv[m], wv[e], acc[m * 8 + e]);
+        }
+        sum_lanes(acc, lane);
+        const float sc = p.scales ? p.scales[s] : 1.f;
+        if (row_id == s) {
+            if (r < ldh) put(H + n * ldh + r, r < R ? sc * acc[0] : 0.f);
+            if (r + 1 < ldh) put(H + n * ldh + r + 1, r + 1 < R ? sc * acc[1] : 0.f);
+        }
+    }
 }
 
 // The adapters among each 128 rows and their rows, for the products that take them
@@ -119,17 +147,18 @@ __device__ void tile_list(const int *__restrict__ ids, int *__restrict__ lists, 
 }
 
 // fp32, F a multiple of 4 and 16-byte aligned: a warp takes eight rows and eight
-// ranks at a time, its lanes the features (four each), and adds the lanes up at
-// the end: 62 shuffles for the 64 sums, each exchange halving what a lane holds.
-// An adapter's pass runs over all eight rows and keeps those that take it.  X runs
+// ranks, its lanes the features (four each), and adds the lanes up at the end.  An
+// adapter's pass runs over all eight rows and keeps those that take it.  X runs
 // two steps ahead in shared memory (cp.async; a lane copies what it reads itself, so
 // nothing is synchronised): at 160 registers the loads of 12 warps an SM alone did
-// not cover X's latency.  25216 x 384, rank 8: 14 us; with 25216 x 1536 beside it 37 us,
-// 5.2 TB/s.
+// not cover X's latency.  25216 x 384, rank 8: 15 us; with 25216 x 1536 beside it 40 us,
+// 4.8 TB/s.  SPLIT warps share eight rows where there are few: their features are
+// dealt in turn and their sums meet in shared memory.
 // Blocks past the rows' build the lists of the product that follows.
+template <int SPLIT>
 __global__ void __launch_bounds__(128)
     shrink_fp32_kernel(const __grid_constant__ ShrinkArgs p, int row_blocks, int *__restrict__ lists, int list_stride) {
-    constexpr int STAGES = 3;
+    constexpr int STAGES = 3, STEP = 128 * SPLIT;
     __shared__ float4 xs[4][STAGES][8][32];
     const ShrinkJob &job = p.job[blockIdx.z];
     const float *__restrict__ const X = static_cast<const float *>(job.X);
@@ -137,36 +166,36 @@ __global__ void __launch_bounds__(128)
     float *__restrict__ const H = static_cast<float *>(job.H);
     const float *const scales = p.scales;
     const long long N = p.N;
-    const int F = job.F, R = p.R, ldh = p.ldh;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int F = job.F, R = p.R, ldh = p.ldh, r0 = blockIdx.y * 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % SPLIT;
     if ((int)blockIdx.x >= row_blocks) {
         const long long tile = (long long)(blockIdx.x - row_blocks) * 4 + warp;
-        if (blockIdx.z == 0 && tile * 128 < N) tile_list(p.ids, lists, list_stride, N, p.S, tile, lane);
+        if (blockIdx.y == 0 && blockIdx.z == 0 && tile * 128 < N)
+            tile_list(p.ids, lists, list_stride, N, p.S, tile, lane);
         return;
     }
-    const long long n0 = ((long long)blockIdx.x * 4 + warp) * 8;
+    const long long n0 = ((long long)blockIdx.x * (4 / SPLIT) + warp / SPLIT) * 8;
     if (n0 >= N) return;
     const int id = lane < 8 ? row_adapter(p.ids, n0 + lane, N, p.S, p.status) : -1;
-    const int row = lane >> 2;  // the row and ranks (2 q, 2 q + 1) whose sums end in this lane
+    const int row = lane >> 2, r = r0 + 2 * (lane & 3);  // whose sums end in this lane (ranks r and r + 1)
     const long long n = n0 + row;
     const int row_id = __shfl_sync(0xFFFFFFFFu, id, row);
-    if (row_id < 0 && n < N)
-        for (int r = 2 * (lane & 3); r < ldh; r += 8) {
-            H[n * ldh + r] = 0.f;
-            if (r + 1 < ldh) H[n * ldh + r + 1] = 0.f;
-        }
+    if (row_id < 0 && n < N && part == 0) {
+        if (r < ldh) H[n * ldh + r] = 0.f;
+        if (r + 1 < ldh) H[n * ldh + r + 1] = 0.f;
+    }
     int found = 0;
     for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) ++found;
     if (found > 2) {  // each pass computes all eight rows: more than two cost more than row by row
-        for (int m = 0; m < 8; ++m) {
+        for (int m = part; m < 8; m += SPLIT) {
             const int s = __shfl_sync(0xFFFFFFFFu, id, m);
             if (s < 0) continue;
-            for (int r = 0; r < ldh; r += 4) {
+            for (int q = r0; q < r0 + 8; q += 4) {
                 float h[4] = {0.f, 0.f, 0.f, 0.f};
-                if (r < R) dot4(X + (n0 + m) * F, W + ((long long)s * R + r) * F, F, R - r, lane, h);
+                if (q < R) dot4(X + (n0 + m) * F, W + ((long long)s * R + q) * F, F, R - q, lane, h);
                 const float v = lane == 0 ? h[0] : lane == 1 ? h[1] : lane == 2 ? h[2] : h[3];
-                if (lane < 4 && r + lane < ldh)
-                    H[(n0 + m) * ldh + r + lane] = r + lane < R ? (scales ? scales[s] : 1.f) * v : 0.f;
+                if (lane < 4 && q + lane < ldh)
+                    H[(n0 + m) * ldh + q + lane] = q + lane < R ? (scales ? scales[s] : 1.f) * v : 0.f;
             }
         }
         return;
@@ -185,55 +214,52 @@ __global__ void __launch_bounds__(128)
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
-        const bool mine = row_id == s;
         const float sc = scales ? scales[s] : 1.f;
-        for (int r0 = 0; r0 < ldh; r0 += 8) {
-            const float *w = W + ((long long)s * R + r0) * F;
-            float acc[64];
+        const float *w = W + ((long long)s * R + (r0 < R ? r0 : 0)) * F;
+        float acc[64];
 #pragma unroll
-            for (int q = 0; q < 64; ++q) acc[q] = 0.f;
-            issue(lane * 4, 0);
-            issue(lane * 4 + 128, 1);
-            int stage = 0;
-            for (int f = lane * 4; f - lane * 4 < F; f += 128) {
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-                float4 x[8];
+        for (int q = 0; q < 64; ++q) acc[q] = 0.f;
+        const int f0 = part * 128 + lane * 4;
+        issue(f0, 0);
+        issue(f0 + STEP, 1);
+        int stage = 0;
+        for (int f = f0; f - lane * 4 < F; f += STEP) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            float4 x[8];
 #pragma unroll
-                for (int m = 0; m < 8; ++m) x[m] = xs[warp][stage][m][lane];
-                issue(f + 256, stage == 0 ? 2 : stage - 1);
-                stage = stage == 2 ? 0 : stage + 1;
-                if (f >= F) continue;
+            for (int m = 0; m < 8; ++m) x[m] = xs[warp][stage][m][lane];
+            issue(f + 2 * STEP, stage == 0 ? 2 : stage - 1);
+            stage = stage == 2 ? 0 : stage + 1;
+            if (f >= F) continue;
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int rr = r0 + r < R ? r : 0;
-                    const float4 v = __ldg(reinterpret_cast<const float4 *>(w + (long long)rr * F + f));
+            for (int e = 0; e < 8; ++e) {
+                const int rr = r0 + e < R ? e : 0;
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(w + (long long)rr * F + f));
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        float a = acc[m * 8 + r];
-                        a = fmaf(x[m].x, v.x, a);
-                        a = fmaf(x[m].y, v.y, a);
-                        a = fmaf(x[m].z, v.z, a);
-                        acc[m * 8 + r] = fmaf(x[m].w, v.w, a);
-                    }
+                for (int m = 0; m < 8; ++m) {
+                    float a = acc[m * 8 + e];
+                    a = fmaf(x[m].x, v.x, a);
+                    a = fmaf(x[m].y, v.y, a);
+                    a = fmaf(x[m].z, v.z, a);
+                    acc[m * 8 + e] = fmaf(x[m].w, v.w, a);
                 }
             }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            // sums over the lanes: a lane keeps the half of its values that its bit picks
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        sum_lanes(acc, lane);
+        if constexpr (SPLIT > 1) {
+            // (the warp's stages are free by now)
+            if (part) xs[warp][0][0][lane] = make_float4(acc[0], acc[1], 0.f, 0.f);
+            __syncthreads();
+            if (!part) {
 #pragma unroll
-            for (int half = 32; half >= 2; half >>= 1) {
-                const int bit = half >> 1;  // lane bits 16, 8, 4, 2, 1
-                const bool up = lane & bit;
-#pragma unroll
-                for (int q = 0; q < half; ++q) {
-                    const float send = up ? acc[q] : acc[q + half], keep = up ? acc[q + half] : acc[q];
-                    acc[q] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, bit);
-                }
+                for (int q = 1; q < SPLIT; ++q) acc[0] += xs[warp + q][0][0][lane].x, acc[1] += xs[warp + q][0][0][lane].y;
             }
-            if (mine) {  // values 2 lane, 2 lane + 1: row lane / 4, ranks 2 (lane % 4) ..
-                const int r = r0 + 2 * (lane & 3);
-                if (r < ldh) H[n * ldh + r] = r < R ? sc * acc[0] : 0.f;
-                if (r + 1 < ldh) H[n * ldh + r + 1] = r + 1 < R ? sc * acc[1] : 0.f;
-            }
+            __syncthreads();
+        }
+        if (row_id == s && part == 0) {
+            if (r < ldh) H[n * ldh + r] = r < R ? sc * acc[0] : 0.f;
+            if (r + 1 < ldh) H[n * ldh + r + 1] = r + 1 < R ? sc * acc[1] : 0.f;
         }
     }
 }
@@ -420,28 +446,6 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- Y = act(Y + bias + H W)
 
-// Any size and alignment: one thread per output.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    expand_any_kernel(T *__restrict__ Y, const T *__restrict__ W, const int *__restrict__ ids,
-                      const float *__restrict__ H, long long N, int F, int R, int ldh, int S, int rs, int fs,
-                      const T *__restrict__ bias, int act) {
-    const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long n = at / F;
-    if (n >= N) return;
-    const int f = (int)(at - n * F);
-    const int s = ids ? ids[n] : 0;
-    float y = to_f(Y[at]);
-    if (s >= 0 && s < S) {
-        const T *w = W + (long long)s * R * F + (long long)f * fs;
-        const float *h = H + n * ldh;
-        float acc = 0.f;
-        for (int r = 0; r < R; ++r) acc = fmaf(h[r], to_f(w[(long long)r * rs]), acc);
-        y += acc;
-    }
-    put(Y + at, ep_apply(y, bias, f, act));
-}
-
 constexpr int kExpandRows = 8;
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
@@ -551,6 +555,73 @@ __global__ void __launch_bounds__(128, 6)
             store4(y + (long long)m * F, v);
         }
     }
+}
+
+// The same for any size and alignment: a thread's four outputs are as far apart as the
+// block is wide.  RV: the ranks come in whole aligned fours (3535 x 570 fp32, rank 64: 34 us,
+// where a thread for each output took 346).
+template <typename T, bool RC, bool RV>
+__global__ void __launch_bounds__(128)
+    expand_any_kernel(T *__restrict__ Y, const T *__restrict__ W, const int *__restrict__ ids,
+                      const float *__restrict__ H, long long N, int F, int R, int ldh, int S,
+                      const T *__restrict__ bias, int act) {
+    constexpr int ROWS = kExpandRows;
+    extern __shared__ float4 hs[];  // [rank / 4][row]
+    const int threads = blockDim.x;
+    const unsigned col_blocks = (unsigned)((F + 4LL * threads - 1) / (4 * threads));
+    const long long n0 = (long long)(blockIdx.x / col_blocks) * ROWS, f0 = (long long)(blockIdx.x % col_blocks) * (4 * threads);
+    const int rows = (int)min((long long)ROWS, N - n0), lane = threadIdx.x & 31;
+    int id = lane < rows ? (ids ? ids[n0 + lane] : 0) : -1;
+    if (id >= S) id = -1;
+    const int rq = ldh / 4;
+    for (int q = threadIdx.x; q < rows * rq; q += threads)
+        hs[(q % rq) * ROWS + q / rq] = *reinterpret_cast<const float4 *>(H + n0 * ldh + (long long)q * 4);
+    __syncthreads();
+    int f[4];
+    bool in[4];
+    float acc[ROWS][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const long long at = f0 + c * threads + threadIdx.x;
+        in[c] = at < F;
+        f[c] = in[c] ? (int)at : 0;
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) acc[m][c] = in[c] && m < rows ? to_f(Y[(n0 + m) * F + f[c]]) : 0.f;
+    }
+    for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
+        const unsigned take = __ballot_sync(0xFFFFFFFFu, id == s);
+        const T *w = W + (long long)s * R * F;
+        for (int r = 0; r < R; r += 4) {
+            float v[4][4];  // ranks r .. r + 3 of output f[c]
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (RV) {
+                    const float4 u = load4(w + (long long)f[c] * R + r);
+                    v[c][0] = u.x, v[c][1] = u.y, v[c][2] = u.z, v[c][3] = u.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[c][e] = r + e < R ? to_f(RC ? w[(long long)f[c] * R + r + e] : w[(long long)(r + e) * F + f[c]])
+                                            : 0.f;
+                }
+            }
+            const float4 *h = hs + (r >> 2) * ROWS;
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m)
+                if (take >> m & 1) {
+                    const float4 x = h[m];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[m][c] = fmaf(x.w, v[c][3],
+                                         fmaf(x.z, v[c][2], fmaf(x.y, v[c][1], fmaf(x.x, v[c][0], acc[m][c]))));
+                }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m)
+            if (in[c] && m < rows) put(Y + (n0 + m) * F + f[c], ep_apply(acc[m][c], bias, f[c], act));
 }
 
 // ---------------------------------------------------------------- dA and dB
@@ -1023,9 +1094,9 @@ bool by_rows(const Adapters &q, long long N, int F) {
 // H = scale X W^T of one or two jobs.  h_bf16: their H are bf16; lists: null, or the
 // lists of the product that takes the adapters as stages, to be built (a tensor-core
 // product's planes are job[0]'s; the caller has made sure of vectors); its bias to
-// be packed; few: row by row (by_rows).
+// be packed; few: row by row (by_rows); widest: F of the widest job that the call can have.
 cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf16, long long N, int ldh, int *lists,
-                   bool few, const BiasPack &bias = BiasPack{}) {
+                   bool few, int widest, const BiasPack &bias = BiasPack{}) {
     ShrinkArgs p{};
     bool vec = true;
     for (int j = 0; j < jobs; ++j) {
@@ -1037,24 +1108,32 @@ cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf1
     p.status = device_status_ptr();
     const unsigned z = (unsigned)jobs;
     if (!vec && jobs == 2) {  // each as it can
-        const cudaError_t e = shrink(q, job, 1, h_bf16, N, ldh, lists, few);
-        return e == cudaSuccess ? shrink(q, job + 1, 1, h_bf16, N, ldh, nullptr, few) : e;
+        const cudaError_t e = shrink(q, job, 1, h_bf16, N, ldh, lists, few, widest);
+        return e == cudaSuccess ? shrink(q, job + 1, 1, h_bf16, N, ldh, nullptr, few, widest) : e;
     }
+    if (few) return launch_shrink_rows(p, jobs, q.bf16, vec, q.st);
     if (!vec) {
-        const dim3 grid((unsigned)((N + 7) / 8), 1, z);
+        const dim3 grid((unsigned)((N + 31) / 32), (unsigned)((ldh + 7) / 8), z);
         if (!q.bf16)
-            shrink_any_kernel<float, float><<<grid, 256, 0, q.st>>>(p);
+            shrink_any_kernel<float, float><<<grid, 128, 0, q.st>>>(p);
         else if (h_bf16)
-            shrink_any_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, q.st>>>(p);
+            shrink_any_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 128, 0, q.st>>>(p);
         else
-            shrink_any_kernel<__nv_bfloat16, float><<<grid, 256, 0, q.st>>>(p);
+            shrink_any_kernel<__nv_bfloat16, float><<<grid, 128, 0, q.st>>>(p);
         return cudaGetLastError();
     }
-    if (few) return launch_shrink_rows(p, jobs, q.bf16, h_bf16, q.st);
     if (!q.bf16) {
-        const int row_blocks = (int)((N + 31) / 32), list_blocks = lists ? (int)((list_tiles(N) + 3) / 4) : 0;
-        shrink_fp32_kernel<<<dim3((unsigned)(row_blocks + list_blocks), 1, z), 128, 0, q.st>>>(p, row_blocks, lists,
-                                                                                               list_stride(q.S));
+        const int octets = (ldh + 7) / 8, list_blocks = lists ? (int)((list_tiles(N) + 3) / 4) : 0;
+        // A block's four warps share eight rows where there are few blocks (841 x 12288, rank 3: 114
+        // and 34 us), or where the features are many, W's being read by neighbours then (25216 x 12288,
+        // rank 8: 329 and 248 us; 25216 x 384: 17 and 25).
+        const bool split = (N + 31) / 32 * octets < 4 * sm_count() || widest >= 2048;
+        const int row_blocks = (int)(split ? (N + 7) / 8 : (N + 31) / 32);
+        const dim3 grid((unsigned)(row_blocks + list_blocks), (unsigned)octets, z);
+        if (split)
+            shrink_fp32_kernel<4><<<grid, 128, 0, q.st>>>(p, row_blocks, lists, list_stride(q.S));
+        else
+            shrink_fp32_kernel<1><<<grid, 128, 0, q.st>>>(p, row_blocks, lists, list_stride(q.S));
         return cudaGetLastError();
     }
     const int cols = lists ? std::max(ldh, p.plane_r) : ldh;
@@ -1084,7 +1163,7 @@ cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long 
     const T *w = static_cast<const T *>(W), *b = static_cast<const T *>(bias);
     const size_t smem = (size_t)ldh * kExpandRows * 4;
     if (F % 4 == 0 && aligned(Y, 4 * sizeof(T)) && aligned(W, 4 * sizeof(T)) && aligned(bias, 4 * sizeof(T)) &&
-        (with_a || q.R % 4 == 0) && (F + 511) / 512 <= 65535) {
+        (with_a || q.R % 4 == 0) && (F + 511LL) / 512 <= 65535) {
         const dim3 grid((unsigned)((N + kExpandRows - 1) / kExpandRows), (unsigned)((F + 511) / 512));
         const auto go = [&](auto kernel) {
             kernel<<<grid, 128, smem, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, b);
@@ -1098,11 +1177,16 @@ cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long 
             default: return go(expand_kernel<T, true, KS_ACT_GELU_ERF>);
         }
     }
-    const int rs = with_a ? F : 1, fs = with_a ? 1 : q.R;
-    const long long blocks = (N * F + 255) / 256;
+    const int threads = F >= 512 ? 128 : round_up((F + 3) / 4, 32);
+    const long long blocks = (N + kExpandRows - 1) / kExpandRows * ((F + 4LL * threads - 1) / (4 * threads));
     if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-    expand_any_kernel<T><<<(unsigned)blocks, 256, 0, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, rs, fs, b, act);
-    return cudaGetLastError();
+    const auto go = [&](auto kernel) {
+        kernel<<<(unsigned)blocks, threads, smem, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, b, act);
+        return cudaGetLastError();
+    };
+    if (with_a) return go(expand_any_kernel<T, false, false>);
+    return q.R % 4 == 0 && aligned(W, 4 * sizeof(T)) ? go(expand_any_kernel<T, true, true>)
+                                                     : go(expand_any_kernel<T, true, false>);
 }
 
 // How the gradients (dA, dB; out null: not wanted) are cut: feature blocks of each,
@@ -1325,7 +1409,7 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
     cudaError_t e;
     char *w = nullptr;
     const int row_ldh = round_up(q.R, 4);
-    if (adapter_rows_supported(p, A, row_ldh)) {
+    if (adapter_rows_supported(p, row_ldh)) {
         // few rows: one launch, or two where A[s] is more than a block should read for itself
         const bool apart = (size_t)q.R * in_f * o.elem > 64 * 1024;
         p.bias = bias;
@@ -1336,8 +1420,8 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         }
         if ((s = alloc(&w, (size_t)batch * row_ldh * 4, q.st)) != KS_OK) return s;
         float *H = reinterpret_cast<float *>(w);
-        const ShrinkArgs h{{{X, A, H, nullptr, in_f}}, scales, ids, batch, q.R, row_ldh, q.S, 0, device_status_ptr()};
-        e = launch_shrink_rows(h, 1, q.bf16, false, q.st);
+        const ShrinkJob job{X, A, H, nullptr, in_f};
+        e = shrink(q, &job, 1, false, batch, row_ldh, nullptr, true, in_f);
         if (e == cudaSuccess) e = launch_adapter_rows(p, A, B, scales, ids, q.S, q.R, H, row_ldh);
     } else if (fuses(q, p, A, in_f)) {
         // the adapters as K steps of the tensor-core product, with its bias and activation
@@ -1357,7 +1441,7 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         }
         e = packed ? pack(q, B, w + b_at, out_f, ldh) : cudaSuccess;
         const ShrinkJob job{X, A, nullptr, reinterpret_cast<unsigned short *>(w + h), in_f};
-        if (e == cudaSuccess) e = shrink(q, &job, 1, true, batch, ldh, reinterpret_cast<int *>(w + l), false, pack_b);
+        if (e == cudaSuccess) e = shrink(q, &job, 1, true, batch, ldh, reinterpret_cast<int *>(w + l), false, in_f, pack_b);
         if (e == cudaSuccess) {
             p.act = activation;
             p.ad = &tc;
@@ -1373,7 +1457,7 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         const auto *vt = reinterpret_cast<const float *>(w + v);
         const ShrinkJob job{X, A, w + h, nullptr, in_f};
         e = launch_transpose_blocks(values, w + v, a * d, b, c, dtype, q.st);
-        if (e == cudaSuccess) e = shrink(q, &job, 1, false, batch, ldh, reinterpret_cast<int *>(w + l), false);
+        if (e == cudaSuccess) e = shrink(q, &job, 1, false, batch, ldh, reinterpret_cast<int *>(w + l), false, in_f);
         p.bias = bias;
         p.act = activation;
         const Fma32Adapters ad{reinterpret_cast<const float *>(w + h), static_cast<const float *>(B),
@@ -1387,7 +1471,7 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         float *H = reinterpret_cast<float *>(w);
         s = run(p, KS_VARIANT_AUTO);
         const ShrinkJob job{X, A, H, nullptr, in_f};
-        e = s == KS_OK ? shrink(q, &job, 1, false, batch, ldh, nullptr, by_rows(q, batch, in_f)) : cudaSuccess;
+        e = s == KS_OK ? shrink(q, &job, 1, false, batch, ldh, nullptr, by_rows(q, batch, in_f), in_f) : cudaSuccess;
         if (s == KS_OK && e == cudaSuccess)
             e = q.bf16 ? expand<__nv_bfloat16>(q, Y, B, false, batch, out_f, H, ldh, bias, activation)
                        : expand<float>(q, Y, B, false, batch, out_f, H, ldh, bias, activation);
@@ -1479,7 +1563,8 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
                                   fused ? reinterpret_cast<unsigned short *>(w + p_at) : nullptr, out_f};
     if (dB) job[n_jobs++] = ShrinkJob{X, A, w + h_at, nullptr, in_f};
     if (e == cudaSuccess)
-        e = shrink(q, job, n_jobs, fused, batch, ldh, lists, !fusable && !fusable32 && by_rows(q, batch, std::max(in_f, out_f)));
+        e = shrink(q, job, n_jobs, fused, batch, ldh, lists,
+                   !fusable && !fusable32 && by_rows(q, batch, std::max(in_f, out_f)), std::max(in_f, out_f));
     if (fused32 && e == cudaSuccess) {
         const Fma32Adapters ad{reinterpret_cast<const float *>(w + g_at), reinterpret_cast<const float *>(w + ap), lists,
                                q.R, ldh, ldh, list_stride(q.S)};

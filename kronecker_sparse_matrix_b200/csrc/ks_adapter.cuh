@@ -86,4 +86,23 @@ __device__ __forceinline__ void dot4(const T *x, const T *w, int F, int ranks, i
     }
 }
 
+// The same for any F and alignment.
+template <typename T>
+__device__ __forceinline__ void dot4_any(const T *x, const T *w, int F, int ranks, int lane, float (&out)[4]) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int f = lane; f < F; f += 32) {
+        const float xf = to_f(x[f]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (r < ranks) acc[r] = fmaf(xf, to_f(w[(long long)r * F + f]), acc[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) acc[r] += __shfl_xor_sync(0xFFFFFFFFu, acc[r], o);
+        out[r] = acc[r];
+    }
+}
+
 }  // namespace ks

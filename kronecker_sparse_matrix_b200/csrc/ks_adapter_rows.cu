@@ -30,12 +30,12 @@ constexpr int kThreads = 256;
 constexpr int kMaxSmem = 96 * 1024;
 
 // H[n][r] = scale[s] sum_f X[n][f] W[s][r][f], r < ldh (zeros past R and for rows without an adapter).
-template <typename T, typename O>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) shrink_rows_kernel(const __grid_constant__ ShrinkArgs p) {
     const ShrinkJob &job = p.job[blockIdx.z];
     const T *__restrict__ const X = static_cast<const T *>(job.X);
     const T *__restrict__ const W = static_cast<const T *>(job.W);
-    O *__restrict__ const H = static_cast<O *>(job.H);
+    float *__restrict__ const H = static_cast<float *>(job.H);
     const float *const scales = p.scales;
     const int F = job.F, R = p.R, ldh = p.ldh;
     const int lane = threadIdx.x & 31, quads = (ldh + 3) / 4;
@@ -46,14 +46,18 @@ __global__ void __launch_bounds__(256) shrink_rows_kernel(const __grid_constant_
     const int s = row_adapter(p.ids, n, p.N, p.S, p.status);
     float h[4] = {0.f, 0.f, 0.f, 0.f};
     if (s >= 0 && r0 < R) {
-        dot4(X + n * F, W + ((long long)s * R + r0) * F, F, R - r0, lane, h);
+        const T *x = X + n * F, *w = W + ((long long)s * R + r0) * F;
+        if constexpr (VEC)
+            dot4(x, w, F, R - r0, lane, h);
+        else
+            dot4_any(x, w, F, R - r0, lane, h);
         const float sc = scales ? scales[s] : 1.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) h[r] = r0 + r < R ? h[r] * sc : 0.f;
     }
     if (lane < 4 && r0 + lane < ldh) {
         const float v = lane == 0 ? h[0] : lane == 1 ? h[1] : lane == 2 ? h[2] : h[3];
-        put(H + n * ldh + r0 + lane, v);
+        H[n * ldh + r0 + lane] = v;
     }
 }
 
@@ -68,17 +72,19 @@ struct RowsParams {
     int lanes_log2;    // lanes of a values row: 1 << lanes_log2
     int pitch;         // elements of a row of x in shared memory, [i][l][j]
     int x_rows;        // rows (i, l) of x in shared memory
-    int b_vec;         // B's rows are whole aligned vectors
+    int x_bytes;       // of all rows of x there
+    int a_vec, b_vec;  // rows of x and A, of B are whole aligned vectors
     unsigned *status;
 };
 
-// RB rows of a block; blockIdx.x: columns, blockIdx.y: rows.
-template <typename T, int RB>
+// RB rows of a block; blockIdx.x: columns, blockIdx.y: rows.  VEC: rows of the values are
+// whole aligned vectors.
+template <typename T, int RB, bool VEC>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowsParams p) {
     constexpr int V = kVec<T>;
     extern __shared__ __align__(16) uint8_t smem[];
     T *const xs = reinterpret_cast<T *>(smem);  // [RB][x_rows][pitch]
-    float *const ys = reinterpret_cast<float *>(smem + (size_t)RB * p.x_rows * p.pitch * sizeof(T));  // [RB][cols]
+    float *const ys = reinterpret_cast<float *>(smem + p.x_bytes);  // [RB][cols]
     float *const hs = ys + RB * p.cols;                                                              // [RB][ldh]
     __shared__ int sid[RB];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -94,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
         if (n0 + m >= p.N) break;
         const T *src = X + (n0 + m) * p.in_f + (long long)i0 * cd;
         T *dst = xs + (size_t)m * p.x_rows * p.pitch;
-        if (p.d % V == 0) {
+        if (VEC && p.d % V == 0) {
             for (int e = tid * V; e < ni * cd; e += kThreads * V) {
                 const int i = e / cd, j = (e - i * cd) / p.d, l = (e - i * cd) - j * p.d;
                 const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + e));
@@ -122,7 +128,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
             const int m = q / quads, r0 = (q - m * quads) * 4, s = sid[m];
             if (s < 0) continue;
             float h[4];
-            dot4(X + (n0 + m) * p.in_f, A + ((long long)s * p.R + r0) * p.in_f, p.in_f, p.R - r0, lane, h);
+            const T *x = X + (n0 + m) * p.in_f, *w = A + ((long long)s * p.R + r0) * p.in_f;
+            if (p.a_vec)
+                dot4(x, w, p.in_f, p.R - r0, lane, h);
+            else
+                dot4_any(x, w, p.in_f, p.R - r0, lane, h);
             const float sc = p.scales ? p.scales[s] : 1.f;
             if (lane < 4) {
                 const float v = lane == 0 ? h[0] : lane == 1 ? h[1] : lane == 2 ? h[2] : h[3];
@@ -143,16 +153,26 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
             float acc[RB];
 #pragma unroll
             for (int m = 0; m < RB; ++m) acc[m] = 0.f;
+            if constexpr (VEC) {
 #pragma unroll 2
-            for (int j = sub * V; j < p.c; j += lanes * V) {
-                float vf[V];
-                unpack(__ldg(reinterpret_cast<const uint4 *>(v + j)), vf);
+                for (int j = sub * V; j < p.c; j += lanes * V) {
+                    float vf[V];
+                    unpack(__ldg(reinterpret_cast<const uint4 *>(v + j)), vf);
 #pragma unroll
-                for (int m = 0; m < RB; ++m) {
-                    float xf[V];
-                    unpack(*reinterpret_cast<const uint4 *>(x + (size_t)m * p.x_rows * p.pitch + j), xf);
+                    for (int m = 0; m < RB; ++m) {
+                        float xf[V];
+                        unpack(*reinterpret_cast<const uint4 *>(x + (size_t)m * p.x_rows * p.pitch + j), xf);
 #pragma unroll
-                    for (int q = 0; q < V; ++q) acc[m] = fmaf(vf[q], xf[q], acc[m]);
+                        for (int q = 0; q < V; ++q) acc[m] = fmaf(vf[q], xf[q], acc[m]);
+                    }
+                }
+            } else {
+#pragma unroll 4
+                for (int j = sub; j < p.c; j += lanes) {
+                    const float vf = to_f(v[j]);
+#pragma unroll
+                    for (int m = 0; m < RB; ++m)
+                        acc[m] = fmaf(vf, to_f(x[(size_t)m * p.x_rows * p.pitch + j]), acc[m]);
                 }
             }
 #pragma unroll
@@ -190,14 +210,18 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
 }
 
 struct RowsPlan {
+    bool vec;
     int rb, cols, lanes_log2, pitch, x_rows, tiles;
-    size_t smem;
+    size_t x_bytes, smem;
 };
 
 // Blocks for about two a SM (at least 32 columns each: one values row for each
 // warp's group of lanes), more rows of a block as the batch grows.
 bool rows_plan(const Problem &p, int ldh, RowsPlan *o) {
-    const int es = p.elem_bytes(), vec = 16 / es;
+    const int es = p.elem_bytes();
+    const uintptr_t al = reinterpret_cast<uintptr_t>(p.X) | reinterpret_cast<uintptr_t>(p.V);
+    o->vec = p.c % (16 / es) == 0 && al % 16 == 0;
+    const int vec = o->vec ? 16 / es : 1;
     const int out_f = (int)p.out_features();
     for (o->rb = p.batch >= 16 ? 4 : p.batch >= 4 ? 2 : 1; o->rb >= 1; o->rb /= 2) {
         const long long groups = (p.batch + o->rb - 1) / o->rb;
@@ -207,10 +231,12 @@ bool rows_plan(const Problem &p, int ldh, RowsPlan *o) {
         int lanes = 0;
         while ((vec << lanes) < p.c && lanes < 5) ++lanes;
         o->lanes_log2 = lanes;
-        o->pitch = (int)p.c + vec;  // rows of 16-byte units, an odd number of them for c a power of two
+        // rows of 16-byte units, an odd number of them for c a power of two
+        o->pitch = o->vec ? (int)p.c + vec : (int)p.c | 1;
         const long long i_n = std::min<long long>(p.a, (o->cols - 1) / (p.b * p.d) + 2);
         o->x_rows = (int)std::min<long long>(i_n * p.d, 1 << 20);
-        const double smem = (double)o->rb * o->x_rows * o->pitch * es + (double)o->rb * (o->cols + ldh) * 4;
+        o->x_bytes = (o->rb * (size_t)o->x_rows * o->pitch * es + 15) / 16 * 16;
+        const double smem = (double)o->x_bytes + (double)o->rb * (o->cols + ldh) * 4;
         if (smem <= kMaxSmem) {
             o->smem = (size_t)smem;
             return true;
@@ -221,26 +247,25 @@ bool rows_plan(const Problem &p, int ldh, RowsPlan *o) {
 
 }  // namespace
 
-bool adapter_rows_supported(const Problem &p, const void *A, int ldh) {
-    // about 5 us and 1 us for each 1.9M products (bf16); the tiles take 25 us and more
-    if (p.dtype == KS_TF32 || p.c % (16 / p.elem_bytes()) || p.batch > 256 ||
-        p.batch * p.out_features() * (p.c + ldh) > 1LL << 25)
-        return false;
-    const uintptr_t al = reinterpret_cast<uintptr_t>(p.X) | reinterpret_cast<uintptr_t>(p.V) |
-                         reinterpret_cast<uintptr_t>(A);
+bool adapter_rows_supported(const Problem &p, int ldh) {
+    // about 5 us and 1 us for each 1.9M products (bf16); the tiles take 25 us and more.  Without
+    // vectors 1 us for each 0.2M products, against products of no tiled kernel: with d a
+    // multiple of a vector 280 us and more (108 rows of (2, 56, 87, 8): 30 and 830 us), otherwise
+    // from 20 us on.
+    const long long work = p.batch * p.out_features() * (p.c + ldh);
+    if (p.dtype == KS_TF32 || p.batch > 256 || work > 1LL << 25) return false;
     RowsPlan o;
-    return al % 16 == 0 && rows_plan(p, ldh, &o);
+    return rows_plan(p, ldh, &o) && (o.vec || p.d % (16 / p.elem_bytes()) == 0 || work <= 1LL << 23);
 }
 
-cudaError_t launch_shrink_rows(const ShrinkArgs &p, int jobs, bool bf16, bool h_bf16, cudaStream_t st) {
+cudaError_t launch_shrink_rows(const ShrinkArgs &p, int jobs, bool bf16, bool vec, cudaStream_t st) {
     const dim3 grid((unsigned)((p.N * ((p.ldh + 3) / 4) + 7) / 8), 1, (unsigned)jobs);
-    if (!bf16)
-        shrink_rows_kernel<float, float><<<grid, 256, 0, st>>>(p);
-    else if (h_bf16)
-        shrink_rows_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, st>>>(p);
-    else
-        shrink_rows_kernel<__nv_bfloat16, float><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
+    const auto go = [&](auto kernel) {
+        kernel<<<grid, 256, 0, st>>>(p);
+        return cudaGetLastError();
+    };
+    if (!bf16) return vec ? go(shrink_rows_kernel<float, true>) : go(shrink_rows_kernel<float, false>);
+    return vec ? go(shrink_rows_kernel<__nv_bfloat16, true>) : go(shrink_rows_kernel<__nv_bfloat16, false>);
 }
 
 cudaError_t launch_adapter_rows(const Problem &pr, const void *A, const void *B, const float *scales, const int *ids,
@@ -254,6 +279,9 @@ cudaError_t launch_adapter_rows(const Problem &pr, const void *A, const void *B,
     p.in_f = (int)pr.in_features(), p.out_f = (int)pr.out_features();
     p.R = R, p.ldh = ldh, p.S = S;
     p.cols = o.cols, p.lanes_log2 = o.lanes_log2, p.pitch = o.pitch, p.x_rows = o.x_rows;
+    p.x_bytes = (int)o.x_bytes;
+    p.a_vec = (reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(pr.X)) % 16 == 0 &&
+              p.in_f * pr.elem_bytes() % 16 == 0;
     p.b_vec = reinterpret_cast<uintptr_t>(B) % 16 == 0 && R * pr.elem_bytes() % 16 == 0;
     p.status = device_status_ptr();
     const dim3 grid((unsigned)o.tiles, (unsigned)((pr.batch + o.rb - 1) / o.rb));
@@ -265,11 +293,17 @@ cudaError_t launch_adapter_rows(const Problem &pr, const void *A, const void *B,
         kernel<<<grid, kThreads, o.smem, pr.stream>>>(p);
         return cudaGetLastError();
     };
-    if (pr.dtype == KS_BF16)
-        return o.rb == 4   ? go(rows_kernel<__nv_bfloat16, 4>)
-               : o.rb == 2 ? go(rows_kernel<__nv_bfloat16, 2>)
-                           : go(rows_kernel<__nv_bfloat16, 1>);
-    return o.rb == 4 ? go(rows_kernel<float, 4>) : o.rb == 2 ? go(rows_kernel<float, 2>) : go(rows_kernel<float, 1>);
+    const auto typed = [&](auto t) {
+        using T = decltype(t);
+        if (o.vec)
+            return o.rb == 4   ? go(rows_kernel<T, 4, true>)
+                   : o.rb == 2 ? go(rows_kernel<T, 2, true>)
+                               : go(rows_kernel<T, 1, true>);
+        return o.rb == 4   ? go(rows_kernel<T, 4, false>)
+               : o.rb == 2 ? go(rows_kernel<T, 2, false>)
+                           : go(rows_kernel<T, 1, false>);
+    };
+    return pr.dtype == KS_BF16 ? typed(__nv_bfloat16{}) : typed(float{});
 }
 
 }  // namespace ks

@@ -101,13 +101,13 @@ cudaError_t launch_tc(const Problem &p, const TcConfig &cfg);
 bool fma32_adapters_supported(const Problem &p);
 cudaError_t launch_fma32_adapters(const Problem &p, const float *vt, const Fma32Adapters &ad);
 
-// Adapters beside a product of few rows (ks_adapter_rows.cu), and H = scale X W^T for few rows (F a
-// multiple of a 16-byte vector, X and W aligned; ks_adapter.cuh).
+// Adapters beside a product of few rows (ks_adapter_rows.cu), and H = scale X W^T for few rows (vec:
+// F is a multiple of a 16-byte vector, X and W are aligned; ks_adapter.cuh).
 struct ShrinkArgs;
-bool adapter_rows_supported(const Problem &p, const void *A, int ldh);
+bool adapter_rows_supported(const Problem &p, int ldh);
 cudaError_t launch_adapter_rows(const Problem &p, const void *A, const void *B, const float *scales, const int *ids,
                                 int S, int R, const float *H, int ldh);
-cudaError_t launch_shrink_rows(const ShrinkArgs &p, int jobs, bool bf16, bool h_bf16, cudaStream_t st);
+cudaError_t launch_shrink_rows(const ShrinkArgs &p, int jobs, bool bf16, bool vec, cudaStream_t st);
 
 // Gradients (ks_backward.cu).  dV[i][l][k][j] = sum_n dY[n,(i,k,l)] X[n,(i,j,l)]
 // is computed over `splits` row ranges into fp32 partials W[split][a][d][b][c],

@@ -587,3 +587,22 @@ def test_a_broken_adapter_among_many_rows_of_many_ranks():
         ks.sync_status()
     other[4000] = False
     assert torch.equal(y[other], clean[other])
+
+
+@pytest.mark.parametrize("p", [(2, 162, 23, 8), (3, 38, 9, 5), (1, 150, 150, 1), (5, 33, 30, 9), (1, 200, 199, 20)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_tokens_of_odd_layers(p, dtype):
+    """Few rows, sizes of which no vector is a multiple; shift: buffers aligned to their elements alone."""
+    for n, r, kind, shift in ((1, 4, "rows", 0), (5, 64, "rows", 0), (33, 13, "segments", 1), (64, 1, "one", 0)):
+        q = make(p, n, 1 if kind == "one" else 3, r, dtype, kind, n, bias=True, shift=shift)
+        assert_forward(call(q, p, act="gelu_erf"), q, p, "gelu_erf")
+
+
+@pytest.mark.parametrize("p,n,r,s", [((8, 192, 48, 8), 131, 3, 20), ((4, 48, 48, 4), 2115, 20, 2), ((3, 38, 8, 5), 1203, 64, 2),
+                                     ((3, 110, 57, 1), 999, 9, 2), ((4, 19, 2, 13), 289, 64, 1), ((3, 29, 4, 13), 700, 30, 40)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wide_and_odd_layers(p, n, r, s, dtype):
+    for kind in ("segments", "rows"):
+        q = make(p, n, s, r, dtype, kind, n, bias=True)
+        assert_forward(call(q, p, act="relu"), q, p, "relu")
+        assert_backward(q, p, ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"]))
