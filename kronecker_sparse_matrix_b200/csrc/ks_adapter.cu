@@ -20,8 +20,9 @@
 //                          further stages (ks_fma32.cu);
 //   anything else          the product, H, and a second pass over Y (expand_kernel).
 // A backward call: one launch that lays out what the others read (prepare_kernel),
-// one for G and H, the product for dX as above, one for the partial sums of dA and
-// dB, one that adds them.
+// one for G and H, the product for dX as above (few rows of a GPT-2-shaped bf16 layer: 41 us
+// for all gradients of 32 rows where the tensor-core product takes 64), one for the partial
+// sums of dA and dB, one that adds them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1529,16 +1530,18 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     // for alone has the bits it has beside the others.
     static const char dummy[16] __attribute__((aligned(256))) = {};
     Problem p{dY, nullptr, dX ? dX : const_cast<char *>(dummy), a, c, b, d, batch, dtype, q.st};
-    const bool fusable = fuses(q, p, nullptr, out_f), fused = fusable && dX;
+    // Few rows: the kernel of few rows, G for H and A transposed for B.
+    const bool rowable = adapter_rows_supported(p, ldh), rows_x = rowable && dX;
+    const bool fusable = !rowable && fuses(q, p, nullptr, out_f), fused = fusable && dX;
     // fp32: the transposed blocks, transposed for the kernel, are the values as they are
-    const bool fusable32 = fuses_fp32(q, p, nullptr, out_f) && aligned(values, 16), fused32 = fusable32 && dX;
+    const bool fusable32 = !rowable && fuses_fp32(q, p, nullptr, out_f) && aligned(values, 16), fused32 = fusable32 && dX;
     const size_t vt = dX && !fused32 ? m.add((size_t)(o.nvals * o.elem)) : 0;
     const bool rows_g = dA || !fused;  // G also as rows
     const size_t h_bytes = (size_t)batch * ldh * (fused ? 2 : 4);
     const size_t g_at = want_g && rows_g ? m.add(h_bytes) : 0, h_at = dB ? m.add(h_bytes) : 0;
     const size_t p_at = fused ? m.add(plane_bytes(batch, q.R)) : 0;
     const size_t l_at = fused || fused32 ? m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4) : 0;
-    const size_t ap = fused || fused32 ? m.add((size_t)q.S * in_f * ldh * o.elem) : 0;
+    const size_t ap = fused || fused32 || rows_x ? m.add((size_t)q.S * in_f * ldh * o.elem) : 0;
     const bool sorted = ids && (dA || dB);
     const size_t perm_at = sorted ? m.add((size_t)batch * 4) : 0, off_at = sorted ? m.add((size_t)(q.S + 1) * 4) : 0;
     GradJob grad[2] = {{X, nullptr, nullptr, dA, in_f, in_f, 1}, {dY, nullptr, nullptr, dB, out_f, 1, q.R}};
@@ -1554,7 +1557,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     prep.perm = perm, prep.offsets = offsets, prep.sorted = sorted ? q.S : 0;
     if (want_g) prep.job[0] = transpose(B, w + bt, q.S, o.out_f, q.R, o.out_f);
     if (dX && !fused32) prep.job[1] = transpose(values, w + vt, a * d, b, c, b);
-    if (fused || fused32) prep.job[2] = transpose(A, w + ap, q.S, q.R, o.in_f, ldh);
+    if (fused || fused32 || rows_x) prep.job[2] = transpose(A, w + ap, q.S, q.R, o.in_f, ldh);
     cudaError_t e = prepare(q, prep, batch);
     ShrinkJob job[2];
     int n_jobs = 0;
@@ -1569,6 +1572,9 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
         const Fma32Adapters ad{reinterpret_cast<const float *>(w + g_at), reinterpret_cast<const float *>(w + ap), lists,
                                q.R, ldh, ldh, list_stride(q.S)};
         e = launch_fma32_adapters(p, static_cast<const float *>(values), ad);
+    } else if (rows_x && e == cudaSuccess) {
+        p.V = w + vt;
+        e = launch_adapter_rows(p, nullptr, w + ap, nullptr, ids, q.S, ldh, reinterpret_cast<const float *>(w + g_at), ldh);
     } else if (dX && e == cudaSuccess) {
         p.V = w + vt;
         const TcAdapters tc{w + ap, w + p_at, lists, q.S, ldh, list_stride(q.S)};
