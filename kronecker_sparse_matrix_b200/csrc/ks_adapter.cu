@@ -18,7 +18,8 @@
 //   fp32, d a multiple of 8, 2^30 flop and more
 //                          H (shrink_fp32_kernel), then the product with the adapters as
 //                          further stages (ks_fma32.cu);
-//   anything else          the product, H, and a second pass over Y (expand_kernel).
+//   anything else          the product (of a tiled kernel, or odd_product_kernel), H, and a second
+//                          pass over Y (expand_kernel).
 // A backward call: one launch that lays out what the others read (prepare_kernel),
 // one for G and H, the product for dX as above (few rows of a GPT-2-shaped bf16 layer: 41 us
 // for all gradients of 32 rows where the tensor-core product takes 64), one for the partial
@@ -625,6 +626,64 @@ __global__ void __launch_bounds__(128)
             if (in[c] && m < rows) put(Y + (n0 + m) * F + f[c], ep_apply(acc[m][c], bias, f[c], act));
 }
 
+// ---------------------------------------------------------------- products of odd layers
+
+// Y = X K^T for patterns that no tiled kernel of the library takes (its streaming kernels
+// read X again for every output): the blocks (i, l) one by one as 64 x 64 tiles of rows and
+// outputs, 16 products deep, through shared memory; a thread holds 4 x 4 sums.  X and Y have
+// stride d here; the blocks of all l run side by side, so that the lines they share are
+// read from L2.  10577 rows of (5, 117, 108, 3) in fp32: 204 us, 20
+// TFLOP/s (streaming: 3000 us); 675 rows of (1, 104, 171, 4) in bf16: 17 us (76).
+constexpr int kOddTile = 64, kOddDepth = 16;
+template <typename T>
+__global__ void __launch_bounds__(256)
+    odd_product_kernel(const T *__restrict__ X, const T *__restrict__ V, T *__restrict__ Y, long long N, int a, int b,
+                       int c, int d) {
+    constexpr int TILE = kOddTile, DEPTH = kOddDepth, LD = TILE + 4;
+    __shared__ __align__(16) float xs[DEPTH][LD], vs[DEPTH][LD];
+    const int k_tiles = (b + TILE - 1) / TILE;
+    const int l = blockIdx.x % d, k0 = blockIdx.x / d % k_tiles * TILE, i = blockIdx.x / d / k_tiles;
+    const long long n0 = (long long)blockIdx.y * TILE;
+    const long long in_f = (long long)a * c * d, out_f = (long long)a * b * d;
+    const int j = threadIdx.x % DEPTH, m = threadIdx.x / DEPTH;  // loads: rows (outputs) m, m + 16, ..
+    const T *const x = X + n0 * in_f + (long long)i * c * d + l;
+    const T *const v = V + ((long long)(i * (long long)d + l) * b + k0) * c;
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;  // outputs 4 tx .., rows 4 ty ..
+    float acc[4][4] = {};
+    float xr[4], vr[4];
+    const auto load = [&](int j0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int at = m + 16 * q;
+            xr[q] = j0 + j < c && n0 + at < N ? to_f(x[at * in_f + (long long)(j0 + j) * d]) : 0.f;
+            vr[q] = j0 + j < c && k0 + at < b ? to_f(v[(long long)at * c + j0 + j]) : 0.f;
+        }
+    };
+    load(0);
+    for (int j0 = 0; j0 < c; j0 += DEPTH) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) xs[j][m + 16 * q] = xr[q], vs[j][m + 16 * q] = vr[q];
+        __syncthreads();
+        load(j0 + DEPTH);  // (in flight during the products)
+#pragma unroll
+        for (int e = 0; e < DEPTH; ++e) {
+            const float4 p = load4(&xs[e][4 * ty]), w = load4(&vs[e][4 * tx]);
+            const float pa[4] = {p.x, p.y, p.z, p.w}, wa[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[r][k] = fmaf(pa[r], wa[k], acc[r][k]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (n0 + 4 * ty + r < N && k0 + 4 * tx + k < b)
+                put(Y + (n0 + 4 * ty + r) * out_f + ((long long)i * b + k0 + 4 * tx + k) * d + l, acc[r][k]);
+}
+
 // ---------------------------------------------------------------- dA and dB
 
 constexpr int kPrepareThreads = 256;
@@ -1190,6 +1249,27 @@ cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long 
                                                      : go(expand_any_kernel<T, true, false>);
 }
 
+// The product of a call that does not take the adapters along.
+ks_status product(const Problem &p) {
+    Plan plan;
+    const char *why = "";
+    const long long blocks = p.a * p.d * ((p.b + kOddTile - 1) / kOddTile), tiles = (p.batch + kOddTile - 1) / kOddTile;
+    // (smaller blocks leave most of a tile empty: 20000 rows of (2, 16, 8, 3) take 19 us of either kind)
+    if (p.dtype == KS_TF32 || p.b < 16 || p.c < 4 || tiles > 65535 || blocks > INT_MAX ||
+        !make_plan(p, KS_VARIANT_AUTO, &plan, &why) || plan.variant != KS_VARIANT_STREAM)
+        return run(p, KS_VARIANT_AUTO);
+    const dim3 grid((unsigned)blocks, (unsigned)tiles);
+    const auto go = [&](auto t) {
+        using T = decltype(t);
+        odd_product_kernel<T><<<grid, 256, 0, p.stream>>>(static_cast<const T *>(p.X), static_cast<const T *>(p.V),
+                                                          static_cast<T *>(p.Y), p.batch, (int)p.a, (int)p.b, (int)p.c,
+                                                          (int)p.d);
+        return cudaGetLastError();
+    };
+    const cudaError_t e = p.dtype == KS_BF16 ? go(__nv_bfloat16{}) : go(float{});
+    return e == cudaSuccess ? KS_OK : cuda_fail(e, "adapter product launch");
+}
+
 // How the gradients (dA, dB; out null: not wanted) are cut: feature blocks of each,
 // `bz` blocks of ranks, chunks of `chunk` of the N rows, for about 16 warps an SM
 // (tensor cores) or 32.
@@ -1470,7 +1550,7 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         const int ldh = round_up(q.R, 4);
         if ((s = alloc(&w, (size_t)batch * ldh * 4, q.st)) != KS_OK) return s;
         float *H = reinterpret_cast<float *>(w);
-        s = run(p, KS_VARIANT_AUTO);
+        s = product(p);
         const ShrinkJob job{X, A, H, nullptr, in_f};
         e = s == KS_OK ? shrink(q, &job, 1, false, batch, ldh, nullptr, by_rows(q, batch, in_f), in_f) : cudaSuccess;
         if (s == KS_OK && e == cudaSuccess)
@@ -1579,7 +1659,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
         p.V = w + vt;
         const TcAdapters tc{w + ap, w + p_at, lists, q.S, ldh, list_stride(q.S)};
         if (fused) p.ad = &tc;
-        s = run(p, fused ? KS_VARIANT_TC : KS_VARIANT_AUTO);
+        s = fused ? run(p, KS_VARIANT_TC) : product(p);
         const float *G = reinterpret_cast<const float *>(w + g_at);
         if (!fused && s == KS_OK)
             e = q.bf16 ? expand<__nv_bfloat16>(q, dX, A, true, batch, in_f, G, ldh, nullptr, KS_ACT_NONE)

@@ -249,13 +249,11 @@ bool rows_plan(const Problem &p, int ldh, RowsPlan *o) {
 
 bool adapter_rows_supported(const Problem &p, int ldh) {
     // about 5 us and 1 us for each 1.9M products (bf16); the tiles take 25 us and more.  Without
-    // vectors 1 us for each 0.2M products, against products of no tiled kernel: with d a
-    // multiple of a vector 280 us and more (108 rows of (2, 56, 87, 8): 30 and 830 us), otherwise
-    // from 20 us on.
+    // vectors 1 us for each 0.2M.
     const long long work = p.batch * p.out_features() * (p.c + ldh);
     if (p.dtype == KS_TF32 || p.batch > 256 || work > 1LL << 25) return false;
     RowsPlan o;
-    return rows_plan(p, ldh, &o) && (o.vec || p.d % (16 / p.elem_bytes()) == 0 || work <= 1LL << 23);
+    return rows_plan(p, ldh, &o) && (o.vec || work <= 1LL << 22);
 }
 
 cudaError_t launch_shrink_rows(const ShrinkArgs &p, int jobs, bool bf16, bool vec, cudaStream_t st) {

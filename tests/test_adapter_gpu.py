@@ -606,3 +606,13 @@ def test_wide_and_odd_layers(p, n, r, s, dtype):
         q = make(p, n, s, r, dtype, kind, n, bias=True)
         assert_forward(call(q, p, act="relu"), q, p, "relu")
         assert_backward(q, p, ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"]))
+
+
+@pytest.mark.parametrize("p,n", [((5, 21, 23, 4), 700), ((3, 90, 37, 2), 300), ((1, 16, 4, 1), 4097), ((2, 65, 17, 9), 129),
+                                 ((1, 104, 171, 4), 300)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_products_of_odd_layers(p, n, dtype):
+    """Blocks that no tile divides, in both directions."""
+    q = make(p, n, 2, 6, dtype, "segments", n, bias=True, shift=1)
+    assert_forward(call(q, p, act="gelu_tanh"), q, p, "gelu_tanh")
+    assert_backward(q, p, ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"]))
