@@ -18,7 +18,7 @@
 //   fp32, d a multiple of 8, 2^30 flop and more
 //                          H (shrink_fp32_kernel), then the product with the adapters as
 //                          further stages (ks_fma32.cu);
-//   anything else          the product (of a tiled kernel, or odd_product_kernel), H, and a second
+//   anything else          the product (of a tiled kernel, or tile_product_kernel), H, and a second
 //                          pass over Y (expand_kernel).
 // A backward call: one launch that lays out what the others read (prepare_kernel),
 // one for G and H, the product for dX as above (few rows of a GPT-2-shaped bf16 layer: 41 us
@@ -626,20 +626,21 @@ __global__ void __launch_bounds__(128)
             if (in[c] && m < rows) put(Y + (n0 + m) * F + f[c], ep_apply(acc[m][c], bias, f[c], act));
 }
 
-// ---------------------------------------------------------------- products of odd layers
+// ---------------------------------------------------------------- Y = X K^T of odd and small layers
 
-// Y = X K^T for patterns that no tiled kernel of the library takes (its streaming kernels
-// read X again for every output): the blocks (i, l) one by one as 64 x 64 tiles of rows and
-// outputs, 16 products deep, through shared memory; a thread holds 4 x 4 sums.  X and Y have
-// stride d here; the blocks of all l run side by side, so that the lines they share are
-// read from L2.  10577 rows of (5, 117, 108, 3) in fp32: 204 us, 20
+// For patterns that no tiled kernel of the library takes (its streaming kernels read X
+// again for every output), and few rows in fp32: the blocks (i, l) one by one as 64 x 64
+// tiles of rows and outputs, 16 products deep, through shared memory; a thread holds 4 x 4
+// sums.  X and Y have stride d here; the blocks of all l run side by side, so that the
+// lines they share are read from L2.  Bound by shared memory's reads, eight bytes for
+// each four FMAs, and by the scattered loads.  10577 rows of (5, 117, 108, 3) in fp32: 204 us, 20
 // TFLOP/s (streaming: 3000 us); 675 rows of (1, 104, 171, 4) in bf16: 17 us (76).
-constexpr int kOddTile = 64, kOddDepth = 16;
+constexpr int kProductTile = 64, kProductDepth = 16;
 template <typename T>
 __global__ void __launch_bounds__(256)
-    odd_product_kernel(const T *__restrict__ X, const T *__restrict__ V, T *__restrict__ Y, long long N, int a, int b,
+    tile_product_kernel(const T *__restrict__ X, const T *__restrict__ V, T *__restrict__ Y, long long N, int a, int b,
                        int c, int d) {
-    constexpr int TILE = kOddTile, DEPTH = kOddDepth, LD = TILE + 4;
+    constexpr int TILE = kProductTile, DEPTH = kProductDepth, LD = TILE + 4;
     __shared__ __align__(16) float xs[DEPTH][LD], vs[DEPTH][LD];
     const int k_tiles = (b + TILE - 1) / TILE;
     const int l = blockIdx.x % d, k0 = blockIdx.x / d % k_tiles * TILE, i = blockIdx.x / d / k_tiles;
@@ -1249,19 +1250,24 @@ cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long 
                                                      : go(expand_any_kernel<T, true, false>);
 }
 
-// The product of a call that does not take the adapters along.
+// The product of a call that does not take the adapters along: in small tiles where the
+// library would stream, and in fp32 where they are at most two for each SM (300 rows of (1, 256, 256,
+// 4): 18 us, 62 of the fp32 kernel, whose CTAs are fewer and longer; from 600 tiles on, 2400
+// rows, it catches up).
 ks_status product(const Problem &p) {
     Plan plan;
     const char *why = "";
-    const long long blocks = p.a * p.d * ((p.b + kOddTile - 1) / kOddTile), tiles = (p.batch + kOddTile - 1) / kOddTile;
+    const long long blocks = p.a * p.d * ((p.b + kProductTile - 1) / kProductTile);
+    const long long tiles = (p.batch + kProductTile - 1) / kProductTile;
     // (smaller blocks leave most of a tile empty: 20000 rows of (2, 16, 8, 3) take 19 us of either kind)
     if (p.dtype == KS_TF32 || p.b < 16 || p.c < 4 || tiles > 65535 || blocks > INT_MAX ||
-        !make_plan(p, KS_VARIANT_AUTO, &plan, &why) || plan.variant != KS_VARIANT_STREAM)
+        !make_plan(p, KS_VARIANT_AUTO, &plan, &why) ||
+        (plan.variant != KS_VARIANT_STREAM && (p.dtype != KS_F32 || blocks * tiles > 2 * sm_count())))
         return run(p, KS_VARIANT_AUTO);
     const dim3 grid((unsigned)blocks, (unsigned)tiles);
     const auto go = [&](auto t) {
         using T = decltype(t);
-        odd_product_kernel<T><<<grid, 256, 0, p.stream>>>(static_cast<const T *>(p.X), static_cast<const T *>(p.V),
+        tile_product_kernel<T><<<grid, 256, 0, p.stream>>>(static_cast<const T *>(p.X), static_cast<const T *>(p.V),
                                                           static_cast<T *>(p.Y), p.batch, (int)p.a, (int)p.b, (int)p.c,
                                                           (int)p.d);
         return cudaGetLastError();
