@@ -5,6 +5,7 @@ marshals torch tensors into the C ABI (ks_adapter_matmul, ks_adapter_backward).
 """
 from __future__ import annotations
 
+import threading
 import weakref
 from typing import Optional
 
@@ -79,6 +80,7 @@ class _EagerGraph:
 
 
 _eager_graphs = weakref.WeakSet()
+_eager_lock = threading.Lock()  # backward passes run in autograd's threads
 
 
 class _KSAdapterFn(torch.autograd.Function):
@@ -88,10 +90,11 @@ class _KSAdapterFn(torch.autograd.Function):
     def forward(ctx, x, values, bias, A, B, scales, ids, pattern):
         ctx.leaves = [weakref.ref(t) for t, need in zip((x, values, bias, A, B), ctx.needs_input_grad)
                       if need and t.is_leaf]
-        if ctx.leaves and torch.cuda.current_stream(x.device).cuda_stream == 0:
+        if ctx.leaves and x.is_cuda and torch.cuda.current_stream(x.device).cuda_stream == 0:
             ctx.graph = _EagerGraph()
             ctx.graph.leaves = ctx.leaves
-            _eager_graphs.add(ctx.graph)
+            with _eager_lock:
+                _eager_graphs.add(ctx.graph)
         values, A, B = values.contiguous(), A.contiguous(), B.contiguous()
         ctx.pattern = pattern
         ctx.save_for_backward(x, values, A, B, scales, ids)
@@ -104,7 +107,9 @@ class _KSAdapterFn(torch.autograd.Function):
         need = ctx.needs_input_grad
         if torch.cuda.is_current_stream_capturing():
             mine = {id(leaf()) for leaf in ctx.leaves} - {id(None)}
-            if any(id(leaf()) in mine for graph in _eager_graphs for leaf in graph.leaves):
+            with _eager_lock:
+                graphs = list(_eager_graphs)
+            if any(id(leaf()) in mine for graph in graphs for leaf in graph.leaves):
                 raise RuntimeError("an autograd graph of the same tensors, recorded on the default stream, still lives: "
                                    "release its results before a backward pass is captured")
         dy = dy.contiguous()
@@ -140,9 +145,10 @@ class KSAdapterLinear(KSLinear):
                                                   dtype=torch.float32, device=device))
 
     def _apply(self, fn, recurse=True):
+        scales = self.scales
         super()._apply(fn, recurse)
-        if self.scales.dtype != torch.float32:  # the scales stay fp32 under .to(dtype)
-            self.scales = self.scales.float()
+        if self.scales.dtype != torch.float32:  # the scales stay what they are under .to(dtype)
+            self.scales = scales.to(self.scales.device)
         return self
 
     def freeze_base(self) -> "KSAdapterLinear":

@@ -616,3 +616,36 @@ def test_products_of_odd_layers(p, n, dtype):
     q = make(p, n, 2, 6, dtype, "segments", n, bias=True, shift=1)
     assert_forward(call(q, p, act="gelu_tanh"), q, p, "gelu_tanh")
     assert_backward(q, p, ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"]))
+
+
+def test_layer_scales_keep_their_value_and_empty_batches_their_shape():
+    layer = ks.KSAdapterLinear((1, 64, 48, 8), 2, 3, alpha=1, bias=True, device=DEV).to(torch.bfloat16)
+    assert torch.equal(layer.scales, torch.full((2,), 1 / 3, device=DEV))
+    x = torch.zeros(2, 0, 384, device=DEV, dtype=torch.bfloat16, requires_grad=True)
+    y = layer(x, torch.zeros(2, dtype=torch.int32, device=DEV))
+    assert y.shape == (2, 0, 512)
+    y.sum().backward()
+    assert x.grad.shape == x.shape
+    for p in layer.parameters():
+        assert p.grad.shape == p.shape and not p.grad.any()
+
+
+def test_two_streams_of_one_device_at_once():
+    """Calls in flight beside one another, workspaces of each their own; few rows, stages and a second pass."""
+    p = (1, 256, 64, 16)
+    qs = [make(p, n, 3, 16, dt, "segments", n, bias=True) for n in (3, 500, 2000) for dt in (torch.bfloat16, torch.float32)]
+    want = [(call(q, p), ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"]))
+            for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for k in range(24):
+        q, st = qs[k % len(qs)], streams[k % len(streams)]
+        y = ks.adapter_matmul(q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"], bias=q["bias"], stream=st)
+        got.append((y, ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"],
+                                           stream=st)))
+    torch.cuda.synchronize()
+    ks.sync_status()
+    for k, (y, grads) in enumerate(got):
+        assert torch.equal(y, want[k % len(qs)][0])
+        assert all(torch.equal(u, v) for u, v in zip(grads, want[k % len(qs)][1]))
