@@ -1497,8 +1497,9 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
     char *w = nullptr;
     const int row_ldh = round_up(q.R, 4);
     if (adapter_rows_supported(p, row_ldh)) {
-        // few rows: one launch, or two where A[s] is more than a block should read for itself
-        const bool apart = (size_t)q.R * in_f * o.elem > 64 * 1024;
+        // few rows: one launch, or two where A[s] is more than a block should read for itself, which
+        // takes four rows from 16 on (32 rows in fp32, A[s] of 64 KB: 25 us in one, 19 in two)
+        const bool apart = (size_t)q.R * in_f * o.elem > (batch < 16 ? 64 : 32) * 1024;
         p.bias = bias;
         p.act = activation;
         if (!apart) {

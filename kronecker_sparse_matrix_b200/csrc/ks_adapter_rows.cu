@@ -248,12 +248,14 @@ bool rows_plan(const Problem &p, int ldh, RowsPlan *o) {
 }  // namespace
 
 bool adapter_rows_supported(const Problem &p, int ldh) {
-    // about 5 us and 1 us for each 1.9M products (bf16); the tiles take 25 us and more.  Without
-    // vectors 1 us for each 0.2M.
+    // About 5 us and 1 us for each 1.9M products in bf16, 0.5M in fp32, 0.2M without vectors,
+    // against 38 to 48 us of the bf16 tiles, 20 to 30 of the fp32 ones and 18 to 25 of odd layers'
+    // (GPT-2-shaped bf16, rank 16: 128 rows 29 and 48 us, 256 rows 53 and 47; fp32, rank 8: 16 rows
+    // 14 and 19, 64 rows 29 and 22).
     const long long work = p.batch * p.out_features() * (p.c + ldh);
-    if (p.dtype == KS_TF32 || p.batch > 256 || work > 1LL << 25) return false;
+    if (p.dtype == KS_TF32 || p.batch > 256 || work > (p.dtype == KS_BF16 ? 50LL : 11LL) * 1000000) return false;
     RowsPlan o;
-    return rows_plan(p, ldh, &o) && (o.vec || work <= 1LL << 22);
+    return rows_plan(p, ldh, &o) && (o.vec || work <= 4000000);
 }
 
 cudaError_t launch_shrink_rows(const ShrinkArgs &p, int jobs, bool bf16, bool vec, cudaStream_t st) {
