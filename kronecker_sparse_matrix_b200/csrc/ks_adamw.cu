@@ -191,6 +191,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
+// x / y from an approximate 1 / y: one Newton step on the quotient, its residual exact by
+// the FMA.  The codes and scales of 8-bit states are then as near as one rounding allows;
+// without it a code falls to the wrong side of a tie twice as often.
+__device__ __forceinline__ float quotient(float x, float y, float reciprocal) {
+    const float q = x * reciprocal;
+    return fmaf(fmaf(-q, y, x), reciprocal, q);
+}
+
 // T: type of p and g; S: type of the states (float, or unsigned char: e4m3).
 template <typename T, typename S, bool MASTER, int NT>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<NT> t, const Hyper h) {
@@ -283,8 +291,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         store8(p, pe, vec, lane, left);
         if constexpr (S8) {
             const float m_top = warp_top(me), v_top = warp_top(ve);
-            const float m_inv = m_top == 0.f ? 0.f : __fdividef(kTop, m_top);
-            const float v_inv = v_top == 0.f ? 0.f : __fdividef(kTop, v_top);
+            const float m_inv = m_top == 0.f ? 0.f : quotient(kTop, m_top, rcp_approx(m_top));
+            const float v_inv = v_top == 0.f ? 0.f : quotient(kTop, v_top, rcp_approx(v_top));
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 me[e] *= m_inv;
@@ -292,8 +300,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 ve[e] = ve[e] > 0.f ? fmaxf(y, kLow) : y;
             }
             if (lane == 0) {  // (the warp's reductions above come after every lane's reads)
-                scales[0][u] = m_top * (1.f / kTop);
-                scales[1][u] = v_top * (1.f / kTop);
+                scales[0][u] = quotient(m_top, kTop, 1.f / kTop);
+                scales[1][u] = quotient(v_top, kTop, 1.f / kTop);
             }
         }
         store8(m, me, vec, lane, left);
