@@ -43,15 +43,15 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;                  // elements of a scale: one warp's
 constexpr int kChunk = kThreads / 32 * kBlock;  // elements that a thread block takes at a time
-// units of a warp in a large step (142M bf16 parameters with 8-bit states: 286 us
-// with 4, 276 us with 8; 49M with masters and fp32 states: 218 and 221 us)
+// units of a warp in a large step (142M bf16 parameters with 8-bit states, before blend: 286
+// us with 4, 276 us with 8; 49M with masters and fp32 states: 218 and 221 us)
 constexpr int kIters8 = 8, kIters32 = 4;
 constexpr float kTop = 448.f;                // largest e4m3 number
 constexpr float kLow = 0.001953125f;         // 2^-9, the smallest positive one
 constexpr float kNone = 7.888609052210118e-31f;  // 2^-100
 
 struct Hyper {
-    float lr, beta1, omb1, beta2, omb2, eps, wd;
+    float lr, beta1, omb1, beta2, omb2, eps, wd, one;
     float bc1, inv_root_bc2;  // 1 - beta1^t and 1 / sqrt(1 - beta2^t), when step is null
     double log_beta1, log_beta2;
     const long long *step;    // device step number, or null
@@ -191,12 +191,20 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
-// x / y from an approximate 1 / y: one Newton step on the quotient, its residual exact by
-// the FMA.  The codes and scales of 8-bit states are then as near as one rounding allows;
-// without it a code falls to the wrong side of a tie twice as often.
-__device__ __forceinline__ float quotient(float x, float y, float reciprocal) {
-    const float q = x * reciprocal;
-    return fmaf(fmaf(-q, y, x), reciprocal, q);
+// 448 / top: the reciprocal to within one rounding by a Newton step, its residual exact
+// by the FMA.  (With the bare approximation more elements fell to the other side of a tie
+// between two codes than rounding alone puts there.)
+__device__ __forceinline__ float codes_per(float top) {
+    const float r = rcp_approx(top);
+    return fmaf(fmaf(-r, top, 1.f), r, r) * kTop;
+}
+
+// x a + y b of pairs, both products and the sum rounded.  The sum is an FMA by a one that
+// the compiler does not know: it contracts a product and a sum of pairs into one FMA, and
+// codes of m near a tie then differ from those of the formula as written.  142M bf16
+// parameters with 8-bit states: 302 us, contracted 257; fp32 states: no difference.
+__device__ __forceinline__ float2 blend(float2 x, float2 a, float2 y, float2 b, float2 one) {
+    return __ffma2_rn(__fmul2_rn(x, a), one, __fmul2_rn(y, b));
 }
 
 // T: type of p and g; S: type of the states (float, or unsigned char: e4m3).
@@ -224,6 +232,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const float2 keep = make_float2(1.f - lr * h.wd, 1.f - lr * h.wd), rate = make_float2(-lr / bc1, -lr / bc1);
     const float2 b1 = make_float2(h.beta1, h.beta1), o1 = make_float2(h.omb1, h.omb1);
     const float2 b2 = make_float2(h.beta2, h.beta2), o2 = make_float2(h.omb2, h.omb2);
+    const float2 one = make_float2(h.one, h.one);
     const float2 gs2 = make_float2(gs, gs), ib = make_float2(ib2, ib2), eps = make_float2(h.eps, h.eps);
     const long long n = t.n[lo];
     const bool vectors = t.aligned[lo];
@@ -273,8 +282,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 v0 = __fmul2_rn(v0, v_scale);
                 v0 = __fmul2_rn(v0, v0);
             }
-            const float2 m1 = __fadd2_rn(__fmul2_rn(m0, b1), __fmul2_rn(gr, o1));
-            const float2 v1 = __fadd2_rn(__fmul2_rn(v0, b2), __fmul2_rn(__fmul2_rn(gr, gr), o2));
+            const float2 m1 = blend(m0, b1, gr, o1, one);
+            const float2 v1 = blend(v0, b2, __fmul2_rn(gr, gr), o2, one);
             float2 root;
             if constexpr (S8)
                 root = make_float2(sqrt_approx(v1.x), sqrt_approx(v1.y));
@@ -291,8 +300,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         store8(p, pe, vec, lane, left);
         if constexpr (S8) {
             const float m_top = warp_top(me), v_top = warp_top(ve);
-            const float m_inv = m_top == 0.f ? 0.f : quotient(kTop, m_top, rcp_approx(m_top));
-            const float v_inv = v_top == 0.f ? 0.f : quotient(kTop, v_top, rcp_approx(v_top));
+            const float m_inv = m_top == 0.f ? 0.f : codes_per(m_top);
+            const float v_inv = v_top == 0.f ? 0.f : codes_per(v_top);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 me[e] *= m_inv;
@@ -300,8 +309,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 ve[e] = ve[e] > 0.f ? fmaxf(y, kLow) : y;
             }
             if (lane == 0) {  // (the warp's reductions above come after every lane's reads)
-                scales[0][u] = quotient(m_top, kTop, 1.f / kTop);
-                scales[1][u] = quotient(v_top, kTop, 1.f / kTop);
+                scales[0][u] = m_top * (1.f / kTop);
+                scales[1][u] = v_top * (1.f / kTop);
             }
         }
         store8(m, me, vec, lane, left);
@@ -478,7 +487,7 @@ ks_status adamw_step(const ks_adamw_tensor *tensors, int64_t n_tensors, int dtyp
     h.lr = (float)opt->lr;
     h.beta1 = (float)opt->beta1, h.omb1 = (float)(1.0 - opt->beta1);
     h.beta2 = (float)opt->beta2, h.omb2 = (float)(1.0 - opt->beta2);
-    h.eps = (float)opt->eps, h.wd = (float)opt->weight_decay;
+    h.eps = (float)opt->eps, h.wd = (float)opt->weight_decay, h.one = 1.f;
     h.bc1 = (float)(1.0 - std::pow(opt->beta1, (double)opt->step));
     h.inv_root_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(opt->beta2, (double)opt->step)));
     h.log_beta1 = std::log(opt->beta1), h.log_beta2 = std::log(opt->beta2);  // -inf for 0: 1 - 0^t = 1
