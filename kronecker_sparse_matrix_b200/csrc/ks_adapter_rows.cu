@@ -27,7 +27,8 @@ namespace ks {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxSmem = 96 * 1024;
+constexpr int kMaxSmem = 96 * 1024;       // dynamic shared memory of a block at most
+constexpr int kDefaultSmem = 48 * 1024;   // without opting in, rows_kernel's own `sid` included
 
 // H[n][r] = scale[s] sum_f X[n][f] W[s][r][f], r < ldh (zeros past R and for rows without an adapter).
 template <typename T, bool VEC>
@@ -286,8 +287,9 @@ cudaError_t launch_adapter_rows(const Problem &pr, const void *A, const void *B,
     p.status = device_status_ptr();
     const dim3 grid((unsigned)o.tiles, (unsigned)((pr.batch + o.rb - 1) / o.rb));
     const auto go = [&](auto kernel) {
-        if (o.smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)o.smem);
+        // (the limit is the function's, for all host threads: one that every call sets to the same value)
+        if (o.smem + 4 * sizeof(int) > kDefaultSmem) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
             if (e != cudaSuccess) return e;
         }
         kernel<<<grid, kThreads, o.smem, pr.stream>>>(p);
