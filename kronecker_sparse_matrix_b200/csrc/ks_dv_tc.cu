@@ -288,11 +288,12 @@ cudaError_t launch_dv_tc(const DvProblem &q, float *W, int splits, long long row
     p.status = device_status_ptr();
     if (!p.status) return cudaErrorUnknown;
     p.wait_ns = pipeline_wait_bound_ns();
-    const int stage_bytes = kDvRows * (kDvM + (int)q.c) * 16;
-    const int smem = kDvStages * stage_bytes + 3 * kDvStages * 8 + 8 + 16 + 1024;
+    const auto smem_of = [](int c) { return kDvStages * kDvRows * (kDvM + c) * 16 + 3 * kDvStages * 8 + 8 + 16 + 1024; };
+    const int smem = smem_of((int)q.c);
     const long long grid = (long long)p.n_g * p.n_kt * splits;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(dv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the limit is the function's, for all host threads: the same of every call, the widest c's)
+    cudaError_t e = cudaFuncSetAttribute(dv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(64));
     if (e != cudaSuccess) return e;
     dv_tc_kernel<<<(int)grid, kDvThreads, smem, q.stream>>>(ymap, xmap, p);
     return cudaGetLastError();

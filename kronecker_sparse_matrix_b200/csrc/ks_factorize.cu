@@ -171,7 +171,10 @@ cudaError_t launch_rank1_fit(const float *P, float *V1, float *V2, int64_t a1, i
     const long long blocks = a1 * b1 * c2 * d2;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const size_t smem = (size_t)(b2 * (c1 + 1) + 2 * c1 + b2 + 32) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(rank1_fit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The limit is the function's, for all host threads: the same of every call, what the largest can
+    // take (2 c1 + b2 < 2 b2 (c1 + 1)).
+    constexpr int limit = (3 * kMaxBlockElems + 32) * (int)sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(rank1_fit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
     if (e != cudaSuccess) return e;
     rank1_fit_kernel<<<(int)blocks, kFitThreads, smem, stream>>>(p);
     return cudaGetLastError();

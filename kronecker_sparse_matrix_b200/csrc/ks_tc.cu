@@ -88,7 +88,9 @@ constexpr int kEpiWarp0 = 6;       // warps 6..9
 constexpr int kEpiWarpBytes = 4096; // staging per epilogue warp: one box of 32 rows x 128 B
 constexpr int kChunkBytes = 128;    // output bytes per row per epilogue chunk
 constexpr int kBiasBytes = 2048;    // fused bias of one tile (bp * DLS * ES <= 2 KB), per buffer and warp
-constexpr int kSmemLimit = 232448; // per-block opt-in maximum on sm_100
+// Per-block opt-in maximum on sm_100, which every launch opts in to: the limit is the function's, and
+// a call on another host thread must not lower it.
+constexpr int kSmemLimit = 232448;
 
 // j per MMA (K = 32 bytes): 16 bf16, 8 fp32 (TF32)
 __host__ __device__ constexpr int step_j(int es) { return 32 / es; }
@@ -1153,7 +1155,7 @@ static cudaError_t launch_dls(const Problem &pr, const TcConfig &cfg) {
             auto kern = tc_kernel<DLS, T, true, false, true>;
             if constexpr (kY4)
                 if (y4d) kern = tc_kernel<DLS, T, true, true, true>;
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
             if (e != cudaSuccess) return e;
             kern<<<(int)grid, kThreads, L.total, pr.stream>>>(xmap, vmap, ymap, p, ad);
             return cudaGetLastError();
@@ -1162,7 +1164,7 @@ static cudaError_t launch_dls(const Problem &pr, const TcConfig &cfg) {
     auto kern = ep ? tc_kernel<DLS, T, true> : tc_kernel<DLS, T, false>;
     if constexpr (kY4)
         if (y4d) kern = ep ? tc_kernel<DLS, T, true, true> : tc_kernel<DLS, T, false, true>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     kern<<<(int)grid, kThreads, L.total, pr.stream>>>(xmap, vmap, ymap, p, TcAd<false>{});
     return cudaGetLastError();
