@@ -837,12 +837,12 @@ struct GradArgs {
 // each 16 bytes of P a lane loads.  Bound by P's latency: what costs warps an SM (rows
 // of P a step ahead in registers, Q's rows in shared memory and eight rows in
 // flight: 106 and 98 us where this takes 59, 25216 x (1536 + 384) rank 8) loses more than it hides.  Types and alignment: any (VEC: vectors of four).
-template <typename T, typename Q, int RC, bool VEC>
+template <typename T, int RC, bool VEC>
 __global__ void __launch_bounds__(128) grad_kernel(const __grid_constant__ GradArgs a) {
     const GradJob &job = a.job[(int)blockIdx.x >= a.first];
     const int bx = (int)blockIdx.x >= a.first ? (int)blockIdx.x - a.first : (int)blockIdx.x;
     const T *__restrict__ const P = static_cast<const T *>(job.P);
-    const Q *__restrict__ const V = static_cast<const Q *>(job.V);
+    const float *__restrict__ const V = static_cast<const float *>(job.V);
     const int *__restrict__ const perm = a.perm, *__restrict__ const offsets = a.offsets;
     float *__restrict__ const W = job.W;
     const int N = a.N, F = job.F, R = a.R, ldh = a.ldh, S = a.S, chunk = a.chunk;
@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(128) grad_kernel(const __grid_constant__ GradA
                 if (f + 2 < F) x.z = to_f(p[2]);
                 if (f + 3 < F) x.w = to_f(p[3]);
             }
-            const Q *v = V + n * ldh + r0;
+            const float *v = V + n * ldh + r0;
 #pragma unroll
             for (int r = 0; r < RC; r += 4) {
                 if (r0 + r >= ldh) break;
@@ -1332,21 +1332,21 @@ cudaError_t grads(const Adapters &q, const GradPlan &g, const GradJob (&job)[2],
         kernel<<<grid, 32 * g.warps, 0, q.st>>>(p);
         return cudaGetLastError();
     };
-    const auto typed = [&](auto v) {
+    const auto mma = [&](auto v) {
         using V = decltype(v);
-        if (g.mma)
-            return g.rc == 16   ? go(grad_mma_kernel<1, V>)
-                   : g.rc == 32 ? go(grad_mma_kernel<2, V>)
-                                : go(grad_mma_kernel<4, V>);
-        if (q.bf16)
-            return g.rc == 8 ? go(grad_kernel<__nv_bfloat16, V, 8, false>) : go(grad_kernel<__nv_bfloat16, V, 16, false>);
-        if constexpr (std::is_same_v<V, float>) {
-            if (g.rc == 8) return g.vec ? go(grad_kernel<float, V, 8, true>) : go(grad_kernel<float, V, 8, false>);
-            return g.vec ? go(grad_kernel<float, V, 16, true>) : go(grad_kernel<float, V, 16, false>);
-        }
-        return cudaErrorInvalidConfiguration;
+        return g.rc == 16   ? go(grad_mma_kernel<1, V>)
+               : g.rc == 32 ? go(grad_mma_kernel<2, V>)
+                            : go(grad_mma_kernel<4, V>);
     };
-    cudaError_t e = v_bf16 ? typed(__nv_bfloat16{}) : typed(float{});
+    cudaError_t e;
+    if (g.mma)
+        e = v_bf16 ? mma(__nv_bfloat16{}) : mma(float{});
+    else if (q.bf16)
+        e = g.rc == 8 ? go(grad_kernel<__nv_bfloat16, 8, false>) : go(grad_kernel<__nv_bfloat16, 16, false>);
+    else if (g.vec)
+        e = g.rc == 8 ? go(grad_kernel<float, 8, true>) : go(grad_kernel<float, 16, true>);
+    else
+        e = g.rc == 8 ? go(grad_kernel<float, 8, false>) : go(grad_kernel<float, 16, false>);
     if (e != cudaSuccess) return e;
     p.first = reduce_blocks[0];
     const dim3 rgrid((unsigned)(reduce_blocks[0] + reduce_blocks[1]), (unsigned)q.S, (unsigned)((q.R + 7) / 8));
@@ -1613,26 +1613,30 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     const bool want_g = dX || dA;
     const size_t bt = want_g ? m.add((size_t)o.bbytes) : 0;
     // dX = dY K: the product of pattern (a, c, b, d) with the transposed blocks.  What
-    // is wanted does not decide how G, H and the sums are computed: a gradient asked
-    // for alone has the bits it has beside the others.
+    // is wanted, and the alignment of what dX alone reads and writes (values, dX), do not decide
+    // how G, H and the sums are computed: a gradient asked for alone has the bits it has beside the others.
     static const char dummy[16] __attribute__((aligned(256))) = {};
-    Problem p{dY, nullptr, dX ? dX : const_cast<char *>(dummy), a, c, b, d, batch, dtype, q.st};
+    Problem p{dY, nullptr, const_cast<char *>(dummy), a, c, b, d, batch, dtype, q.st};
     // Few rows: the kernel of few rows, G for H and A transposed for B.
     const bool rowable = adapter_rows_supported(p, ldh), rows_x = rowable && dX;
-    const bool fusable = !rowable && fuses(q, p, nullptr, out_f), fused = fusable && dX;
+    const bool fusable = !rowable && fuses(q, p, nullptr, out_f), fused = fusable && dX && aligned(dX, 16);
     // fp32: the transposed blocks, transposed for the kernel, are the values as they are
-    const bool fusable32 = !rowable && fuses_fp32(q, p, nullptr, out_f) && aligned(values, 16), fused32 = fusable32 && dX;
+    const bool fusable32 = !rowable && fuses_fp32(q, p, nullptr, out_f);
+    const bool fused32 = fusable32 && dX && aligned(dX, 16) && aligned(values, 16);
+    p.Y = dX;
+    GradJob grad[2] = {{X, nullptr, nullptr, dA, in_f, in_f, 1}, {dY, nullptr, nullptr, dB, out_f, 1, q.R}};
+    const GradPlan plan = grad_plan(q, grad, batch);
+    // rows of G and H in bf16 where no kernel sees more of them: those of the tensor cores round them themselves
+    const bool v_bf16 = fused && plan.mma;
     const size_t vt = dX && !fused32 ? m.add((size_t)(o.nvals * o.elem)) : 0;
     const bool rows_g = dA || !fused;  // G also as rows
-    const size_t h_bytes = (size_t)batch * ldh * (fused ? 2 : 4);
+    const size_t h_bytes = (size_t)batch * ldh * (v_bf16 ? 2 : 4);
     const size_t g_at = want_g && rows_g ? m.add(h_bytes) : 0, h_at = dB ? m.add(h_bytes) : 0;
     const size_t p_at = fused ? m.add(plane_bytes(batch, q.R)) : 0;
     const size_t l_at = fused || fused32 ? m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4) : 0;
     const size_t ap = fused || fused32 || rows_x ? m.add((size_t)q.S * in_f * ldh * o.elem) : 0;
     const bool sorted = ids && (dA || dB);
     const size_t perm_at = sorted ? m.add((size_t)batch * 4) : 0, off_at = sorted ? m.add((size_t)(q.S + 1) * 4) : 0;
-    GradJob grad[2] = {{X, nullptr, nullptr, dA, in_f, in_f, 1}, {dY, nullptr, nullptr, dB, out_f, 1, q.R}};
-    const GradPlan plan = grad_plan(q, grad, batch);
     const size_t w_at = dA || dB ? m.add(plan.bytes) : 0;
     char *w = nullptr;
     if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
@@ -1653,7 +1657,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
                                   fused ? reinterpret_cast<unsigned short *>(w + p_at) : nullptr, out_f};
     if (dB) job[n_jobs++] = ShrinkJob{X, A, w + h_at, nullptr, in_f};
     if (e == cudaSuccess)
-        e = shrink(q, job, n_jobs, fused, batch, ldh, lists,
+        e = shrink(q, job, n_jobs, v_bf16, batch, ldh, lists,
                    !fusable && !fusable32 && by_rows(q, batch, std::max(in_f, out_f)), std::max(in_f, out_f));
     if (fused32 && e == cudaSuccess) {
         const Fma32Adapters ad{reinterpret_cast<const float *>(w + g_at), reinterpret_cast<const float *>(w + ap), lists,
@@ -1675,7 +1679,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     if ((dA || dB) && e == cudaSuccess && s == KS_OK) {
         grad[0].V = w + g_at;
         grad[1].V = w + h_at;
-        e = grads(q, plan, grad, fused, ldh, perm, offsets, batch, w + w_at);
+        e = grads(q, plan, grad, v_bf16, ldh, perm, offsets, batch, w + w_at);
     }
     if (e != cudaSuccess && s == KS_OK) s = cuda_fail(e, "adapter gradient launch");
     e = cudaFreeAsync(w, q.st);
