@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kDvThreads, 1)
             mbar_init(&x_empty[s], 1);
         }
         mbar_init(done, 1);
-        *abort_flag = 0;
+        *abort_flag = p.wait_ns == 0;  // (an injected timeout: the first wait that is not over gives up)
+        if (p.wait_ns == 0) atomicOr(p.status, kDevTimeout);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc(tmem_holder, 512);

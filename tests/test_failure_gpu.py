@@ -130,3 +130,33 @@ def test_dv_tensor_core_wait_timeout_is_reported_and_the_next_call_is_correct(mo
     dv = ks.matmul_dv(dy, f.X, p)
     ks.sync_status()
     assert oracle.max_rel_err(dv.cpu().reshape(-1), oracle.dv(dy.cpu(), f.X.cpu(), p)) <= 1e-2
+
+
+def test_every_injected_timeout_is_reported(monkeypatch):
+    """However fast the copies that a wait waits for: small products, again and again."""
+    cases = [(p, inputs.factor_inputs(p, n, seed=19, dtype=torch.bfloat16, device=DEV))
+             for p, n in (((1, 64, 64, 1), 300), ((2, 64, 64, 1), 1500), ((2, 64, 32, 2), 300), ((1, 64, 48, 8), 20),
+                          ((1, 64, 64, 16), 300), ((1, 128, 16, 8), 16))]
+    ks.sync_status()
+    missed = []
+    monkeypatch.setenv("KS_FAULT_INJECT", "timeout")
+    for k in range(60):
+        for p, f in cases:
+            try:
+                ks.matmul(f.X, f.values, p)
+                ks.sync_status()
+                missed.append((k, p))
+            except ks.KsError as err:
+                assert err.status == 6
+    p, f = cases[-1]
+    dy = torch.ones(16, inputs.out_features(p), dtype=torch.bfloat16, device=DEV)
+    for _ in range(60):
+        ks.matmul_dv(dy, f.X, p)
+        with pytest.raises(ks.KsError):
+            ks.sync_status()
+    monkeypatch.delenv("KS_FAULT_INJECT")
+    assert not missed, f"{len(missed)} of 360, first {missed[0]}"
+    for p, f in cases:
+        Y = ks.matmul(f.X, f.values, p)
+        ks.sync_status()
+        assert oracle.max_rel_err(Y.cpu(), oracle.matmul(f.X.cpu(), f.values.cpu(), p)) <= 1e-2
