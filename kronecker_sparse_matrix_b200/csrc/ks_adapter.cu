@@ -18,8 +18,9 @@
 //   fp32, d a multiple of 8, 2^30 flop and more
 //                          H (shrink_fp32_kernel), then the product with the adapters as
 //                          further stages (ks_fma32.cu);
-//   anything else          the product (of a tiled kernel, or tile_product_kernel), H, and a second
-//                          pass over Y (expand_kernel).
+//   anything else          H, the product (of a tiled kernel, or tile_product_kernel), and a second
+//                          pass over it (expand_kernel); in bf16 the product is held in fp32 for
+//                          that pass, some rows at a time, so that the result is rounded once.
 // A backward call: one launch that lays out what the others read (prepare_kernel),
 // one for G and H, the product for dX as above (few rows of a GPT-2-shaped bf16 layer: 41 us
 // for all gradients of 32 rows where the tensor-core product takes 64), one for the partial
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// ---------------------------------------------------------------- Y = act(Y + bias + H W)
+// ---------------------------------------------------------------- Y = act(P + bias + H W)
 
 constexpr int kExpandRows = 8;
 
@@ -466,13 +467,14 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
 // F a multiple of 4 and vectors of four aligned (25216 x 384 fp32, rank 8: 17 us, 4.5
 // TB/s; 16 rows a thread took 23): a thread owns four outputs of eight
 // rows and passes once over the weights of each adapter among them, four ranks at
-// a time; H is read from shared memory (the same address in a warp), Y before the
-// products, so that its latency is theirs.
+// a time; H is read from shared memory (the same address in a warp), P before the
+// products, so that its latency is theirs.  P is the KS product in fp32: Y itself, or in
+// bf16 a workspace.
 // RC: the ranks are contiguous in W (B) and come in whole fours; otherwise the
 // features are (A).
 template <typename T, bool RC, int ACT>
 __global__ void __launch_bounds__(128, 6)
-    expand_kernel(T *__restrict__ Y, const T *__restrict__ W, const int *__restrict__ ids,
+    expand_kernel(T *Y, const float *P, const T *__restrict__ W, const int *__restrict__ ids,
                   const float *__restrict__ H, long long N, int F, int R, int ldh, int S,
                   const T *__restrict__ bias) {
     constexpr int ROWS = kExpandRows;
@@ -491,6 +493,7 @@ __global__ void __launch_bounds__(128, 6)
     const int f = (blockIdx.y * 128 + threadIdx.x) * 4;
     const bool in = f < F;
     T *y = Y + n0 * F + f;
+    const float *product = P + n0 * F + f;
     float4 acc[ROWS];
     {
         const float4 b = bias && in ? load4(bias + f) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(128, 6)
         for (int m = 0; m < ROWS; ++m) {
             acc[m] = b;
             if (in && m < rows) {
-                const float4 v = load4(y + (long long)m * F);
+                const float4 v = load4(product + (long long)m * F);
                 acc[m] = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
             }
         }
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(128, 6)
 // where a thread for each output took 346).
 template <typename T, bool RC, bool RV>
 __global__ void __launch_bounds__(128)
-    expand_any_kernel(T *__restrict__ Y, const T *__restrict__ W, const int *__restrict__ ids,
+    expand_any_kernel(T *Y, const float *P, const T *__restrict__ W, const int *__restrict__ ids,
                       const float *__restrict__ H, long long N, int F, int R, int ldh, int S,
                       const T *__restrict__ bias, int act) {
     constexpr int ROWS = kExpandRows;
@@ -588,7 +591,7 @@ __global__ void __launch_bounds__(128)
         in[c] = at < F;
         f[c] = in[c] ? (int)at : 0;
 #pragma unroll
-        for (int m = 0; m < ROWS; ++m) acc[m][c] = in[c] && m < rows ? to_f(Y[(n0 + m) * F + f[c]]) : 0.f;
+        for (int m = 0; m < ROWS; ++m) acc[m][c] = in[c] && m < rows ? P[(n0 + m) * F + f[c]] : 0.f;
     }
     for (int s = next_id(id, -1); s != INT_MAX; s = next_id(id, s)) {
         const unsigned take = __ballot_sync(0xFFFFFFFFu, id == s);
@@ -638,8 +641,8 @@ __global__ void __launch_bounds__(128)
 constexpr int kProductTile = 64, kProductDepth = 16;
 template <typename T>
 __global__ void __launch_bounds__(256)
-    tile_product_kernel(const T *__restrict__ X, const T *__restrict__ V, T *__restrict__ Y, long long N, int a, int b,
-                       int c, int d) {
+    tile_product_kernel(const T *__restrict__ X, const T *__restrict__ V, float *__restrict__ Y, long long N, int a,
+                       int b, int c, int d) {
     constexpr int TILE = kProductTile, DEPTH = kProductDepth, LD = TILE + 4;
     __shared__ __align__(16) float xs[DEPTH][LD], vs[DEPTH][LD];
     const int k_tiles = (b + TILE - 1) / TILE;
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (n0 + 4 * ty + r < N && k0 + 4 * tx + k < b)
-                put(Y + (n0 + 4 * ty + r) * out_f + ((long long)i * b + k0 + 4 * tx + k) * d + l, acc[r][k]);
+                Y[(n0 + 4 * ty + r) * out_f + ((long long)i * b + k0 + 4 * tx + k) * d + l] = acc[r][k];
 }
 
 // ---------------------------------------------------------------- dA and dB
@@ -1216,18 +1219,18 @@ cudaError_t shrink(const Adapters &q, const ShrinkJob *job, int jobs, bool h_bf1
     return h_bf16 ? ranks(__nv_bfloat16{}) : ranks(float{});
 }
 
-// Y = act(Y + bias + H W); with_a: W is A (rank x F), else B (F x rank).
+// Y = act(P + bias + H W), P in fp32 (Y itself, or a workspace); with_a: W is A (rank x F), else B (F x rank).
 template <typename T>
-cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long long N, int F, const float *H, int ldh,
-                   const void *bias, int act) {
+cudaError_t expand(const Adapters &q, void *Y, const float *P, const void *W, bool with_a, long long N, int F,
+                   const float *H, int ldh, const void *bias, int act) {
     T *y = static_cast<T *>(Y);
     const T *w = static_cast<const T *>(W), *b = static_cast<const T *>(bias);
     const size_t smem = (size_t)ldh * kExpandRows * 4;
-    if (F % 4 == 0 && aligned(Y, 4 * sizeof(T)) && aligned(W, 4 * sizeof(T)) && aligned(bias, 4 * sizeof(T)) &&
-        (with_a || q.R % 4 == 0) && (F + 511LL) / 512 <= 65535) {
+    if (F % 4 == 0 && aligned(Y, 4 * sizeof(T)) && aligned(P, 16) && aligned(W, 4 * sizeof(T)) &&
+        aligned(bias, 4 * sizeof(T)) && (with_a || q.R % 4 == 0) && (F + 511LL) / 512 <= 65535) {
         const dim3 grid((unsigned)((N + kExpandRows - 1) / kExpandRows), (unsigned)((F + 511) / 512));
         const auto go = [&](auto kernel) {
-            kernel<<<grid, 128, smem, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, b);
+            kernel<<<grid, 128, smem, q.st>>>(y, P, w, q.ids, H, N, F, q.R, ldh, q.S, b);
             return cudaGetLastError();
         };
         if (with_a) return go(expand_kernel<T, false, KS_ACT_NONE>);
@@ -1242,7 +1245,7 @@ cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long 
     const long long blocks = (N + kExpandRows - 1) / kExpandRows * ((F + 4LL * threads - 1) / (4 * threads));
     if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
     const auto go = [&](auto kernel) {
-        kernel<<<(unsigned)blocks, threads, smem, q.st>>>(y, w, q.ids, H, N, F, q.R, ldh, q.S, b, act);
+        kernel<<<(unsigned)blocks, threads, smem, q.st>>>(y, P, w, q.ids, H, N, F, q.R, ldh, q.S, b, act);
         return cudaGetLastError();
     };
     if (with_a) return go(expand_any_kernel<T, false, false>);
@@ -1250,7 +1253,7 @@ cudaError_t expand(const Adapters &q, void *Y, const void *W, bool with_a, long 
                                                      : go(expand_any_kernel<T, true, false>);
 }
 
-// The product of a call that does not take the adapters along: in small tiles where the
+// The product of a call that does not take the adapters along (bf16: with y_f32), in small tiles where the
 // library would stream, and in fp32 where they are at most two for each SM (300 rows of (1, 256, 256,
 // 4): 18 us, 62 of the fp32 kernel, whose CTAs are fewer and longer; from 600 tiles on, 2400
 // rows, it catches up).
@@ -1268,12 +1271,49 @@ ks_status product(const Problem &p) {
     const auto go = [&](auto t) {
         using T = decltype(t);
         tile_product_kernel<T><<<grid, 256, 0, p.stream>>>(static_cast<const T *>(p.X), static_cast<const T *>(p.V),
-                                                          static_cast<T *>(p.Y), p.batch, (int)p.a, (int)p.b, (int)p.c,
-                                                          (int)p.d);
+                                                          static_cast<float *>(p.Y), p.batch, (int)p.a, (int)p.b,
+                                                          (int)p.c, (int)p.d);
         return cudaGetLastError();
     };
     const cudaError_t e = p.dtype == KS_BF16 ? go(__nv_bfloat16{}) : go(float{});
     return e == cudaSuccess ? KS_OK : cuda_fail(e, "adapter product launch");
+}
+
+// The product and the second pass over it: p.Y = act(X K^T + bias + H W).  In bf16 the product goes
+// to `sums` in fp32, product_rows() rows at a time (p's bias and act are the second pass's).  Twice
+// the bytes of a product in bf16 between the two passes: (1, 96, 24, 8) 58 us either way, (8, 2, 2,
+// 256) 181 us for 156, 8000 rows each.  Pieces of 64 MB do not gain by L2 what they lose at their
+// ends (195 us, 24 MB: 234), so the limit is one on memory.
+constexpr long long kSumsBytes = 256 << 20;
+long long product_rows(const Problem &p) {
+    const long long rows = kSumsBytes / (4 * p.out_features()) / 128 * 128;
+    return p.dtype == KS_BF16 ? std::min<long long>(p.batch, std::max<long long>(128, rows)) : p.batch;
+}
+size_t sums_bytes(const Problem &p) {
+    return p.dtype == KS_BF16 ? (size_t)(product_rows(p) * p.out_features() * 4) : 0;
+}
+ks_status product_and_expand(Adapters q, const Problem &p, char *sums, const void *W, bool with_a, const float *H,
+                             int ldh) {
+    const int F = (int)p.out_features(), es = p.elem_bytes();
+    const long long step = product_rows(p);
+    for (long long n0 = 0; n0 < p.batch; n0 += step) {
+        Problem part = p;
+        part.X = static_cast<const char *>(p.X) + n0 * p.in_features() * es;
+        part.batch = std::min<long long>(step, p.batch - n0);
+        void *const Y = static_cast<char *>(p.Y) + n0 * F * es;
+        part.Y = q.bf16 ? sums : Y;
+        part.y_f32 = q.bf16;
+        part.bias = nullptr, part.act = KS_ACT_NONE;
+        const ks_status s = product(part);
+        if (s != KS_OK) return s;
+        const auto *P = static_cast<const float *>(part.Y);
+        const cudaError_t e =
+            q.bf16 ? expand<__nv_bfloat16>(q, Y, P, W, with_a, part.batch, F, H + n0 * ldh, ldh, p.bias, p.act)
+                   : expand<float>(q, Y, P, W, with_a, part.batch, F, H + n0 * ldh, ldh, p.bias, p.act);
+        if (e != cudaSuccess) return cuda_fail(e, "adapter launch");
+        if (q.ids) q.ids += step;
+    }
+    return KS_OK;
 }
 
 // How the gradients (dA, dB; out null: not wanted) are cut: feature blocks of each,
@@ -1410,9 +1450,8 @@ struct Layout {
 };
 
 // Whether the tensor-core kernel can take the product with adapters beside it:
-// bf16, a pattern that AUTO gives to it, and A's vectors aligned (null: a
-// workspace's).  The product's V may be null: a workspace's.
-bool fuses(const Adapters &q, Problem p, const void *A, int F) {
+// bf16, and a pattern that AUTO gives to it.  The product's V may be null: a workspace's.
+bool fuses(const Adapters &q, Problem p, int F) {
     if (!q.bf16) return false;
     static const char dummy[16] __attribute__((aligned(256))) = {};
     if (!p.V) p.V = dummy;
@@ -1422,10 +1461,10 @@ bool fuses(const Adapters &q, Problem p, const void *A, int F) {
     const TcAdapters tc{dummy, dummy, nullptr, q.S, ldh, 0};
     p.ad = &tc;
     return make_plan(p, KS_VARIANT_AUTO, &plan, &why) && plan.variant == KS_VARIANT_TC &&
-           tc_adapters_supported(p, tc) && shrink_vec(q, p.X, A, F);
+           tc_adapters_supported(p, tc) && shrink_vec(q, p.X, nullptr, F);
 }
 
-// The same for the fp32 kernel.
+// The same for the fp32 kernel, with A's vectors aligned (null: a workspace's).
 bool fuses_fp32(const Adapters &q, Problem p, const void *A, int F) {
     static const char dummy[16] __attribute__((aligned(256))) = {};
     if (!p.V) p.V = dummy;
@@ -1511,13 +1550,14 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
         const ShrinkJob job{X, A, H, nullptr, in_f};
         e = shrink(q, &job, 1, false, batch, row_ldh, nullptr, true, in_f);
         if (e == cudaSuccess) e = launch_adapter_rows(p, A, B, scales, ids, q.S, q.R, H, row_ldh);
-    } else if (fuses(q, p, A, in_f)) {
+    } else if (fuses(q, p, in_f)) {
         // the adapters as K steps of the tensor-core product, with its bias and activation
         Layout m;
         const int ldh = round_up(q.R, 8);
         const size_t h = m.add(plane_bytes(batch, q.R)), l = m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4);
         const bool packed = q.R != ldh || !aligned(B, 16);
         const size_t b_at = packed ? m.add((size_t)q.S * out_f * ldh * 2) : 0;
+        const size_t a_at = aligned(A, 16) ? 0 : m.add((size_t)o.abytes);  // a copy that H's vectors can read
         const size_t bias_at = bias ? m.add((size_t)out_f * 16) : 0, ones_at = bias ? m.add(4096) : 0;
         if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
         TcAdapters tc{packed ? w + b_at : B, w + h, reinterpret_cast<int *>(w + l), q.S, ldh, list_stride(q.S)};
@@ -1528,7 +1568,12 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
                               reinterpret_cast<uint4 *>(w + ones_at), out_f, (out_f + 255) / 256};
         }
         e = packed ? pack(q, B, w + b_at, out_f, ldh) : cudaSuccess;
-        const ShrinkJob job{X, A, nullptr, reinterpret_cast<unsigned short *>(w + h), in_f};
+        const void *vectors = A;
+        if (!aligned(A, 16)) {
+            vectors = w + a_at;
+            if (e == cudaSuccess) e = cudaMemcpyAsync(w + a_at, A, (size_t)o.abytes, cudaMemcpyDeviceToDevice, q.st);
+        }
+        const ShrinkJob job{X, vectors, nullptr, reinterpret_cast<unsigned short *>(w + h), in_f};
         if (e == cudaSuccess) e = shrink(q, &job, 1, true, batch, ldh, reinterpret_cast<int *>(w + l), false, in_f, pack_b);
         if (e == cudaSuccess) {
             p.act = activation;
@@ -1552,17 +1597,17 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
                                reinterpret_cast<const int *>(w + l), q.R, ldh, q.R, list_stride(q.S)};
         if (e == cudaSuccess) e = launch_fma32_adapters(p, vt, ad);
     } else {
-        // The product, then one pass that adds the adapters, the bias and the
-        // activation.  In bf16 the product is rounded before they are added.
+        // H, then the product and one pass that adds the adapters, the bias and the activation
+        Layout m;
         const int ldh = round_up(q.R, 4);
-        if ((s = alloc(&w, (size_t)batch * ldh * 4, q.st)) != KS_OK) return s;
-        float *H = reinterpret_cast<float *>(w);
-        s = product(p);
-        const ShrinkJob job{X, A, H, nullptr, in_f};
-        e = s == KS_OK ? shrink(q, &job, 1, false, batch, ldh, nullptr, by_rows(q, batch, in_f), in_f) : cudaSuccess;
-        if (s == KS_OK && e == cudaSuccess)
-            e = q.bf16 ? expand<__nv_bfloat16>(q, Y, B, false, batch, out_f, H, ldh, bias, activation)
-                       : expand<float>(q, Y, B, false, batch, out_f, H, ldh, bias, activation);
+        const size_t h = m.add((size_t)batch * ldh * 4), sums = m.add(sums_bytes(p));
+        if ((s = alloc(&w, m.bytes, q.st)) != KS_OK) return s;
+        const ShrinkJob job{X, A, w + h, nullptr, in_f};
+        e = shrink(q, &job, 1, false, batch, ldh, nullptr, by_rows(q, batch, in_f), in_f);
+        p.bias = bias;
+        p.act = activation;
+        if (e == cudaSuccess)
+            s = product_and_expand(q, p, w + sums, B, false, reinterpret_cast<const float *>(w + h), ldh);
     }
     if (e != cudaSuccess && s == KS_OK) s = cuda_fail(e, "adapter launch");
     e = cudaFreeAsync(w, q.st);
@@ -1619,7 +1664,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     Problem p{dY, nullptr, const_cast<char *>(dummy), a, c, b, d, batch, dtype, q.st};
     // Few rows: the kernel of few rows, G for H and A transposed for B.
     const bool rowable = adapter_rows_supported(p, ldh), rows_x = rowable && dX;
-    const bool fusable = !rowable && fuses(q, p, nullptr, out_f), fused = fusable && dX && aligned(dX, 16);
+    const bool fusable = !rowable && fuses(q, p, out_f), fused = fusable && dX && aligned(dX, 16);
     // fp32: the transposed blocks, transposed for the kernel, are the values as they are
     const bool fusable32 = !rowable && fuses_fp32(q, p, nullptr, out_f);
     const bool fused32 = fusable32 && dX && aligned(dX, 16) && aligned(values, 16);
@@ -1635,6 +1680,7 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
     const size_t p_at = fused ? m.add(plane_bytes(batch, q.R)) : 0;
     const size_t l_at = fused || fused32 ? m.add((size_t)list_tiles(batch) * list_stride(q.S) * 4) : 0;
     const size_t ap = fused || fused32 || rows_x ? m.add((size_t)q.S * in_f * ldh * o.elem) : 0;
+    const size_t sums = dX && !fused && !fused32 && !rows_x ? m.add(sums_bytes(p)) : 0;
     const bool sorted = ids && (dA || dB);
     const size_t perm_at = sorted ? m.add((size_t)batch * 4) : 0, off_at = sorted ? m.add((size_t)(q.S + 1) * 4) : 0;
     const size_t w_at = dA || dB ? m.add(plan.bytes) : 0;
@@ -1670,11 +1716,8 @@ ks_status ks_adapter_backward(const void *dY, const void *X, const void *values,
         p.V = w + vt;
         const TcAdapters tc{w + ap, w + p_at, lists, q.S, ldh, list_stride(q.S)};
         if (fused) p.ad = &tc;
-        s = fused ? run(p, KS_VARIANT_TC) : product(p);
-        const float *G = reinterpret_cast<const float *>(w + g_at);
-        if (!fused && s == KS_OK)
-            e = q.bf16 ? expand<__nv_bfloat16>(q, dX, A, true, batch, in_f, G, ldh, nullptr, KS_ACT_NONE)
-                       : expand<float>(q, dX, A, true, batch, in_f, G, ldh, nullptr, KS_ACT_NONE);
+        s = fused ? run(p, KS_VARIANT_TC)
+                  : product_and_expand(q, p, w + sums, A, true, reinterpret_cast<const float *>(w + g_at), ldh);
     }
     if ((dA || dB) && e == cudaSuccess && s == KS_OK) {
         grad[0].V = w + g_at;

@@ -62,8 +62,8 @@ template <> struct Elem<float> {
         v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
         v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
     }
-    __device__ static uint4 pack(const float (&v)[4]) {
-        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    __device__ static void store(float *p, const float (&v)[4]) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
     }
 };
 template <> struct Elem<__nv_bfloat16> {
@@ -76,14 +76,18 @@ template <> struct Elem<__nv_bfloat16> {
             v[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
         }
     }
-    __device__ static uint4 pack(const float (&v)[8]) {
+    __device__ static void store(__nv_bfloat16 *p, const float (&v)[8]) {
         uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
             w[q] = *reinterpret_cast<uint32_t *>(&h);
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ static void store(float *p, const float (&v)[8]) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
 };
 
@@ -103,7 +107,8 @@ struct Tile {
     static constexpr int SMEM_FLOATS = (2 * STAGE > EPI) ? 2 * STAGE : EPI;
 };
 
-template <typename T, int DL, int WM, int WK, int TN>
+// O: type of Y, T or float.
+template <typename T, typename O, int DL, int WM, int WK, int TN>
 __global__ void __launch_bounds__(kThreads, 1) fma_kernel(const FmaParams p) {
     using TL = Tile<DL, WM, WK, TN>;
     constexpr int E = Elem<T>::E;
@@ -127,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) fma_kernel(const FmaParams p) {
 
     const T *__restrict__ X = static_cast<const T *>(p.X);
     const T *__restrict__ V = static_cast<const T *>(p.V);
-    T *__restrict__ Y = static_cast<T *>(p.Y);
+    O *__restrict__ Y = static_cast<O *>(p.Y);
     const int n_stages = (p.c + kJT - 1) / kJT;
     const int groups_per_i = p.d / DL;
 
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) fma_kernel(const FmaParams p) {
                         for (int e = 0; e < E; ++e) v[e] += ep_bias(static_cast<const T *>(p.bias), col + e);
                     }
                     if (p.act) ep_act_array(v, p.act);
-                    *reinterpret_cast<uint4 *>(Y + row * p.out_f + col) = Elem<T>::pack(v);
+                    Elem<T>::store(Y + row * p.out_f + col, v);
                 }
             }
             __syncthreads();
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) fma_kernel(const FmaParams p) {
     }
 }
 
-template <typename T, int DL, int WM, int WK, int TN>
+template <typename T, typename O, int DL, int WM, int WK, int TN>
 cudaError_t launch_cfg(const Problem &pr) {
     using TL = Tile<DL, WM, WK, TN>;
     FmaParams p;
@@ -316,7 +321,7 @@ cudaError_t launch_cfg(const Problem &pr) {
     p.n_kb = (int)((pr.b + TL::BKL - 1) / TL::BKL);
     p.n_tiles = (long long)p.n_rb * p.n_g * p.n_kb;
     const size_t smem = (size_t)TL::SMEM_FLOATS * sizeof(float);
-    auto kern = fma_kernel<T, DL, WM, WK, TN>;
+    auto kern = fma_kernel<T, O, DL, WM, WK, TN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long grid = std::min<long long>(p.n_tiles, (long long)sm_count());
@@ -324,10 +329,10 @@ cudaError_t launch_cfg(const Problem &pr) {
     return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, typename O = T>
 cudaError_t launch_typed(const Problem &p, const FmaConfig &c) {
 #define KS_FMA_CASE(DL_, WM_, WK_, TN_) \
-    if (c.dl == DL_ && c.wm == WM_ && c.wk == WK_ && c.tn == TN_) return launch_cfg<T, DL_, WM_, WK_, TN_>(p);
+    if (c.dl == DL_ && c.wm == WM_ && c.wk == WK_ && c.tn == TN_) return launch_cfg<T, O, DL_, WM_, WK_, TN_>(p);
     KS_FMA_CASE(8, 1, 1, 16)
     KS_FMA_CASE(8, 1, 1, 12)
     KS_FMA_CASE(8, 1, 1, 8)
@@ -407,7 +412,8 @@ FmaConfig fma_choose(const Problem &p) {
 }
 
 cudaError_t launch_fma(const Problem &p, const FmaConfig &c) {
-    if (p.dtype == KS_BF16) return launch_typed<__nv_bfloat16>(p, c);
+    if (p.dtype == KS_BF16)
+        return p.y_f32 ? launch_typed<__nv_bfloat16, float>(p, c) : launch_typed<__nv_bfloat16>(p, c);
     // fp32 (KS_F32, and KS_TF32 computed in full fp32) runs on the cp.async
     // ring kernel; this register-staged one remains for grids whose tile count
     // does not fit its 32-bit tile index.

@@ -53,6 +53,8 @@ struct Problem {
     // of staging a transposed copy in a pooled workspace).
     bool no_workspace = false;
     const TcAdapters *ad = nullptr;  // adapters of the tensor-core kernel (plan with tc_adapters_supported)
+    // bf16: Y is fp32, the sums as they are, for a caller that adds to them (no tensor-core kernel, no epilogue).
+    bool y_f32 = false;
 
     int64_t in_features() const { return a * c * d; }
     int64_t out_features() const { return a * b * d; }

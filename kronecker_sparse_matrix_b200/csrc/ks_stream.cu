@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "ks_epilogue.cuh"
 #include "ks_internal.h"
@@ -58,6 +59,10 @@ template <> struct Vec16<__nv_bfloat16> {
         for (int q = 0; q < 4; ++q) h[q] = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
         *reinterpret_cast<uint4 *>(p) = t;
     }
+    __device__ static void store(float *p, const float (&v)[8]) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
 };
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -68,9 +73,10 @@ __device__ __forceinline__ void from_f(__nv_bfloat16 &o, float v) { o = __float2
 // One thread per (n, i, l-group of VEC); loops over k in chunks of KB.
 // Requires d % VEC == 0 and 16-byte aligned X, Y (then every row offset is
 // 16-byte aligned too, since a*c*d and a*b*d are multiples of VEC).
-template <typename T, int KB>
+// O, here and below: type of Y, T or float.
+template <typename T, typename O, int KB>
 __global__ void __launch_bounds__(256) stream_vec_kernel(const T *__restrict__ X, const T *__restrict__ V,
-                                                         T *__restrict__ Y, long long total, int a, int b,
+                                                         O *__restrict__ Y, long long total, int a, int b,
                                                          int c, int d, const T *__restrict__ bias, int act) {
     constexpr int VEC = Vec16<T>::N;
     const int dq = d / VEC;
@@ -83,7 +89,7 @@ __global__ void __launch_bounds__(256) stream_vec_kernel(const T *__restrict__ X
         const long long n = ni / a;
         const int l0 = lq * VEC;
         const T *x = X + n * in_f + (long long)i * c * d + l0;
-        T *y = Y + n * out_f + (long long)i * b * d + l0;
+        O *y = Y + n * out_f + (long long)i * b * d + l0;
         // values[i][l0 + e][k][j] = v[(e * b + k) * c + j]
         const T *v = V + ((long long)i * d + l0) * b * c;
         for (int k0 = 0; k0 < b; k0 += KB) {
@@ -123,9 +129,9 @@ __global__ void __launch_bounds__(256) stream_vec_kernel(const T *__restrict__ X
 }
 
 // One thread per output element; any pattern, element-aligned pointers.
-template <typename T>
+template <typename T, typename O>
 __global__ void __launch_bounds__(256) stream_scalar_kernel(const T *__restrict__ X, const T *__restrict__ V,
-                                                            T *__restrict__ Y, long long total, int a, int b,
+                                                            O *__restrict__ Y, long long total, int a, int b,
                                                             int c, int d, const T *__restrict__ bias, int act) {
     const long long in_f = (long long)a * c * d, out_f = (long long)a * b * d;
     const long long bd = (long long)b * d;
@@ -167,9 +173,9 @@ __host__ __device__ constexpr int merged_units(int B, int C, int D, int VEC) {
 // Threads form a TU x TR grid per CTA: TU consecutive units by TR row lanes.
 // EP: fused epilogue (bias and activation) compiled in; the plain
 // instantiation carries none of its code.
-template <typename T, int B, int C, int D, bool EP>
+template <typename T, typename O, int B, int C, int D, bool EP>
 __global__ void __launch_bounds__(256) stream_reg_kernel(const T *__restrict__ X, const T *__restrict__ V,
-                                                         T *__restrict__ Y, long long N, int d, int units,
+                                                         O *__restrict__ Y, long long N, int d, int units,
                                                          int in_f, int out_f, int tu_log2, int rows_per_cta,
                                                          const T *__restrict__ bias, int act) {
     constexpr int VEC = Vec16<T>::N;
@@ -210,7 +216,7 @@ __global__ void __launch_bounds__(256) stream_reg_kernel(const T *__restrict__ X
 #pragma unroll 2
     for (long long n = n_begin; n < n_end; n += TR) {
         const T *x = X + n * in_f + x_off;
-        T *y = Y + n * out_f + y_off;
+        O *y = Y + n * out_f + y_off;
         float xv[NL * C];  // xv[e*C + j]: lane e, input j
         if constexpr (D == 0) {
 #pragma unroll
@@ -284,7 +290,7 @@ int grid_for(long long work, int threads) {
     return (int)std::max<long long>(1, std::min(blocks, cap));
 }
 
-template <typename T, int B, int C, int D>
+template <typename T, typename O, int B, int C, int D>
 cudaError_t launch_reg(const Problem &p) {
     constexpr int VEC = Vec16<T>::N;
     constexpr int U = D == 0 ? 1 : merged_units(B, C, D, VEC);
@@ -298,9 +304,11 @@ cudaError_t launch_reg(const Problem &p) {
     const long long by = std::max<long long>(1, std::min(max_by, (target + bx - 1) / bx));
     const long long rows_per_cta = (p.batch + by - 1) / by;
     if (bx > INT32_MAX || rows_per_cta > INT32_MAX) return cudaErrorInvalidConfiguration;
-    auto kern = (p.bias || p.act) ? stream_reg_kernel<T, B, C, D, true> : stream_reg_kernel<T, B, C, D, false>;
+    auto kern = stream_reg_kernel<T, O, B, C, D, false>;
+    if constexpr (std::is_same_v<T, O>)  // (fp32 sums of a bf16 product take no epilogue)
+        if (p.bias || p.act) kern = stream_reg_kernel<T, O, B, C, D, true>;
     kern<<<dim3((unsigned)bx, (unsigned)by), 256, 0, p.stream>>>(
-        static_cast<const T *>(p.X), static_cast<const T *>(p.V), static_cast<T *>(p.Y), p.batch, (int)p.d,
+        static_cast<const T *>(p.X), static_cast<const T *>(p.V), static_cast<O *>(p.Y), p.batch, (int)p.d,
         (int)units, (int)p.in_features(), (int)p.out_features(), tu_log2, (int)rows_per_cta,
         static_cast<const T *>(p.bias), p.act);
     return cudaGetLastError();
@@ -309,21 +317,21 @@ cudaError_t launch_reg(const Problem &p) {
 // The register-weight kernel for (b, c) in {1, 2, 4}^2, if the layout allows:
 // 16-byte aligned X, values and Y; d % VEC == 0 (l-vector layout), or d < VEC
 // with a merged unit of U blocks dividing a.  cudaErrorNotSupported otherwise.
-template <typename T, int B, int C>
+template <typename T, typename O, int B, int C>
 cudaError_t launch_reg_bc(const Problem &p) {
     constexpr int VEC = Vec16<T>::N;
-    if (p.d % VEC == 0) return launch_reg<T, B, C, 0>(p);
+    if (p.d % VEC == 0) return launch_reg<T, O, B, C, 0>(p);
     switch (p.d) {
         case 1:
-            if (merged_units(B, C, 1, VEC) && p.a % merged_units(B, C, 1, VEC) == 0) return launch_reg<T, B, C, 1>(p);
+            if (merged_units(B, C, 1, VEC) && p.a % merged_units(B, C, 1, VEC) == 0) return launch_reg<T, O, B, C, 1>(p);
             break;
         case 2:
-            if (merged_units(B, C, 2, VEC) && p.a % merged_units(B, C, 2, VEC) == 0) return launch_reg<T, B, C, 2>(p);
+            if (merged_units(B, C, 2, VEC) && p.a % merged_units(B, C, 2, VEC) == 0) return launch_reg<T, O, B, C, 2>(p);
             break;
         case 4:
             if constexpr (VEC == 8) {
                 if (merged_units(B, C, 4, VEC) && p.a % merged_units(B, C, 4, VEC) == 0)
-                    return launch_reg<T, B, C, 4>(p);
+                    return launch_reg<T, O, B, C, 4>(p);
             }
             break;
         default: break;
@@ -331,50 +339,50 @@ cudaError_t launch_reg_bc(const Problem &p) {
     return cudaErrorNotSupported;
 }
 
-template <typename T, int B>
+template <typename T, typename O, int B>
 cudaError_t launch_reg_b(const Problem &p) {
     switch (p.c) {
-        case 1: return launch_reg_bc<T, B, 1>(p);
-        case 2: return launch_reg_bc<T, B, 2>(p);
-        case 4: return launch_reg_bc<T, B, 4>(p);
+        case 1: return launch_reg_bc<T, O, B, 1>(p);
+        case 2: return launch_reg_bc<T, O, B, 2>(p);
+        case 4: return launch_reg_bc<T, O, B, 4>(p);
         default: return cudaErrorNotSupported;
     }
 }
 
-template <typename T>
+template <typename T, typename O>
 cudaError_t launch_reg_any(const Problem &p) {
     const uintptr_t al = reinterpret_cast<uintptr_t>(p.X) | reinterpret_cast<uintptr_t>(p.V) |
                          reinterpret_cast<uintptr_t>(p.Y);
     if (al % 16) return cudaErrorNotSupported;
     switch (p.b) {
-        case 1: return launch_reg_b<T, 1>(p);
-        case 2: return launch_reg_b<T, 2>(p);
-        case 4: return launch_reg_b<T, 4>(p);
+        case 1: return launch_reg_b<T, O, 1>(p);
+        case 2: return launch_reg_b<T, O, 2>(p);
+        case 4: return launch_reg_b<T, O, 4>(p);
         default: return cudaErrorNotSupported;
     }
 }
 
-template <typename T>
+template <typename T, typename O = T>
 cudaError_t launch_typed(const Problem &p) {
     constexpr int VEC = Vec16<T>::N;
     const T *X = static_cast<const T *>(p.X);
     const T *V = static_cast<const T *>(p.V);
-    T *Y = static_cast<T *>(p.Y);
+    O *Y = static_cast<O *>(p.Y);
     const T *B = static_cast<const T *>(p.bias);
-    const cudaError_t er = launch_reg_any<T>(p);
+    const cudaError_t er = launch_reg_any<T, O>(p);
     if (er != cudaErrorNotSupported) return er;
     const bool aligned = (reinterpret_cast<uintptr_t>(p.X) % 16 == 0) && (reinterpret_cast<uintptr_t>(p.Y) % 16 == 0);
     if (aligned && p.d % VEC == 0) {
         const long long total = p.batch * p.a * (p.d / VEC);
         if (p.b <= 2)
-            stream_vec_kernel<T, 2><<<grid_for(total, 256), 256, 0, p.stream>>>(X, V, Y, total, (int)p.a, (int)p.b,
+            stream_vec_kernel<T, O, 2><<<grid_for(total, 256), 256, 0, p.stream>>>(X, V, Y, total, (int)p.a, (int)p.b,
                                                                                (int)p.c, (int)p.d, B, p.act);
         else
-            stream_vec_kernel<T, 4><<<grid_for(total, 256), 256, 0, p.stream>>>(X, V, Y, total, (int)p.a, (int)p.b,
+            stream_vec_kernel<T, O, 4><<<grid_for(total, 256), 256, 0, p.stream>>>(X, V, Y, total, (int)p.a, (int)p.b,
                                                                                (int)p.c, (int)p.d, B, p.act);
     } else {
         const long long total = p.batch * p.out_features();
-        stream_scalar_kernel<T><<<grid_for(total, 256), 256, 0, p.stream>>>(X, V, Y, total, (int)p.a, (int)p.b,
+        stream_scalar_kernel<T, O><<<grid_for(total, 256), 256, 0, p.stream>>>(X, V, Y, total, (int)p.a, (int)p.b,
                                                                             (int)p.c, (int)p.d, B, p.act);
     }
     return cudaGetLastError();
@@ -385,7 +393,8 @@ cudaError_t launch_typed(const Problem &p) {
 bool stream_supported(const Problem &) { return true; }
 
 cudaError_t launch_stream(const Problem &p) {
-    if (p.dtype == KS_BF16) return launch_typed<__nv_bfloat16>(p);
+    if (p.dtype == KS_BF16)
+        return p.y_f32 ? launch_typed<__nv_bfloat16, float>(p) : launch_typed<__nv_bfloat16>(p);
     return launch_typed<float>(p);  // KS_F32, and KS_TF32 computed in full fp32
 }
 

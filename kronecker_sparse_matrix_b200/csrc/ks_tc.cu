@@ -979,6 +979,7 @@ bool tc_supported(const Problem &p, const char **why) {
         *why = "fp32 products keep fp32 arithmetic (CUDA cores); the tensor-core kernel serves KS_TF32 and KS_BF16";
         return false;
     }
+    if (p.y_f32) { *why = "fp32 sums of a bf16 product"; return false; }
     const int es = tc_es(p);
     const int dls = tc_dls(p);
     if (!dls) { *why = "d must be 1, 2, 4 or a multiple of 8"; return false; }
