@@ -1417,7 +1417,7 @@ ks_status check(int64_t a, int64_t b, int64_t c, int64_t d, int64_t batch, int d
     if (rank < 1 || rank > kMaxRank)
         return record_error(KS_ERR_INVALID_ARG, "rank must be in 1..%d (got %lld)", kMaxRank, (long long)rank);
     // rows are indexed with 32 bits (ids and their order), one thread per output in places
-    if (batch > INT32_MAX / 2) return record_error(KS_ERR_INVALID_ARG, "adapters take at most 2^30 rows");
+    if (batch > (int64_t{1} << 30)) return record_error(KS_ERR_INVALID_ARG, "adapters take at most 2^30 rows");
     o->elem = dtype == KS_BF16 ? 2 : 4;
     o->abytes = n_adapters * rank * o->in_f * o->elem;
     o->bbytes = n_adapters * rank * o->out_f * o->elem;

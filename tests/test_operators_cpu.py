@@ -103,3 +103,12 @@ def test_adamw_other_refusals(lib):
 def test_adamw_nothing_to_do(lib):
     assert adamw(lib, []) == 0
     assert adamw(lib, [_lib.KsAdamwTensor(n=0)]) == 0
+
+
+def test_the_largest_batch(lib):
+    """2^30 rows pass the check of the batch (and meet the next one), one more does not."""
+    for call in (matmul, backward):
+        assert call(lib, batch=1 << 30, A=None) == 1
+        assert b"A and B" in lib.ks_last_error()
+        assert call(lib, batch=(1 << 30) + 1, A=None) == 1
+        assert b"2^30 rows" in lib.ks_last_error()
