@@ -371,7 +371,8 @@ typedef struct ks_adamw_options {
  * for each 256 consecutive elements of a tensor (scale = largest magnitude /
  * 448; a block with nothing above 2^-100 is held as zeros; a positive sqrt(v)
  * is never held as zero).  An infinite gradient makes its block's 8-bit states
- * NaN, a NaN one its own element's.  Tensors of zero elements are skipped.  A parameter or
+ * NaN, a finite one whose square leaves fp32's range (above 1.8e19) its block's
+ * sqrt(v), a NaN one its own element's.  Tensors of zero elements are skipped.  A parameter or
  * state that shares bytes with any other buffer of the step is
  * KS_ERR_INVALID_ARG, as are masters for some tensors only, betas outside
  * [0, 1), or a negative or non-finite lr, eps or weight_decay.  Allocates no

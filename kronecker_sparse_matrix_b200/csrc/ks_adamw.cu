@@ -11,7 +11,8 @@
 // 2^-9/448 of the block's largest sqrt(v).  A positive sqrt(v) is never held as
 // zero (the smallest e4m3 number stands for it), so no step divides by eps
 // alone because of the format.  A block whose largest magnitude is below 2^-100
-// is held as zeros (448 / top would leave the fp32 range).
+// is held as zeros (448 / top would leave the fp32 range).  One whose largest magnitude
+// is infinite (in v: also that of a gradient whose square leaves the fp32 range) is held as NaN.
 //
 // The step needs p, g, m and v read and p, m and v written once: 28 bytes per
 // fp32 element with fp32 states, 10.06 bytes per bf16 element with 8-bit ones.
@@ -193,7 +194,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 // 448 / top: the reciprocal to within one rounding by a Newton step, its residual exact
 // by the FMA.  (With the bare approximation more elements fell to the other side of a tie
-// between two codes than rounding alone puts there.)
+// between two codes than rounding alone puts there.)  NaN for an infinite top.  `top` is
+// below 2^126 or infinite: the reciprocal of a larger number is subnormal, which the
+// approximation flushes.
 __device__ __forceinline__ float codes_per(float top) {
     const float r = rcp_approx(top);
     return fmaf(fmaf(-r, top, 1.f), r, r) * kTop;
@@ -300,7 +303,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         store8(p, pe, vec, lane, left);
         if constexpr (S8) {
             const float m_top = warp_top(me), v_top = warp_top(ve);
-            const float m_inv = m_top == 0.f ? 0.f : codes_per(m_top);
+            // (m can be as large as a gradient: 448 / m_top as 28 / (m_top / 16))
+            const float m_inv = m_top == 0.f ? 0.f : codes_per(m_top * (1.f / 16.f)) * (1.f / 16.f);
             const float v_inv = v_top == 0.f ? 0.f : codes_per(v_top);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
             }
             if (lane == 0) {  // (the warp's reductions above come after every lane's reads)
                 scales[0][u] = m_top * (1.f / kTop);
-                scales[1][u] = v_top * (1.f / kTop);
+                scales[1][u] = fmaf(v_inv, 0.f, v_top * (1.f / kTop));  // NaN with v_inv, for codes that fmaxf made kLow
             }
         }
         store8(m, me, vec, lane, left);
