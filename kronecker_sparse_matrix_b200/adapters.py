@@ -45,9 +45,12 @@ def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: t
             _act(act), _DTYPES_TF32 if tf32 else _DTYPES)
     if values is None:
         raise ValueError("values must be a tensor")
+    given = out is not None
     status, out = _on_device(run, args, x, stream)
     if status:
         _lib.check(status)
+    if given:
+        torch.autograd.graph.increment_version(out)  # changed in place behind autograd's back
     return out
 
 

@@ -28,7 +28,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     ceil(numel/256) scales (zeros are valid fresh states of both kinds).
     ``masters``: fp32 masters of bf16 parameters.  step counts from 1.  step (int64), lr and
     grad_scale (float32) may be one-element CUDA tensors, read when the step
-    runs: a captured step follows them.  Asynchronous on ``stream``."""
+    runs: a captured step follows them.  Autograd counts parameters and masters as
+    changed in place.  Asynchronous on ``stream``."""
     if len(params) == 0:
         return
     from ._ks_marshal import adamw_step as run  # built with the library
@@ -43,6 +44,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
             status = run(*args)
     if status:
         _lib.check(status)
+    # changed in place behind autograd's back (the states are nobody's but the optimizer's)
+    torch.autograd.graph.increment_version(params if masters is None else [*params, *masters])
 
 
 class AdamW(torch.optim.Optimizer):
@@ -108,9 +111,8 @@ class AdamW(torch.optim.Optimizer):
                 adamw_step(ps, [p.grad.contiguous() for p in ps], [s["exp_avg"] for s in states],
                            [s["exp_avg_sq"] for s in states], step=done + 1, lr=group["lr"], betas=group["betas"],
                            eps=group["eps"], weight_decay=group["weight_decay"], grad_scale=grad_scale, **more)
-                for p, s in zip(ps, states):
+                for s in states:
                     s["step"] = done + 1
-                    torch.autograd.graph.increment_version(p)  # changed in place behind autograd's back
         return loss
 
     def load_state_dict(self, state_dict) -> None:
