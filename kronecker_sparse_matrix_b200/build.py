@@ -1,21 +1,25 @@
 """Builds the KS CUDA library in-tree: kronecker_sparse_matrix_b200/libks_b200.so,
-and the host-side module that reads tensor lists for it, _ks_marshal.so.
+and, where torch is installed, the host-side module that reads tensors for it,
+_ks_marshal (with the interpreter's suffix).  The library needs neither torch nor Python.
 
 Every kernel is compiled for sm_100a only
 (``-gencode arch=compute_100a,code=sm_100a``) with nvcc; objects go to
 ``_build/`` at the repository root.  Usage: ``python -m
-kronecker_sparse_matrix_b200.build [--force] [--verbose]``.
+kronecker_sparse_matrix_b200.build [--force] [--verbose]``, or this file as a script
+where there is no torch.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,7 +28,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libks_b200.so")
 MARSHAL_SRC = os.path.join(CSRC, "ks_marshal.cpp")
-MARSHAL = os.path.join(PKG, "_ks_marshal.so")
+MARSHAL = os.path.join(PKG, "_ks_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
+MARSHAL_STAMP = os.path.join(BUILD, "_ks_marshal.stamp")  # what the module was built for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -63,24 +68,38 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
     return (r.stdout + r.stderr).strip()
 
 
-def build_marshal(force: bool = False) -> str:
-    """The CPython module that reads tensor lists (host code only)."""
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SRC):
-        return MARSHAL
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+def build_marshal(force: bool = False) -> Optional[str]:
+    """The CPython module that reads tensors (host code only); None without torch, whose
+    headers it needs.  Rebuilt when its source, Python or torch has changed."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    include = os.path.join(os.path.dirname(spec.origin), "include")
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # (a source tree on the path)
+        version = "unknown"
+    stamp = f"python {sys.version}\ntorch {version} {include}\n"
+    if not force and os.path.exists(MARSHAL) and os.path.exists(MARSHAL_STAMP):
+        newest = _newest([p for p in (MARSHAL_SRC, os.path.join(include, "ATen", "dlpack.h")) if os.path.exists(p)])
+        with open(MARSHAL_STAMP) as f:
+            if f.read() == stamp and os.path.getmtime(MARSHAL) >= newest:
+                return MARSHAL
+    os.makedirs(BUILD, exist_ok=True)
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-o", tmp, MARSHAL_SRC,
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch, "include")]
+           "-I", sysconfig.get_paths()["include"], "-I", include]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on ks_marshal.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL)
+    with open(MARSHAL_STAMP, "w") as f:
+        f.write(stamp)
     return MARSHAL
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    build_marshal(force)
     hdr_time = _newest(headers())
     jobs = []
     objs = []
@@ -103,6 +122,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    build_marshal(force)  # after the library, which does not need it
     return LIB
 
 
