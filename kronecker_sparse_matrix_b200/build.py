@@ -81,14 +81,15 @@ def build_marshal(force: bool = False) -> Optional[str]:
         version = "unknown"
     stamp = f"python {sys.version}\ntorch {version} {include}\n"
     if not force and os.path.exists(MARSHAL) and os.path.exists(MARSHAL_STAMP):
-        newest = _newest([p for p in (MARSHAL_SRC, os.path.join(include, "ATen", "dlpack.h")) if os.path.exists(p)])
+        read = (MARSHAL_SRC, os.path.join(INCLUDE, "ks.h"), os.path.join(include, "ATen", "dlpack.h"))
+        newest = _newest([p for p in read if os.path.exists(p)])
         with open(MARSHAL_STAMP) as f:
             if f.read() == stamp and os.path.getmtime(MARSHAL) >= newest:
                 return MARSHAL
     os.makedirs(BUILD, exist_ok=True)
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-o", tmp, MARSHAL_SRC,
-           "-I", sysconfig.get_paths()["include"], "-I", include]
+           "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, "-I", include]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on ks_marshal.cpp:\n{r.stdout}\n{r.stderr}")

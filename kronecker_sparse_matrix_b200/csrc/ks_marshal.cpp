@@ -13,6 +13,8 @@
 #include <cstdint>
 #include <cstring>
 
+#include "ks.h"
+
 namespace {
 
 const DLPackExchangeAPI *g_api = nullptr;
@@ -130,16 +132,22 @@ const char *const kNames[7] = {"params", "grads", "exp_avgs", "exp_avg_sqs", "ma
                                "exp_avg_sq_scales"};
 constexpr int64_t kBlock = 256;  // elements that share a scale in an 8-bit state
 
-// ks_adamw_options
-struct Options {
-    double lr, beta1, beta2, eps, weight_decay;
-    int64_t step;
-    const void *step_ptr, *lr_ptr, *grad_scale;
-};
-using AdamwStep = int (*)(const void *, int64_t, int, int, const Options *, void *);
+// The buffer of list c (kNames) of a tensor.
+void set_buffer(ks_adamw_tensor *t, int c, void *p) {
+    switch (c) {
+        case 0: t->param = p; break;
+        case 1: t->grad = p; break;
+        case 2: t->exp_avg = p; break;
+        case 3: t->exp_avg_sq = p; break;
+        case 4: t->master = static_cast<float *>(p); break;
+        case 5: t->exp_avg_scale = static_cast<float *>(p); break;
+        default: t->exp_avg_sq_scale = static_cast<float *>(p); break;
+    }
+}
 
 // A tensor of one element of the given type (kind kNone: int64) on the device, or false with an error set.
-bool scalar_of(PyObject *o, const char *name, int kind, int device, const void **out) {
+template <typename T>
+bool scalar_of(PyObject *o, const char *name, int kind, int device, const T **out) {
     Info t;
     DLTensor d;
     if (!read(o, &t) || g_api->dltensor_from_py_object_no_sync(o, &d) != 0) return false;
@@ -149,14 +157,14 @@ bool scalar_of(PyObject *o, const char *name, int kind, int device, const void *
                      kind == kNone ? "torch.int64" : kind_name(kind), device);
         return false;
     }
-    *out = reinterpret_cast<const void *>((uintptr_t)t.ptr);
+    *out = reinterpret_cast<const T *>((uintptr_t)t.ptr);
     return true;
 }
 
 // A step's numbers, args: lr, step, grad_scale (each a number or a tensor; grad_scale may be
 // None), beta1, beta2, eps, weight_decay.
-bool options_of(PyObject *const *args, int device, Options *o) {
-    *o = Options{};
+bool options_of(PyObject *const *args, int device, ks_adamw_options *o) {
+    *o = ks_adamw_options{};
     double *const number[4] = {&o->beta1, &o->beta2, &o->eps, &o->weight_decay};
     for (int k = 0; k < 4; ++k) {
         *number[k] = PyFloat_AsDouble(args[3 + k]);
@@ -183,16 +191,16 @@ bool options_of(PyObject *const *args, int device, Options *o) {
 // dtypes and stream: dtype_of, stream_of).  Lists of equal lengths; masters and scales may be None.
 PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     if (nargs != 17) return PyErr_Format(PyExc_TypeError, "adamw_step takes 17 arguments");
-    const auto function = reinterpret_cast<AdamwStep>(PyLong_AsVoidPtr(args[0]));
+    const auto function = reinterpret_cast<decltype(&ks_adamw_step)>(PyLong_AsVoidPtr(args[0]));
     if (!function) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "no function");
     PyObject *const *const options = args + 8;
     ++args;
     PyObject *list[7] = {}, *table = nullptr, *result = nullptr;
-    Options opt;
+    ks_adamw_options opt;
     int ks_dtype = 0, status = 0;
     Py_ssize_t count = 0;
     int dtype = kNone, state = kNone, device = -1;
-    uint64_t *words = nullptr;
+    ks_adamw_tensor *tensors = nullptr;
     unsigned long long stream = 0;
     for (int c = 0; c < 7; ++c) {
         if (args[c] == Py_None && c >= 4) continue;
@@ -205,10 +213,10 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
             goto done;
         }
     }
-    table = PyBytes_FromStringAndSize(nullptr, count * 64);  // ks_adamw_tensor: eight 64-bit words
+    table = PyBytes_FromStringAndSize(nullptr, count * (Py_ssize_t)sizeof(ks_adamw_tensor));
     if (!table) goto done;
-    words = reinterpret_cast<uint64_t *>(PyBytes_AS_STRING(table));
-    memset(words, 0, (size_t)count * 64);
+    tensors = reinterpret_cast<ks_adamw_tensor *>(PyBytes_AS_STRING(table));
+    memset(static_cast<void *>(tensors), 0, (size_t)count * sizeof(ks_adamw_tensor));
     for (int c = 0; c < 7; ++c) {
         if (!list[c]) continue;
         PyObject **items = PySequence_Fast_ITEMS(list[c]);
@@ -244,16 +252,16 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
                 goto done;
             }
             if (c == 0) {
-                words[8 * k + 7] = (uint64_t)t.numel;
+                tensors[k].n = t.numel;
             } else {
-                const int64_t n = (int64_t)words[8 * k + 7];
+                const int64_t n = tensors[k].n;
                 if (t.numel != (c < 5 ? n : (n + kBlock - 1) / kBlock)) {
                     PyErr_Format(PyExc_ValueError,
                                  "%s must have the parameters' element counts (scales: one for each 256)", kNames[c]);
                     goto done;
                 }
             }
-            words[8 * k + c] = t.ptr;
+            set_buffer(&tensors[k], c, address(t));
         }
     }
     if (count == 0) {
@@ -269,7 +277,7 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         !stream_of(options[8], device, &stream))
         goto done;
     Py_BEGIN_ALLOW_THREADS
-    status = function(words, count, ks_dtype, state == kE4M3 ? 8 : 32, &opt, reinterpret_cast<void *>((uintptr_t)stream));
+    status = function(tensors, count, ks_dtype, state == kE4M3 ? 8 : 32, &opt, reinterpret_cast<void *>((uintptr_t)stream));
     Py_END_ALLOW_THREADS
     result = PyLong_FromLong(status);
 done:
@@ -324,12 +332,9 @@ bool check_adapters(PyObject *const *args, long long width, long long in_f, long
 // Checks the tensors, makes out (None: a new tensor) and calls ks_adapter_matmul
 // (function: its address; dtypes and stream: dtype_of, stream_of).  Through ctypes the
 // call alone takes 2 us more.
-using AdapterMatmul = int (*)(const void *, const void *, int64_t, int64_t, int64_t, int64_t, int64_t, void *, int,
-                              const void *, int, const void *, const void *, const float *, const int32_t *, int64_t,
-                              int64_t, void *);
 PyObject *adapter_matmul(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     if (nargs != 16) return PyErr_Format(PyExc_TypeError, "adapter_matmul takes 16 arguments");
-    const auto function = reinterpret_cast<AdapterMatmul>(PyLong_AsVoidPtr(args[0]));
+    const auto function = reinterpret_cast<decltype(&ks_adapter_matmul)>(PyLong_AsVoidPtr(args[0]));
     if (!function) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "no function");
     long long n[5];  // a, b, c, d, activation
     Sizes z;
@@ -367,12 +372,9 @@ PyObject *adapter_matmul(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
 // adapter_backward(function, dy, values, A, B, ids, scales, x, a, b, c, d, need_dx, need_da, need_db, dtypes, stream)
 //   -> (status, dx, da, db)
 // The same for ks_adapter_backward; gradients that are not needed are None.
-using AdapterBackward = int (*)(const void *, const void *, const void *, int64_t, int64_t, int64_t, int64_t, int64_t,
-                                int, const void *, const void *, const float *, const int32_t *, int64_t, int64_t,
-                                void *, void *, void *, void *);
 PyObject *adapter_backward(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     if (nargs != 17) return PyErr_Format(PyExc_TypeError, "adapter_backward takes 17 arguments");
-    const auto function = reinterpret_cast<AdapterBackward>(PyLong_AsVoidPtr(args[0]));
+    const auto function = reinterpret_cast<decltype(&ks_adapter_backward)>(PyLong_AsVoidPtr(args[0]));
     if (!function) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "no function");
     long long n[4];
     Sizes z;
