@@ -143,36 +143,30 @@ __device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t *bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Calls stage(adapter, entry, its rows' words, group, first rank) for each stage of
-// the adapters among a tile's rows (n0 .. n0 + BM), in the order that the copying
-// and the computing warps share.
+// Calls stage(adapter, its rows' words, first rank) for each stage of the adapters
+// among a tile's rows (n0 .. n0 + BM, of one 128-row group), in the order that the
+// copying and the computing warps share.
 template <int BM, typename F>
-__device__ __forceinline__ void for_adapter_stages(const Fma32Adapters &ad, long long n0, long long N, bool &ok,
-                                                   F &&stage) {
-    constexpr int kGroups = BM < 128 ? 1 : BM / 128;
-    for (int li = 0; li < kGroups && ok; ++li) {
-        const long long group = n0 / 128 + li;
-        if (group * 128 >= N) break;
-        const int *list = ad.lists + group * ad.list_stride;
-        const int count = __ldg(list);
-        for (int q = 0; q < count && ok; ++q) {
-            const int *entry = list + 8 + 8 * q;
-            if (BM < 128) {  // only the words of the tile's rows
-                unsigned off = 0xFFFFFFFFu;
-                for (int w = 0; w < (BM + 31) / 32; ++w) off &= (unsigned)__ldg(entry + 4 + (int)(n0 % 128) / 32 + w);
-                if (off == 0xFFFFFFFFu) continue;
-            }
-            const int s = __ldg(entry);
-            for (int r0 = 0; r0 < ad.R && ok; r0 += kJT) stage(s, q, entry + 4, li, r0);
+__device__ __forceinline__ void for_adapter_stages(const Fma32Adapters &ad, long long n0, bool &ok, F &&stage) {
+    static_assert(128 % BM == 0, "a tile's rows have one list");
+    const int *list = ad.lists + n0 / 128 * ad.list_stride;
+    const int count = __ldg(list);
+    for (int q = 0; q < count && ok; ++q) {
+        const int *entry = list + 8 + 8 * q;
+        if (BM < 128) {  // only the words of the tile's rows
+            unsigned off = 0xFFFFFFFFu;
+            for (int w = 0; w < (BM + 31) / 32; ++w) off &= (unsigned)__ldg(entry + 4 + (int)(n0 % 128) / 32 + w);
+            if (off == 0xFFFFFFFFu) continue;
         }
+        const int s = __ldg(entry);
+        for (int r0 = 0; r0 < ad.R && ok; r0 += kJT) stage(s, entry + 4, r0);
     }
 }
 
 // Low-rank adapters beside the product (Fma32Adapters): Y[n] += H[n] W[s]^T for the
 // rows n of adapter s, as further stages of a tile, eight ranks each: the rows' H
 // (compact, the same for every l) in place of X, W[s] of the tile's outputs in place
-// of the values.  A stage is one adapter's, for the rows of one 128-row group that
-// take it; in a warp that holds other rows too the products of those are left out
+// of the values.  A stage is one adapter's, for the rows of the tile that take it; in a warp that holds other rows too the products of those are left out
 // row by row, so that nothing an adapter holds (infinities, NaN) reaches them.
 template <bool AD>
 struct Fma32Ad {};
@@ -320,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p,
                 cp_async_mbar_arrive_noinc(&full_bar[buf]);  // fires when this lane's copies have landed
             }
             if constexpr (AD) {
-                for_adapter_stages<BM>(ad, n0, p.N, ok, [&](int s, int, const int *, int li, int r0) {
+                for_adapter_stages<BM>(ad, n0, ok, [&](int s, const int *, int r0) {
                     const int buf = (int)(fill % kNS);
                     ok = sm100::mbar_wait(&empty_bar[buf], ((fill / kNS) & 1) ^ 1, abort_flag, p.status);
                     if (!ok) return;
@@ -329,10 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p,
 #pragma unroll 1
                     for (int v = 0; v < kT / (kThreads - 256); ++v) {
                         const int vt = pt + 128 * v;
-                        // H: two 16-byte units of each of the group's rows
-                        constexpr int GR = BM < 128 ? BM : 128;
-                        if (vt < 2 * GR) {
-                            const int row = li * 128 + (vt >> 1), r = r0 + 4 * (vt & 1);
+                        // H: two 16-byte units of each row
+                        if (vt < 2 * BM) {
+                            const int row = vt >> 1, r = r0 + 4 * (vt & 1);
                             const bool in = n0 + row < p.N && r < ad.ldh;
                             cp_async16(st + (uint32_t)(row * TL::RA + 4 * (vt & 1)) * 4u,
                                        in ? ad.H + (n0 + row) * ad.ldh + r : p.X, in);
@@ -412,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p,
         if constexpr (AD) {
             const long long n0 = (long long)(tile / p.n_kb / p.n_g) * BM;
             if (ok)
-                for_adapter_stages<BM>(ad, n0, p.N, ok, [&](int, int, const int *off, int li, int) {
+                for_adapter_stages<BM>(ad, n0, ok, [&](int, const int *off, int) {
                     const int buf = (int)(fill % kNS);
                     ok = __all_sync(0xffffffffu, sm100::mbar_wait(&full_bar[buf], (fill / kNS) & 1, abort_flag, p.status));
                     if (!ok) return;
@@ -424,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) fma32_kernel(const Fma32Params p,
                     unsigned take = 0;
 #pragma unroll
                     for (int m = 0; m < 8; ++m) {
-                        const int at = (int)(n0 & 127) * (BM < 128) + a_row + LN::RG * m - 128 * li;  // row of the group
-                        if (at >= 0 && at < 128 && !(__ldg(off + (at >> 5)) >> (at & 31) & 1)) take |= 1u << m;
+                        const int at = (int)(n0 & 127) + a_row + LN::RG * m;  // row of the group
+                        if (!(__ldg(off + (at >> 5)) >> (at & 31) & 1)) take |= 1u << m;
                     }
                     const bool all = __all_sync(0xffffffffu, take == 0xFFu);
                     const auto products = [&](auto every) {
