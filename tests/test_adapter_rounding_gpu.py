@@ -97,3 +97,45 @@ def test_alignment_of_a_alone_changes_nothing():
     q = make(p, 600, 3, 16, torch.bfloat16, "segments", 17, bias=True)
     odd = make(p, 600, 3, 16, torch.bfloat16, "segments", 17, bias=True, shift=1)
     assert torch.equal(call(dict(q, A=odd["A"]), p, act="gelu_tanh"), call(q, p, act="gelu_tanh"))
+
+
+@pytest.mark.parametrize("p", [(1, 256, 64, 16), (1, 64, 48, 8), (2, 96, 64, 1), (3, 20, 12, 5), (8, 2, 2, 16)])
+def test_one_rounding_of_few_rows(p):
+    """The kernel of few rows holds H in fp32 too."""
+    for n, r, shift in ((1, 16, 0), (9, 5, 0), (64, 16, 1)):
+        q = make(p, n, 3, r, torch.bfloat16, "rows", n, bias=True, shift=shift)
+        assert_forward_once(call(q, p, act="relu"), q, p, "relu")
+        assert_dx_once(dx_of(q, p), q, p)
+
+
+@pytest.mark.parametrize("p", [(1, 256, 64, 16), (1, 64, 48, 8), (2, 96, 64, 1), (2, 64, 32, 2), (2, 32, 48, 4)])
+def test_tensor_core_products_round_h_and_the_result_alone(p):
+    a, b, c, d = p
+    for n, r in ((600, 16), (1031, 20)):
+        q = make(p, n, 4, r, torch.bfloat16, "segments", n, bias=True)
+        ref, z, _, base_abs, low_abs = forward64(q, p)
+        tol = (c + 4) * U * base_abs + ((a * c * d + r + 8) * U + BF) * low_abs + 8 * U * z.abs() + 4 * U * q["bias"].to(F64).abs()
+        assert_rounded_once(call(q, p), ref, tol)
+
+
+def test_unaligned_calls_in_replayed_graphs():
+    """A copy of A, and fp32 sums of a product, in workspaces of each graph's own."""
+    runs = []
+    for p, names in (((1, 64, 48, 8), ("A",)), ((1, 96, 24, 8), ()), ((5, 21, 23, 4), ("x",))):
+        q, odd = (make(p, 700, 3, 16, torch.bfloat16, "segments", 5, bias=True, shift=s) for s in (0, 1))
+        q.update({name: odd[name] for name in names})
+        want = call(q, p), dx_of(q, p)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = ks.adapter_matmul(q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"], bias=q["bias"])
+            dx, _, _ = ks.adapter_backward(q["dy"], q["x"], q["values"], p, q["A"], q["B"], q["ids"], q["scales"])
+        runs.append((g, torch.cuda.Stream(), (y, dx), want, q))  # (a replay reads q again)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, st, *_ in runs:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    ks.sync_status()
+    for _, _, got, want, _ in runs:
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
