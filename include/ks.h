@@ -310,8 +310,11 @@ ks_status ks_butterfly_factorize(const void *A, int log2n, void *const *factors,
  * X, values, bias, activation and dtype are as for ks_matmul_ep (KS_TF32: the
  * KS product uses TF32 as there, the adapters' products are fp32).  Y must not
  * overlap any input.  1 <= n_adapters <= 4096, 1 <= rank <= 1024, batch <=
- * 2^30.  H = scales[s] * X A[s]^T lives in a stream-ordered workspace from the
- * library's pool (KS_ERR_ALLOC if it cannot be had). */
+ * 2^30.  Sums are fp32, and a bf16 Y is rounded once; where H = scales[s] * X A[s]^T
+ * is an operand of the tensor cores (bf16 patterns of their kernel, but for few rows) it is
+ * rounded to bf16 too.  H, and what else a call has to lay out (in bf16 the sums of products without
+ * tensor cores, 256 MB at most but for rows of more than 2^19 outputs), lives in a stream-ordered workspace from
+ * the library's pool (KS_ERR_ALLOC if it cannot be had). */
 ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_t b, int64_t c, int64_t d,
                             int64_t batch, void *Y, int dtype, const void *bias, int activation, const void *A,
                             const void *B, const float *scales, const int32_t *ids, int64_t n_adapters,
@@ -328,8 +331,8 @@ ks_status ks_adapter_matmul(const void *X, const void *values, int64_t a, int64_
  * they have beside it.  The gradients of the values
  * and of the bias are ks_matmul_dv's and ks_bias_grad's.  Sums are fp32 in an
  * order that depends on the sizes, the ids and the alignment of the buffers alone, so
- * the results are deterministic; bf16 gradients are rounded once.  No output may overlap an
- * input or another output.  batch == 0 writes zeros to dA and dB.  Limits, ids
+ * the results are deterministic; bf16 gradients are rounded once, and so are G and H where
+ * they are operands of the tensor cores.  No output may overlap an input or another output.  batch == 0 writes zeros to dA and dB.  Limits, ids
  * and workspace are as for ks_adapter_matmul. */
 ks_status ks_adapter_backward(const void *dY, const void *X, const void *values, int64_t a, int64_t b, int64_t c,
                               int64_t d, int64_t batch, int dtype, const void *A, const void *B,

@@ -38,7 +38,8 @@ def adapter_matmul(x: torch.Tensor, values: torch.Tensor, pattern: Pattern, A: t
     per row (a negative id: no adapter; None: every row takes adapter 0);
     scales: float32, one per adapter (None: ones).  An id that is too large
     takes no adapter, and the next ``sync_status`` raises.  Rows of one adapter
-    next to each other run fastest.  Asynchronous on ``stream``."""
+    next to each other run fastest.  Sums are fp32, a bf16 Y is rounded once (and
+    X A[s]^T where it is a tensor-core operand).  Asynchronous on ``stream``."""
     from ._ks_marshal import adapter_matmul as run  # built with the library
     a, b, c, d = pattern
     args = (_lib.address("ks_adapter_matmul"), x, values, A, B, ids, scales, bias, out, int(a), int(b), int(c), int(d),
@@ -61,7 +62,9 @@ def adapter_backward(dy: torch.Tensor, x: Optional[torch.Tensor], values: Option
     """Gradients (dX, dA, dB) of ``adapter_matmul`` without an activation from
     dY (batch, a*b*d); None in the place of one that is not needed (values may
     be None without dX, x without dA and dB).  An adapter without rows gets
-    zeros.  Deterministic; fp32 sums, bf16 gradients rounded once."""
+    zeros.  Deterministic; fp32 sums, bf16 gradients rounded once (and dY B[s] and
+    X A[s]^T where they are tensor-core operands).  A gradient asked for alone has
+    the bits it has beside the others."""
     from ._ks_marshal import adapter_backward as run  # built with the library
     a, b, c, d = pattern
     args = (_lib.address("ks_adapter_backward"), dy, values, A, B, ids, scales, x, int(a), int(b), int(c), int(d),

@@ -8,8 +8,8 @@
 // the h that it needs by itself (A[s] is read again by each block of a row, from
 // L2) instead of waiting for another launch, and a values row is read by
 // neighbouring lanes as 16-byte vectors for all rows of the block.  fp32 sums, one
-// rounding.  GPT-2-shaped bf16 layer, rank 16: 5.6 us for one row, 14 us for 32 rows of
-// 32 adapters, against 28 and 81 us of the tile kernels.
+// rounding.  GPT-2-shaped bf16 layer, rank 16, bias and GELU: 6.1 us for one row, 14 us for 32 rows
+// of 32 adapters, against 28 and 81 us of the tile kernels.
 //
 // h can also come from memory (shrink_rows_kernel, one warp for four ranks of a
 // row): where A[s] is large, reading it in every block costs more than a launch.

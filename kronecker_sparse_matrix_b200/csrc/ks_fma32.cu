@@ -691,8 +691,8 @@ cudaError_t launch_fma32(const Problem &p, const FmaConfig &c_in) {
 
 // Adapters beside a product that the transposed copy of the values pays for (as in
 // launch_fma32, 8 l a tile); the caller has the values transposed per block in vt,
-// 16-byte aligned.  ViT, 25216 rows, four adapters of rank 8: 122 us where the product
-// alone takes 99 and a second pass over Y took 60 and more.
+// 16-byte aligned.  ViT, 25216 rows, four adapters of rank 8: 123 us where the product
+// alone takes 102 and a second pass over Y took 60 and more (147 with bias and erf GELU).
 bool fma32_adapters_supported(const Problem &p) {
     if (p.dtype != KS_F32 || p.b % 4 || 2.0 * (double)p.batch * (double)(p.a * p.b * p.c * p.d) < 1073741824.0)
         return false;
